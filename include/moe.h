@@ -71,7 +71,9 @@ typedef enum {
 } moe_status;
 
 typedef enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 } moe_score_fn;
-typedef enum { MOE_BF16 = 0, MOE_F32 = 1 } moe_dtype;
+/* MOE_F16 is served by the norm, feed-forward block and 8-bit entry points
+ * only; moe_config takes MOE_BF16 or MOE_F32. */
+typedef enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_F16 = 2 } moe_dtype;
 /* How the k expert outputs of a token are summed ("Tutorial 11", section 3,
  * Step 3: unsort, then the gate-weighted sum over the k experts).
  *   MOE_COMBINE_ADD: each expert row is added into an fp32 accumulator by
@@ -390,6 +392,59 @@ moe_status moe_forward_q4(const moe_config *cfg, const moe_route_opts *opts, con
                           const float *s_down, const void *sh_gate, const void *sh_up,
                           const void *sh_down, const void *w_shared_gate, void *y, void *ws,
                           size_t ws_bytes, void *stream);
+
+/* ---- layer norm and RMS norm of token rows, forward and backward: the norm in
+ * front of the layer ("Tutorial 11", section 4: the decoder block normalises,
+ * runs the MoE layer and adds the residual), with the residual addition and
+ * the gradients of the weight and the bias.
+ *
+ *   h    = x + residual, rounded to dtype (h = x without a residual)
+ *   mean = avg_i h_i (MOE_NORM_LAYER), 0 (MOE_NORM_RMS)
+ *   rstd = 1 / sqrt(avg_i (h_i - mean)^2 + eps)
+ *   y_i  = (h_i - mean) rstd weight_i + bias_i
+ */
+#define MOE_NORM_MAX_WIDTH 16384
+typedef enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 } moe_norm_kind;
+typedef struct {
+    int64_t T;       /* rows; 0 is allowed */
+    int32_t d;       /* width: any from 1 to MOE_NORM_MAX_WIDTH (beyond: MOE_ERR_UNSUPPORTED) */
+    int32_t kind;    /* moe_norm_kind */
+    int32_t dtype;   /* moe_dtype of x, residual, h, y and their gradients: all three */
+    int32_t w_dtype; /* moe_dtype of weight and bias: dtype or MOE_F32 */
+    float eps;       /* finite, >= 0 */
+} moe_norm_config;
+
+/* Forward pass.
+ *   x [T, d]; residual [T, d] or NULL; weight [d]; bias [d] or NULL;
+ *   h [T, d] out with a residual (else NULL; one without the other is
+ *     MOE_ERR_INVALID_ARG); y [T, d] out;
+ *   mean, rstd [T] fp32 out, each optional: what moe_norm_backward takes.
+ * h may be x or residual, and y may be x or residual, but not both the same
+ * tensor.  Statistics are fp32, the variance summed about the mean. */
+moe_status moe_norm_forward(const moe_norm_config *cfg, const void *x, const void *residual,
+                            const void *weight, const void *bias, void *h, void *y, float *mean,
+                            float *rstd, void *stream);
+
+/* Bytes of scratch that moe_norm_backward needs for the gradients of weight
+ * and bias (host only). */
+moe_status moe_norm_workspace_size(const moe_norm_config *cfg, size_t *bytes);
+
+/* Backward pass, given dy = dL/dy:
+ *   h [T, d] the rows that were normalised (the forward's h, or x); mean [T]
+ *     (MOE_NORM_LAYER; NULL for MOE_NORM_RMS) and rstd [T] from the forward;
+ *   dh [T, d] or NULL: the gradient that reaches h by other paths (the
+ *     residual stream), added to dx;
+ *   dx [T, d] out: the gradient of h (and so of x and of residual); may be dy
+ *     or dh;
+ *   dweight, dbias [d] fp32 out, each optional (NULL: not computed);
+ *   ws, ws_bytes: at least moe_norm_workspace_size(cfg) bytes, 256-byte
+ *     aligned (not needed when dweight and dbias are NULL).
+ * Sums over the rows are fp32 in a fixed order: repeated calls give identical
+ * bits.  T = 0 writes zeros into dweight and dbias. */
+moe_status moe_norm_backward(const moe_norm_config *cfg, const void *h, const void *weight,
+                             const float *mean, const float *rstd, const void *dy, const void *dh,
+                             void *dx, float *dweight, float *dbias, void *ws, size_t ws_bytes,
+                             void *stream);
 
 /* Largest T*k that moe_forward serves with the CUDA-core small-batch kernels
  * (one warp per weight row, weights streamed once); larger batches use the

@@ -26,7 +26,8 @@ EXPORTED = ["moe_status_string", "moe_validate", "moe_workspace_size", "moe_work
             "moe_selftest_wait_timeout",
             "moe_route_workspace_size", "moe_update_bias", "moe_balance_loss", "moe_train_workspace_size",
             "moe_forward_train", "moe_backward", "moe_quantize_q4", "moe_forward_q4",
-            "moe_forward_host_workspace_size", "moe_forward_host"]
+            "moe_forward_host_workspace_size", "moe_forward_host",
+            "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward"]
 STAGES = ["route", "permute", "gate_up", "shared_gate_up", "down", "shared_down", "finalize"]
 
 
@@ -45,6 +46,11 @@ class MoEConfig(ctypes.Structure):
 class RouteOpts(ctypes.Structure):
     """moe_route_opts: balance bias (selection only) and the score-mean output."""
     _fields_ = [("balance_bias", ctypes.c_void_p), ("score_mean", ctypes.c_void_p)]
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("kind", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
 class WorkspaceViews(ctypes.Structure):
@@ -66,6 +72,7 @@ def lib() -> ctypes.CDLL:
         L = ctypes.CDLL(LIB_PATH)
         P, S = ctypes.c_void_p, ctypes.c_size_t
         C = ctypes.POINTER(MoEConfig)
+        N = ctypes.POINTER(NormConfig)
         sig = {
             "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "moe_validate": ([C], ctypes.c_int),
@@ -89,6 +96,9 @@ def lib() -> ctypes.CDLL:
             "moe_quantize_q4": ([P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, P, P, P], ctypes.c_int),
             "moe_forward_q4": ([C, ctypes.POINTER(RouteOpts)] + [P] * 13 + [P, S, P], ctypes.c_int),
             "moe_balance_loss": ([C, P, P, ctypes.c_float, P, P, P], ctypes.c_int),
+            "moe_norm_workspace_size": ([N, ctypes.POINTER(S)], ctypes.c_int),
+            "moe_norm_forward": ([N] + [P] * 9, ctypes.c_int),
+            "moe_norm_backward": ([N] + [P] * 10 + [S, P], ctypes.c_int),
             "moe_decode_max_rows": ([], ctypes.c_int32),
             "moe_device_status": ([P], ctypes.c_int),
             "moe_profile_nvtx": ([ctypes.c_int32], ctypes.c_int),
@@ -577,3 +587,69 @@ def profile_nvtx(on: bool = True) -> None:
     """moe_profile_nvtx: NVTX ranges around each forward stage on this thread."""
     _check(lib().moe_profile_nvtx(int(bool(on))), "moe_profile_nvtx")
 
+
+
+# ----------------------------------------------------------------------------- norms
+
+DTYPES = {"bf16": 0, "f32": 1, "f16": 2}
+_TORCH_DTYPES = {0: torch.bfloat16, 1: torch.float32, 2: torch.float16}
+NORM_KINDS = {"layer": 0, "rms": 1}
+
+
+def _choice(table: dict, value, name: str) -> int:
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def norm_config(T, d, kind="layer", eps=1e-5, dtype="bf16", w_dtype=None) -> NormConfig:
+    """moe_norm_config.  kind: "layer" or "rms"; dtype ("bf16", "f16", "f32") of the rows;
+    w_dtype of weight and bias: dtype (the default) or "f32"."""
+    return NormConfig(int(T), int(d), _choice(NORM_KINDS, kind, "kind"), _choice(DTYPES, dtype, "dtype"),
+                      _choice(DTYPES, dtype if w_dtype is None else w_dtype, "w_dtype"), float(eps))
+
+
+def norm_workspace_size(cfg: NormConfig) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_norm_workspace_size(ctypes.byref(cfg), ctypes.byref(n)), "moe_norm_workspace_size")
+    return n.value
+
+
+def norm_forward(cfg: NormConfig, x, weight, bias=None, residual=None, y=None, h=None, want_stats=False, stream=None):
+    """moe_norm_forward: (y[T,d], h[T,d] | None, mean[T] | None, rstd[T] | None).  h = x + residual with a
+    residual (allocated unless given); mean (layer norm) and rstd with want_stats."""
+    dt, wt = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype]
+    rows, dev = (cfg.T, cfg.d), x.device
+    if y is None:
+        y = torch.empty(rows, dtype=dt, device=dev)
+    if h is None and residual is not None:
+        h = torch.empty(rows, dtype=dt, device=dev)
+    mean = torch.empty(cfg.T, dtype=torch.float32, device=dev) if want_stats and cfg.kind == 0 else None
+    rstd = torch.empty(cfg.T, dtype=torch.float32, device=dev) if want_stats else None
+    _check(lib().moe_norm_forward(ctypes.byref(cfg), _ptr(x, "x", rows, dt), _ptr(residual, "residual", rows, dt),
+                                  _ptr(weight, "weight", (cfg.d,), wt), _ptr(bias, "bias", (cfg.d,), wt),
+                                  _ptr(h, "h", rows, dt), _ptr(y, "y", rows, dt), _ptr(mean, "mean"),
+                                  _ptr(rstd, "rstd"), _stream(stream)), "moe_norm_forward")
+    return y, h, mean, rstd
+
+
+def norm_backward(cfg: NormConfig, h, weight, mean, rstd, dy, dh=None, dx=None, want_weight=True, want_bias=False,
+                  ws=None, stream=None):
+    """moe_norm_backward: (dx[T,d], dweight[d] float32 | None, dbias[d] float32 | None).  h: the rows that were
+    normalised; mean (None for an RMS norm) and rstd from norm_forward; dh: the gradient that reaches h by other
+    paths, added to dx."""
+    dt, wt = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype]
+    rows, dev = (cfg.T, cfg.d), h.device
+    if dx is None:
+        dx = torch.empty(rows, dtype=dt, device=dev)
+    dweight = torch.empty(cfg.d, dtype=torch.float32, device=dev) if want_weight else None
+    dbias = torch.empty(cfg.d, dtype=torch.float32, device=dev) if want_bias else None
+    if ws is None and (want_weight or want_bias):
+        ws = torch.empty(max(norm_workspace_size(cfg), 1), dtype=torch.uint8, device=dev)
+    _check(lib().moe_norm_backward(ctypes.byref(cfg), _ptr(h, "h", rows, dt), _ptr(weight, "weight", (cfg.d,), wt),
+                                   _ptr(mean, "mean", (cfg.T,), torch.float32),
+                                   _ptr(rstd, "rstd", (cfg.T,), torch.float32), _ptr(dy, "dy", rows, dt),
+                                   _ptr(dh, "dh", rows, dt), _ptr(dx, "dx", rows, dt), _ptr(dweight, "dweight"),
+                                   _ptr(dbias, "dbias"), _ptr(ws, "ws", dtype=torch.uint8),
+                                   0 if ws is None else ws.numel(), _stream(stream)), "moe_norm_backward")
+    return dx, dweight, dbias

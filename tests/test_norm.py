@@ -1,0 +1,344 @@
+"""Layer norm and RMS norm, forward and backward, against their formulas in 64 bits.
+
+Tolerances.  An output element is one rounding of a 32-bit result: half a step of its type, eps / 2
+relative to the value, plus the 32-bit error of the computation before it.  That error is a sum over
+at most d (or T) terms of one rounding each, in blocks of a tree, and cancellations in h - mean lose
+at most the rounding of the mean; it is bounded here by 64 roundings of 2^-24 relative to the largest
+magnitude in the row (the column for the weight's gradient, whose sums run over T rows: 64 roundings
+of the sum of the terms' magnitudes).
+"""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from sparse_mixture_experts_sigmoid_b200 import binding as B
+
+TORCH = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+F32 = 64 * 2.0 ** -24
+
+
+def half_step(name):
+    return 0.0 if name == "f32" else torch.finfo(TORCH[name]).eps / 2
+
+
+# ------------------------------------------------------------------ host checks (no GPU)
+
+FAKE = ctypes.c_void_p(0x10000)
+
+
+def _fwd(cfg, x=FAKE, residual=None, weight=FAKE, bias=None, h=None, y=FAKE, mean=None, rstd=None):
+    return B.lib().moe_norm_forward(ctypes.byref(cfg), x, residual, weight, bias, h, y, mean, rstd, None)
+
+
+def _bwd(cfg, h=FAKE, weight=FAKE, mean=FAKE, rstd=FAKE, dy=FAKE, dx=FAKE, dw=FAKE, db=None, ws=FAKE, n=1 << 40):
+    return B.lib().moe_norm_backward(ctypes.byref(cfg), h, weight, mean, rstd, dy, None, dx, dw, db, ws, n, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), 1), (dict(d=0), 1), (dict(kind=2), 1), (dict(kind=-1), 1), (dict(dtype=3), 1), (dict(dtype=-1), 1),
+    (dict(dtype=0, w_dtype=2), 1), (dict(dtype=1, w_dtype=0), 1), (dict(eps=-1e-6), 1), (dict(eps=float("nan")), 1),
+    (dict(eps=float("inf")), 1), (dict(d=16385), 2), (dict(T=1 << 41), 2),
+])
+def test_norm_config_is_checked(kw, status):
+    base = dict(T=16, d=64, kind=0, dtype=0, w_dtype=0, eps=1e-5)
+    base.update(kw)
+    cfg = B.NormConfig(**base)
+    n = ctypes.c_size_t(0)
+    assert B.lib().moe_norm_workspace_size(ctypes.byref(cfg), ctypes.byref(n)) == status
+    assert _fwd(cfg) == status
+    assert _bwd(cfg) == status
+
+
+def test_norm_pointers_are_checked():
+    cfg = B.norm_config(16, 64)
+    for missing in ("x", "weight", "y"):
+        assert _fwd(cfg, **{missing: None}) == 1, missing
+    assert _fwd(cfg, residual=FAKE) == 1 and _fwd(cfg, h=FAKE) == 1     # one without the other
+    for missing in ("h", "weight", "mean", "rstd", "dy", "dx"):
+        assert _bwd(cfg, **{missing: None}) == 1, missing
+    assert _bwd(B.norm_config(16, 64, kind="rms")) == 1                 # an RMS norm has no mean
+    need = B.norm_workspace_size(cfg)
+    assert need == 16 * 2 * 64 * 4
+    assert _bwd(cfg, ws=None) == 3 and _bwd(cfg, n=need - 1) == 3 and _bwd(cfg, ws=ctypes.c_void_p(0x10010)) == 3
+    assert _fwd(B.norm_config(0, 64), x=None, weight=None, y=None) == 0  # no rows: nothing to do
+    assert B.lib().moe_norm_workspace_size(ctypes.byref(cfg), None) == 1
+
+
+def test_norm_binding_names_what_it_refuses():
+    with pytest.raises(ValueError, match="kind"):
+        B.norm_config(4, 8, kind="batch")
+    with pytest.raises(ValueError, match="dtype"):
+        B.norm_config(4, 8, dtype="f64")
+    with pytest.raises(ValueError, match="CUDA"):
+        B.norm_forward(B.norm_config(4, 8), torch.zeros(4, 8, dtype=torch.bfloat16), torch.zeros(8, dtype=torch.bfloat16))
+
+
+# ------------------------------------------------------------------ the formulas in 64 bits
+
+def ref_forward(x, weight, bias, residual, kind, eps, dt):
+    h = x.double()
+    if residual is not None:
+        h = (x.float() + residual.float()).to(dt).double()
+    mean = h.mean(1) if kind == "layer" else torch.zeros(h.shape[0], dtype=torch.float64)
+    z = h - mean[:, None]
+    rstd = 1 / torch.sqrt((z * z).mean(1) + eps)
+    y = z * rstd[:, None] * weight.double()
+    return h, mean, rstd, y if bias is None else y + bias.double()
+
+
+def ref_backward(h, weight, mean, rstd, dy, dh, kind):
+    xh = (h.double() - mean[:, None]) * rstd[:, None]
+    g = dy.double() * weight.double()
+    dx = g - xh * (g * xh).mean(1, keepdim=True)
+    if kind == "layer":
+        dx = dx - g.mean(1, keepdim=True)
+    dx = dx * rstd[:, None]
+    return dx if dh is None else dx + dh.double(), (dy.double() * xh).sum(0), dy.double().sum(0)
+
+
+def make(T, d, dtype, w_dtype, seed, offset=0.0):
+    g = torch.Generator().manual_seed(seed)
+    dt, wt = TORCH[dtype], TORCH[w_dtype]
+
+    def n(*s, t=dt, m=0.0):
+        return (torch.randn(*s, generator=g) + m).to(t)
+
+    return dict(x=n(T, d, m=offset), residual=n(T, d), weight=n(d, t=wt), bias=n(d, t=wt), dy=n(T, d), dh=n(T, d))
+
+
+def cuda(t):
+    return None if t is None else t.to("cuda")
+
+
+def check_forward(kind, dtype, w_dtype, T, d, use_res, use_bias, eps=1e-5, offset=0.0, seed=0):
+    v = make(T, d, dtype, w_dtype, seed + T + d, offset)
+    res, bias = (v["residual"] if use_res else None), (v["bias"] if use_bias else None)
+    cfg = B.norm_config(T, d, kind=kind, eps=eps, dtype=dtype, w_dtype=w_dtype)
+    y, h, mean, rstd = B.norm_forward(cfg, cuda(v["x"]), cuda(v["weight"]), cuda(bias), cuda(res), want_stats=True)
+    h0, mean0, rstd0, y0 = ref_forward(v["x"], v["weight"], bias, res, kind, eps, TORCH[dtype])
+    if use_res:
+        assert torch.equal(h.cpu().double(), h0)
+    else:
+        assert h is None
+    big = h0.abs().amax(1)
+    # the mean: 32-bit sums; 1 / spread: relative error of the sum of squares about a mean that is off by that much
+    if kind == "layer":
+        assert ((mean.cpu().double() - mean0).abs() <= F32 * big).all()
+    else:
+        assert mean is None
+    lose = F32 * (1 + (big * rstd0) ** 2 * (F32 if kind == "layer" else 0))
+    assert ((rstd.cpu().double() / rstd0 - 1).abs() <= lose).all()
+    scale = (big[:, None] * rstd0[:, None]) * v["weight"].double().abs() + (0 if bias is None else bias.double().abs())
+    err = (y.cpu().double() - y0).abs()
+    assert (err <= half_step(dtype) * y0.abs() * (1 + 2 * F32) + F32 * scale + torch.finfo(TORCH[dtype]).tiny).all()
+    return v, cfg
+
+
+FORWARD = [
+    ("layer", "bf16", "bf16", 5, 64, False, True), ("rms", "bf16", "f32", 33, 640, True, False),
+    ("layer", "f16", "f16", 7, 768, True, True), ("rms", "f16", "f32", 3, 776, False, False),
+    ("layer", "f32", "f32", 9, 384, False, False), ("rms", "f32", "f32", 2, 388, True, True),
+    ("layer", "bf16", "f32", 4, 4096, True, True), ("layer", "bf16", "bf16", 2, 8192, True, False),
+    ("rms", "f16", "f16", 3, 8200, False, True), ("layer", "f32", "f32", 2, 8192, True, True),
+    ("layer", "f32", "f32", 3, 8196, False, True), ("rms", "f32", "f32", 1, 16384, True, False),
+    ("layer", "bf16", "bf16", 2, 16384, True, True),
+    # widths that are not whole 16-byte words, up to and past the register kernel's
+    ("layer", "bf16", "bf16", 5, 1, False, True), ("rms", "bf16", "bf16", 5, 1, False, False),
+    ("layer", "f16", "f32", 11, 7, True, True), ("layer", "bf16", "bf16", 17, 257, True, False),
+    ("layer", "f32", "f32", 6, 1411, False, True), ("rms", "f16", "f16", 4, 4095, True, True),
+    ("layer", "bf16", "f32", 3, 4097, True, True), ("rms", "f32", "f32", 2, 16383, True, False),
+    # more rows than one round of the grid
+    ("layer", "bf16", "bf16", 20011, 24, False, True), ("rms", "f32", "f32", 5003, 301, True, False),
+    ("layer", "f16", "f16", 3001, 1032, True, True),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", FORWARD, ids=["-".join(map(str, c)) for c in FORWARD])
+def test_forward(case):
+    check_forward(*case)
+
+
+@pytest.mark.gpu
+def test_forward_of_rows_far_from_zero():
+    """The variance is summed about the mean: rows of mean 1000 and unit spread keep it."""
+    check_forward("layer", "f32", "f32", 8, 1024, False, False, offset=1000.0)
+    check_forward("layer", "f32", "f32", 8, 1023, False, False, offset=1000.0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 2048, 333, 5001])
+def test_constant_and_zero_rows(d):
+    """No spread: y is the bias (1 / sqrt(eps) times zero), and with eps = 0 the zero row is 0 / 0."""
+    x = torch.zeros(3, d)
+    x[1] = 3.0
+    w, b = torch.full((d,), 2.0), torch.full((d,), 0.25)
+    y, _, mean, rstd = B.norm_forward(B.norm_config(3, d, dtype="f32"), cuda(x), cuda(w), cuda(b), want_stats=True)
+    assert torch.equal(y.cpu(), b.expand(3, d)) and torch.equal(mean.cpu(), torch.tensor([0.0, 3.0, 0.0]))
+    assert np.allclose(rstd.cpu().numpy(), 1e-5 ** -0.5, rtol=1e-6)
+    y, _, _, _ = B.norm_forward(B.norm_config(3, d, dtype="f32", kind="rms", eps=0.0), cuda(x), cuda(w))
+    # 1 / sqrt(9) has no 32-bit value: half a step of the type, and the root's own error of two steps, twice over
+    assert y[0].isnan().all() and ((y[1] - 2.0).abs() <= 2.0 * F32).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [64, 2048, 333, 5001])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_infinities_and_nan_stay_in_their_row(d, kind):
+    x = torch.randn(6, d, generator=torch.Generator().manual_seed(d))
+    clean = x.clone()
+    x[1, d // 2], x[4, d - 1] = float("nan"), float("inf")
+    w = torch.ones(d)
+    cfg = B.norm_config(6, d, kind=kind, dtype="f32")
+    y = B.norm_forward(cfg, cuda(x), cuda(w))[0].cpu()
+    y0 = B.norm_forward(cfg, cuda(clean), cuda(w))[0].cpu()
+    for r in (0, 2, 3, 5):
+        assert torch.equal(y[r], y0[r])
+    assert y[1].isnan().all() and y[4, d - 1].isnan()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [512, 515, 9001])
+def test_forward_in_place_and_unaligned(d):
+    v = make(19, d, "bf16", "bf16", 5)
+    cfg = B.norm_config(19, d, kind="rms")
+    w = cuda(v["weight"])
+    y0, h0, _, _ = B.norm_forward(cfg, cuda(v["x"]), w, residual=cuda(v["residual"]))
+    x, res = cuda(v["x"]), cuda(v["residual"])
+    y, h, _, _ = B.norm_forward(cfg, x, w, residual=res, h=res, y=x)     # the residual stream goes on in place
+    assert h is res and y is x and torch.equal(h, h0) and torch.equal(y, y0)
+    # the same rows two bytes further on
+    raw = torch.zeros(19 * d + 1, dtype=torch.bfloat16, device="cuda")
+    raw[1:] = cuda(v["x"]).flatten()
+    rw = torch.zeros(d + 1, dtype=torch.bfloat16, device="cuda")
+    rw[1:] = w
+    y2, h2, _, _ = B.norm_forward(cfg, raw[1:].view(19, d), rw[1:], residual=cuda(v["residual"]))
+    assert torch.equal(h2, h0)
+    assert (y2.float() - y0.float()).abs().max() <= torch.finfo(torch.bfloat16).eps * y0.float().abs().max()
+
+
+# ------------------------------------------------------------------ backward
+
+BACKWARD = FORWARD + [("layer", "bf16", "f32", 2999, 640, True, True), ("rms", "f16", "f16", 1200, 2048, False, False)]
+
+
+def check_backward(kind, dtype, w_dtype, T, d, use_dh, use_bias):
+    v = make(T, d, dtype, w_dtype, 3 * T + d)
+    dt = TORCH[dtype]
+    _, mean0, rstd0, _ = ref_forward(v["x"], v["weight"], None, None, kind, 1e-5, dt)
+    mean32, rstd32 = mean0.float(), rstd0.float()
+    dh = v["dh"] if use_dh else None
+    cfg = B.norm_config(T, d, kind=kind, dtype=dtype, w_dtype=w_dtype)
+    args = (cuda(v["x"]), cuda(v["weight"]), cuda(mean32) if kind == "layer" else None, cuda(rstd32), cuda(v["dy"]))
+    dx, dw, db = B.norm_backward(cfg, *args, dh=cuda(dh), want_bias=use_bias)
+    # the formula of the same 32-bit statistics
+    m, r = (mean32 if kind == "layer" else torch.zeros(T)).double(), rstd32.double()
+    dx0, dw0, db0 = ref_backward(v["x"], v["weight"], m, r, v["dy"], dh, kind)
+    xh = ((v["x"].double() - m[:, None]) * r[:, None]).abs()
+    g = (v["dy"].double() * v["weight"].double()).abs()
+    # every term of the sum that dx is, by magnitude
+    terms = r[:, None] * (g + xh * (g * xh).mean(1, keepdim=True) + g.mean(1, keepdim=True)) * (1 + 0 * xh)
+    if dh is not None:
+        terms = terms + dh.double().abs()
+    err = (dx.cpu().double() - dx0).abs()
+    assert (err <= half_step(dtype) * dx0.abs() * (1 + 2 * F32) + F32 * terms + torch.finfo(dt).tiny).all()
+    big = v["x"].double().abs().amax(1, keepdim=True) * r[:, None]
+    assert ((dw.cpu().double() - dw0).abs() <= F32 * (v["dy"].double().abs() * (xh + big)).sum(0)).all()
+    if use_bias:
+        assert ((db.cpu().double() - db0).abs() <= F32 * v["dy"].double().abs().sum(0)).all()
+    else:
+        assert db is None
+    again = B.norm_backward(cfg, *args, dh=cuda(dh), want_bias=use_bias)
+    for a, b in zip((dx, dw, db), again):
+        assert a is None or torch.equal(a, b)   # a fixed order
+    return v, cfg, args, (dx, dw, db)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", BACKWARD, ids=["-".join(map(str, c)) for c in BACKWARD])
+def test_backward(case):
+    check_backward(*case)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_backward_against_differences(kind):
+    """dL/dx, dL/dw and dL/db of L = sum(y * dy) against central differences of the formula in 64 bits."""
+    T, d = 3, 40
+    v = make(T, d, "f32", "f32", 77)
+    cfg = B.norm_config(T, d, kind=kind, dtype="f32")
+    _, _, mean, rstd = B.norm_forward(cfg, cuda(v["x"]), cuda(v["weight"]), cuda(v["bias"]), want_stats=True)
+    dx, dw, db = B.norm_backward(cfg, cuda(v["x"]), cuda(v["weight"]), mean, rstd, cuda(v["dy"]), want_bias=True)
+    vals = [v["x"].double(), v["weight"].double(), v["bias"].double()]
+
+    def loss():
+        m = vals[0].mean(1, keepdim=True) if kind == "layer" else 0.0
+        z = vals[0] - m
+        return ((z / torch.sqrt((z * z).mean(1, keepdim=True) + 1e-5) * vals[1] + vals[2]) * v["dy"].double()).sum()
+
+    step = 1e-5
+    for t, got in zip(vals, (dx, dw, db)):
+        flat, g = t.view(-1), got.cpu().double().view(-1)
+        for i in range(0, flat.numel(), 7):
+            keep = flat[i].item()
+            flat[i] = keep + step
+            up = loss()
+            flat[i] = keep - step
+            down = loss()
+            flat[i] = keep
+            # differences are off by step^2 times a third derivative of order 10, and 64-bit rounding over the step
+            assert abs((up - down).item() / (2 * step) - g[i].item()) <= 1e-6 + 64 * 2.0 ** -24 * 10 * (1 + abs(g[i].item()))
+
+
+@pytest.mark.gpu
+def test_backward_without_the_parameters_and_in_place():
+    v, cfg, args, (dx, _, _) = check_backward("layer", "bf16", "bf16", 50, 1024, True, True)
+    dy, dh = args[4].clone(), cuda(v["dh"])
+    got, dw, db = B.norm_backward(cfg, *args[:4], dy, dh=dh, dx=dy, want_weight=False)
+    assert dw is None and db is None and got is dy and torch.equal(dy, dx)
+    got, _, _ = B.norm_backward(cfg, *args, dh=dh, dx=dh)
+    assert got is dh and torch.equal(dh, dx)
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    cfg = B.norm_config(0, 48, dtype="f32")
+    e = torch.empty(0, 48, device="cuda")
+    w = torch.ones(48, device="cuda")
+    assert B.norm_forward(cfg, e, w)[0].shape == (0, 48)
+    dx, dw, db = B.norm_backward(cfg, e, w, torch.empty(0, device="cuda"), torch.empty(0, device="cuda"), e, want_bias=True)
+    assert dx.shape == (0, 48) and (dw == 0).all() and (db == 0).all()
+
+
+@pytest.mark.gpu
+def test_captured_and_on_another_stream():
+    """One graph of forward and backward, replayed on new inputs, beside eager calls on a second stream."""
+    v = make(100, 1536, "bf16", "bf16", 9)
+    cfg = B.norm_config(100, 1536)
+    x, w, dy = cuda(v["x"]), cuda(v["weight"]), cuda(v["dy"])
+
+    def step():
+        y, _, mean, rstd = B.norm_forward(cfg, x, w, want_stats=True)
+        return (y,) + B.norm_backward(cfg, x, w, mean, rstd, dy, want_bias=True)
+
+    want = [t.clone() for t in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        eager = step()
+    side.synchronize()
+    for a, b in zip(eager, want):
+        assert torch.equal(a, b)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    graph.replay()
+    for a, b in zip(out, want):
+        assert torch.equal(a, b)
+    x.copy_(cuda(v["dh"]))
+    graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip([t.clone() for t in out], step()):
+        assert torch.equal(a, b)
