@@ -446,6 +446,54 @@ moe_status moe_norm_backward(const moe_norm_config *cfg, const void *h, const vo
                              void *dx, float *dweight, float *dbias, void *ws, size_t ws_bytes,
                              void *stream);
 
+/* ---- the dense gated feed-forward block: the MLP of the decoder blocks that
+ * are not MoE layers ("Tutorial 11", section 4: decoder_sparse_step and
+ * mlp_only_layers say which blocks are), forward, training and backward.
+ *
+ *   u = x W_gate^T,  v = x W_up^T,  a = act(u) v,  y = a W_down^T
+ *
+ * and, given dy, with r = dy W_down:  du = r v act'(u),  dv = r act(u),
+ *   dx = du W_gate + dv W_up,  dW_gate = du^T x,  dW_up = dv^T x,
+ *   dW_down = dy^T a.
+ *
+ * Accumulation is fp32.  a, and for training u, v, du and dv, are rounded to
+ * dtype once each between the products; every output is rounded once. */
+typedef enum { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 } moe_ffn_act;
+typedef struct {
+    int64_t T;      /* tokens; 0 is allowed */
+    int32_t d, h;   /* model and hidden width, multiples of 8 (else MOE_ERR_UNSUPPORTED) */
+    int32_t act;    /* moe_ffn_act: u sigmoid(u), or u (1 + tanh(sqrt(2/pi) (u + 0.044715 u^3))) / 2 */
+    int32_t dtype;  /* MOE_BF16 or MOE_F16 (MOE_F32: MOE_ERR_UNSUPPORTED) */
+} moe_ffn_config;
+
+/* Bytes of device workspace of moe_ffn_forward (train == 0), or of one
+ * training step, moe_ffn_forward_train and moe_ffn_backward on the same
+ * workspace (train != 0) (host only).  Limits: T * max(d, h) < 2^40, T < 2^31 - 256. */
+moe_status moe_ffn_workspace_size(const moe_ffn_config *cfg, int32_t train, size_t *bytes);
+
+/* x [T, d]; w_gate, w_up [h, d]; w_down [d, h]; y [T, d] out; all 16-byte
+ * aligned (else MOE_ERR_INVALID_ARG).  ws: at least moe_ffn_workspace_size
+ * bytes, 256-byte aligned.  moe_ffn_forward_train gives the same y and keeps
+ * in ws what moe_ffn_backward needs (u, v and a). */
+moe_status moe_ffn_forward(const moe_ffn_config *cfg, const void *x, const void *w_gate,
+                           const void *w_up, const void *w_down, void *y, void *ws, size_t ws_bytes,
+                           void *stream);
+moe_status moe_ffn_forward_train(const moe_ffn_config *cfg, const void *x, const void *w_gate,
+                                 const void *w_up, const void *w_down, void *y, void *ws,
+                                 size_t ws_bytes, void *stream);
+
+/* Gradients of the block after moe_ffn_forward_train with the same inputs on
+ * the same workspace, which stays as the forward left it (the call may be
+ * repeated, with another dy).  dx [T, d], dw_gate, dw_up [h, d], dw_down [d, h]
+ * are overwritten; each may be NULL (not computed).  x is read only for dw_gate
+ * and dw_up, the weights only for dx and for them.  Every sum has a fixed
+ * order: repeated calls give identical bits.  T = 0 writes zero weight
+ * gradients. */
+moe_status moe_ffn_backward(const moe_ffn_config *cfg, const void *x, const void *w_gate,
+                            const void *w_up, const void *w_down, const void *dy, void *ws,
+                            size_t ws_bytes, void *dx, void *dw_gate, void *dw_up, void *dw_down,
+                            void *stream);
+
 /* Largest T*k that moe_forward serves with the CUDA-core small-batch kernels
  * (one warp per weight row, weights streamed once); larger batches use the
  * tensor-core grouped GEMM. */

@@ -27,7 +27,8 @@ EXPORTED = ["moe_status_string", "moe_validate", "moe_workspace_size", "moe_work
             "moe_route_workspace_size", "moe_update_bias", "moe_balance_loss", "moe_train_workspace_size",
             "moe_forward_train", "moe_backward", "moe_quantize_q4", "moe_forward_q4",
             "moe_forward_host_workspace_size", "moe_forward_host",
-            "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward"]
+            "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward",
+            "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_forward_train", "moe_ffn_backward"]
 STAGES = ["route", "permute", "gate_up", "shared_gate_up", "down", "shared_down", "finalize"]
 
 
@@ -53,6 +54,11 @@ class NormConfig(ctypes.Structure):
                 ("w_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class FfnConfig(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int64), ("d", ctypes.c_int32), ("h", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 class WorkspaceViews(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("ids", "gates", "shared_gate", "counts", "offsets",
                                                "sorted_rows", "inv_rows", "act", "act_shared", "y_acc",
@@ -73,6 +79,7 @@ def lib() -> ctypes.CDLL:
         P, S = ctypes.c_void_p, ctypes.c_size_t
         C = ctypes.POINTER(MoEConfig)
         N = ctypes.POINTER(NormConfig)
+        F = ctypes.POINTER(FfnConfig)
         sig = {
             "moe_status_string": ([ctypes.c_int], ctypes.c_char_p),
             "moe_validate": ([C], ctypes.c_int),
@@ -99,6 +106,10 @@ def lib() -> ctypes.CDLL:
             "moe_norm_workspace_size": ([N, ctypes.POINTER(S)], ctypes.c_int),
             "moe_norm_forward": ([N] + [P] * 9, ctypes.c_int),
             "moe_norm_backward": ([N] + [P] * 10 + [S, P], ctypes.c_int),
+            "moe_ffn_workspace_size": ([F, ctypes.c_int32, ctypes.POINTER(S)], ctypes.c_int),
+            "moe_ffn_forward": ([F] + [P] * 6 + [S, P], ctypes.c_int),
+            "moe_ffn_forward_train": ([F] + [P] * 6 + [S, P], ctypes.c_int),
+            "moe_ffn_backward": ([F] + [P] * 6 + [S] + [P] * 5, ctypes.c_int),
             "moe_decode_max_rows": ([], ctypes.c_int32),
             "moe_device_status": ([P], ctypes.c_int),
             "moe_profile_nvtx": ([ctypes.c_int32], ctypes.c_int),
@@ -653,3 +664,63 @@ def norm_backward(cfg: NormConfig, h, weight, mean, rstd, dy, dh=None, dx=None, 
                                    _ptr(dbias, "dbias"), _ptr(ws, "ws", dtype=torch.uint8),
                                    0 if ws is None else ws.numel(), _stream(stream)), "moe_norm_backward")
     return dx, dweight, dbias
+
+
+# ----------------------------------------------------------------------------- dense gated feed-forward block
+
+FFN_ACTS = {"silu": 0, "gelu_tanh": 1}
+
+
+def ffn_config(T, d, h, act="silu", dtype="bf16") -> FfnConfig:
+    """moe_ffn_config.  act: "silu" or "gelu_tanh"; dtype: "bf16" or "f16"."""
+    return FfnConfig(int(T), int(d), int(h), _choice(FFN_ACTS, act, "act"), _choice(DTYPES, dtype, "dtype"))
+
+
+def ffn_workspace_size(cfg: FfnConfig, train: bool = False) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().moe_ffn_workspace_size(ctypes.byref(cfg), int(bool(train)), ctypes.byref(n)), "moe_ffn_workspace_size")
+    return n.value
+
+
+def alloc_ffn_workspace(cfg: FfnConfig, train: bool = False, device=None) -> torch.Tensor:
+    """A uint8 device tensor of moe_ffn_workspace_size bytes."""
+    return torch.empty(max(ffn_workspace_size(cfg, train), 1), dtype=torch.uint8, device=device or "cuda")
+
+
+def _ffn_forward(name, cfg, x, w_gate, w_up, w_down, y, ws, stream):
+    dt = _TORCH_DTYPES[cfg.dtype]
+    if y is None:
+        y = torch.empty(cfg.T, cfg.d, dtype=dt, device=x.device)
+    _check(getattr(lib(), name)(ctypes.byref(cfg), _ptr(x, "x", (cfg.T, cfg.d), dt),
+                                _ptr(w_gate, "w_gate", (cfg.h, cfg.d), dt), _ptr(w_up, "w_up", (cfg.h, cfg.d), dt),
+                                _ptr(w_down, "w_down", (cfg.d, cfg.h), dt), _ptr(y, "y", (cfg.T, cfg.d), dt),
+                                _ptr(ws, "ws", dtype=torch.uint8), ws.numel(), _stream(stream)), name)
+    return y
+
+
+def ffn_forward(cfg: FfnConfig, x, w_gate, w_up, w_down, y=None, ws=None, stream=None):
+    """moe_ffn_forward: y[T,d] of the dense gated block (allocated unless given); ws is allocated if not given."""
+    if ws is None:
+        ws = alloc_ffn_workspace(cfg, device=x.device)
+    return _ffn_forward("moe_ffn_forward", cfg, x, w_gate, w_up, w_down, y, ws, stream)
+
+
+def ffn_forward_train(cfg: FfnConfig, x, w_gate, w_up, w_down, ws, y=None, stream=None):
+    """moe_ffn_forward_train: y[T,d]; ws (alloc_ffn_workspace with train=True) keeps what ffn_backward needs."""
+    return _ffn_forward("moe_ffn_forward_train", cfg, x, w_gate, w_up, w_down, y, ws, stream)
+
+
+def ffn_backward(cfg: FfnConfig, x, w_gate, w_up, w_down, dy, ws, grads=None, stream=None) -> dict:
+    """moe_ffn_backward after ffn_forward_train(cfg, x, ..., ws): the gradients dx, dw_gate, dw_up and dw_down, all
+    allocated, or those that ``grads`` holds (one that is absent or None there is not computed)."""
+    dt = _TORCH_DTYPES[cfg.dtype]
+    shapes = {"dx": (cfg.T, cfg.d), "dw_gate": (cfg.h, cfg.d), "dw_up": (cfg.h, cfg.d), "dw_down": (cfg.d, cfg.h)}
+    if grads is None:
+        grads = {n: torch.empty(s, dtype=dt, device=dy.device) for n, s in shapes.items()}
+    _check(lib().moe_ffn_backward(ctypes.byref(cfg), _ptr(x, "x", shapes["dx"], dt),
+                                  _ptr(w_gate, "w_gate", shapes["dw_gate"], dt), _ptr(w_up, "w_up", shapes["dw_up"], dt),
+                                  _ptr(w_down, "w_down", shapes["dw_down"], dt), _ptr(dy, "dy", shapes["dx"], dt),
+                                  _ptr(ws, "ws", dtype=torch.uint8), ws.numel(),
+                                  *(_ptr(grads.get(n), n, s, dt) for n, s in shapes.items()), _stream(stream)),
+           "moe_ffn_backward")
+    return grads

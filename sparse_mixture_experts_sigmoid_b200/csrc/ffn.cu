@@ -1,0 +1,186 @@
+// Entry points of the dense gated feed-forward block (contracts in
+// include/moe.h): argument checks, the workspace's layout and the launches.
+//
+//   forward : GATED  (x, W_gate, W_up -> a; u and v kept for training)
+//             STORE  (a, W_down -> y)
+//   backward: DGATED (dy, W_down, u, v -> du, dv)
+//             STORE  (dy^T a -> dW_down), STORE (du W_gate + dv W_up -> dx),
+//             STORE  (du^T x, dv^T x -> dW_gate, dW_up: one launch)
+#include "ffn.cuh"
+
+namespace moe {
+namespace ffn {
+namespace {
+
+size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+struct Layout {
+    size_t act, pre, grad, total;   // offsets: a [T, h]; u | v [T, 2h]; du | dv [T, 2h]
+};
+Layout layout(const moe_ffn_config &c, bool train) {
+    const size_t rows = (size_t)c.T * (size_t)c.h * 2;
+    Layout L{};
+    L.act = 0;
+    L.pre = align256(rows);
+    L.grad = L.pre + (train ? align256(2 * rows) : 0);
+    L.total = L.grad + (train ? align256(2 * rows) : 0);
+    return L;
+}
+
+moe_status check(const moe_ffn_config *c) {
+    if (!c) return MOE_ERR_INVALID_ARG;
+    if (c->T < 0 || c->d < 1 || c->h < 1) return MOE_ERR_INVALID_ARG;
+    if (c->act != MOE_ACT_SILU && c->act != MOE_ACT_GELU_TANH) return MOE_ERR_INVALID_ARG;
+    if (c->dtype != MOE_BF16 && c->dtype != MOE_F32 && c->dtype != MOE_F16) return MOE_ERR_INVALID_ARG;
+    if (c->dtype == MOE_F32 || c->d % 8 || c->h % 8) return MOE_ERR_UNSUPPORTED;
+    if (c->d >= (1 << 30) || c->h >= (1 << 30)) return MOE_ERR_UNSUPPORTED;
+    const int64_t w = c->d > c->h ? c->d : c->h;
+    if (c->T >= ((int64_t)1 << 31) - 256 || c->T * w >= (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+// The fields that every product of a call shares.
+Gemm product(const moe_ffn_config &c, Kind kind, bool a_mn, bool b_mn, int64_t M, int N, int64_t K, uint32_t *err) {
+    Gemm g{};
+    g.kind = kind;
+    g.a_mn = a_mn;
+    g.b_mn = b_mn;
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.ranges = g.halves = 1;
+    g.act = c.act;
+    g.bf16 = c.dtype == MOE_BF16;
+    g.err = err;
+    return g;
+}
+
+moe_status forward(const moe_ffn_config *c, bool train, const void *x, const void *wg, const void *wu, const void *wd,
+                   void *y, void *ws, size_t ws_bytes, void *stream) {
+    const moe_status st = check(c);
+    if (st != MOE_OK) return st;
+    if (c->T == 0) return MOE_OK;
+    if (!x || !wg || !wu || !wd || !y) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(x) || !aligned16(wg) || !aligned16(wu) || !aligned16(wd) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+    const Layout L = layout(*c, train);
+    if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOE_ERR_WORKSPACE;
+    uint32_t *err = device_error_word();
+    if (!err) return MOE_ERR_CUDA;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t T = c->T, d = c->d, h = c->h;
+    char *act = static_cast<char *>(ws) + L.act, *pre = static_cast<char *>(ws) + L.pre;
+    Gemm g = product(*c, GATED, false, false, T, c->h, d, err);
+    g.a0 = {x, T, d, d};
+    g.b0 = {wg, h, d, d};
+    g.b1 = {wu, h, d, d};
+    g.c0 = {act, T, h, h};
+    if (train) {
+        g.c1 = {pre, T, h, 2 * h};
+        g.c2 = {pre + 2 * h, T, h, 2 * h};
+    }
+    cudaError_t e = launch_pair_gemm(g, s);
+    if (e == cudaSuccess) {
+        g = product(*c, STORE, false, false, T, c->d, h, err);
+        g.a0 = {act, T, h, h};
+        g.b0 = {wd, d, h, h};
+        g.c0 = {y, T, d, d};
+        e = launch_pair_gemm(g, s);
+    }
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // namespace
+}  // namespace ffn
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::ffn;
+
+extern "C" {
+
+moe_status moe_ffn_workspace_size(const moe_ffn_config *c, int32_t train, size_t *bytes) {
+    if (!bytes) return MOE_ERR_INVALID_ARG;
+    const moe_status st = check(c);
+    if (st != MOE_OK) return st;
+    *bytes = layout(*c, train != 0).total;
+    return MOE_OK;
+}
+
+moe_status moe_ffn_forward(const moe_ffn_config *c, const void *x, const void *w_gate, const void *w_up,
+                           const void *w_down, void *y, void *ws, size_t ws_bytes, void *stream) {
+    return forward(c, false, x, w_gate, w_up, w_down, y, ws, ws_bytes, stream);
+}
+
+moe_status moe_ffn_forward_train(const moe_ffn_config *c, const void *x, const void *w_gate, const void *w_up,
+                                 const void *w_down, void *y, void *ws, size_t ws_bytes, void *stream) {
+    return forward(c, true, x, w_gate, w_up, w_down, y, ws, ws_bytes, stream);
+}
+
+moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *w_gate, const void *w_up,
+                            const void *w_down, const void *dy, void *ws, size_t ws_bytes, void *dx, void *dw_gate,
+                            void *dw_up, void *dw_down, void *stream) {
+    const moe_status st = check(c);
+    if (st != MOE_OK) return st;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t T = c->T, d = c->d, h = c->h;
+    cudaError_t e = cudaSuccess;
+    if (T == 0) {   // no tokens: the weights' gradients are zero
+        for (void *p : {dw_gate, dw_up, dw_down})
+            if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, 2 * (size_t)d * (size_t)h, s);
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
+    const bool gates = dw_gate || dw_up, inner = dx || gates;   // inner: du and dv are needed
+    if (!inner && !dw_down) return MOE_OK;
+    if (!dy || (inner && !w_down) || (dx && (!w_gate || !w_up)) || (gates && !x)) return MOE_ERR_INVALID_ARG;
+    for (const void *p : {x, w_gate, w_up, w_down, dy, (const void *)dx, (const void *)dw_gate, (const void *)dw_up,
+                          (const void *)dw_down})
+        if (!aligned16(p)) return MOE_ERR_INVALID_ARG;
+    const Layout L = layout(*c, true);
+    if (!ws || ws_bytes < L.total || (reinterpret_cast<uintptr_t>(ws) & 255)) return MOE_ERR_WORKSPACE;
+    uint32_t *err = device_error_word();
+    if (!err) return MOE_ERR_CUDA;
+    char *act = static_cast<char *>(ws) + L.act, *pre = static_cast<char *>(ws) + L.pre,
+         *grad = static_cast<char *>(ws) + L.grad;
+    const Matrix du{grad, T, h, 2 * h}, dv{grad + 2 * h, T, h, 2 * h};
+    if (inner) {
+        Gemm g = product(*c, DGATED, false, true, T, c->h, d, err);
+        g.a0 = {dy, T, d, d};
+        g.b0 = {w_down, d, h, h};
+        g.u = {pre, T, h, 2 * h};
+        g.v = {pre + 2 * h, T, h, 2 * h};
+        g.c0 = du;
+        g.c1 = dv;
+        e = launch_pair_gemm(g, s);
+    }
+    if (e == cudaSuccess && dw_down) {
+        Gemm g = product(*c, STORE, true, true, d, c->h, T, err);
+        g.a0 = {dy, T, d, d};
+        g.b0 = {act, T, h, h};
+        g.c0 = {dw_down, d, h, h};
+        e = launch_pair_gemm(g, s);
+    }
+    if (e == cudaSuccess && dx) {
+        Gemm g = product(*c, STORE, false, true, T, c->d, h, err);
+        g.ranges = 2;
+        g.a0 = du;
+        g.a1 = dv;
+        g.b0 = {w_gate, h, d, d};
+        g.b1 = {w_up, h, d, d};
+        g.c0 = {dx, T, d, d};
+        e = launch_pair_gemm(g, s);
+    }
+    if (e == cudaSuccess && gates) {
+        Gemm g = product(*c, STORE, true, true, h, c->d, T, err);
+        g.halves = dw_gate && dw_up ? 2 : 1;
+        g.a0 = dw_gate ? du : dv;
+        g.a1 = dv;
+        g.b0 = {x, T, d, d};
+        g.c0 = {dw_gate ? dw_gate : dw_up, h, d, d};
+        g.c1 = {dw_up, h, d, d};
+        e = launch_pair_gemm(g, s);
+    }
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,330 @@
+"""The dense gated feed-forward block, forward and backward, against its formulas in 64 bits.
+
+Tolerances.  With half = finfo(dtype).eps / 2 (one rounding), and acc = 2^-17 for what the fp32 sums
+and the exponential lose relative to the sum of the terms' magnitudes (a sum of n terms of one
+rounding each in a fixed tree; products of 16-bit values are exact in fp32):
+
+  u, v   : off by acc * (|x| |W|^T); kept for the backward pass with one rounding more
+  a      : off by |act'| |v| e_u + |act| e_v + half |a|          (|act'| <= 1.2)
+  y      : off by e_a |Wd|^T + acc (|a| |Wd|^T) + half |y|
+  r      : off by acc * (|dy| |Wd|)
+  du     : off by e_r |v act'| + |r| e_v |act'| + |r v| |act''| e_u + half |du|   (|act''| <= 0.8)
+  dv     : off by e_r |act| + |r| |act'| e_u + half |dv|
+  dx     : off by e_du |Wg| + e_dv |Wu| + acc (...) + half |dx|, the weights' gradients likewise
+
+and a twentieth more for the products of two errors.  These bounds add every error with the same
+sign; independent roundings grow with the root, so each output's error is also held in norm: every
+rounding on the way to it adds at most `half` of the norm.
+"""
+import ctypes
+
+import pytest
+import torch
+
+from sparse_mixture_experts_sigmoid_b200 import binding as B
+
+TORCH = {"bf16": torch.bfloat16, "f16": torch.float16}
+ACC = 2.0 ** -17
+GRADS = ("dx", "dw_gate", "dw_up", "dw_down")
+
+# ------------------------------------------------------------------ host checks (no GPU)
+
+FAKE = ctypes.c_void_p(0x10000)
+
+
+
+
+def _forward(cfg, skip=None, ws=FAKE, n=1 << 45, train=False, at=None):
+    p = [FAKE] * 5
+    if skip is not None:
+        p[skip] = None if at is None else at
+    f = B.lib().moe_ffn_forward_train if train else B.lib().moe_ffn_forward
+    return f(ctypes.byref(cfg), *p, ws, n, None)
+
+
+def _backward(cfg, ins=(FAKE,) * 5, outs=(FAKE,) * 4, ws=FAKE, n=1 << 45):
+    return B.lib().moe_ffn_backward(ctypes.byref(cfg), *ins, ws, n, *outs, None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(T=-1), 1), (dict(d=0), 1), (dict(h=-8), 1), (dict(act=2), 1), (dict(act=-1), 1), (dict(dtype=3), 1),
+    (dict(dtype=1), 2), (dict(d=12), 2), (dict(h=100), 2), (dict(T=1 << 31), 2), (dict(T=1 << 30, h=2048), 2),
+    (dict(d=1 << 30), 2),
+])
+def test_ffn_config_is_checked(kw, status):
+    base = dict(T=16, d=64, h=128, act=0, dtype=0)
+    base.update(kw)
+    cfg = B.FfnConfig(**base)
+    n = ctypes.c_size_t(0)
+    assert B.lib().moe_ffn_workspace_size(ctypes.byref(cfg), 0, ctypes.byref(n)) == status
+    assert _forward(cfg) == status and _forward(cfg, train=True) == status and _backward(cfg) == status
+
+
+def test_ffn_pointers_and_workspace_are_checked():
+    cfg = B.ffn_config(16, 64, 128)
+    for i in range(5):
+        assert _forward(cfg, skip=i) == 1 and _forward(cfg, skip=i, train=True) == 1
+        assert _forward(cfg, skip=i, at=ctypes.c_void_p(0x10008)) == 1      # 16-byte aligned tensors
+    need, train = B.ffn_workspace_size(cfg), B.ffn_workspace_size(cfg, True)
+    assert need == 16 * 128 * 2 and train == 5 * need
+    for w, n in ((None, need), (ctypes.c_void_p(0x10080), need), (FAKE, need - 1)):
+        assert _forward(cfg, ws=w, n=n) == 3
+    assert _forward(cfg, n=train - 1, train=True) == 3 and _backward(cfg, n=train - 1) == 3
+    none = (None,) * 4
+    assert _backward(cfg, outs=none) == 0                                   # nothing asked for
+    for i in (0, 1, 2, 3, 4):
+        ins = [FAKE] * 5
+        ins[i] = None
+        assert _backward(cfg, ins=ins) == 1
+    assert _backward(cfg, outs=(ctypes.c_void_p(0x10008), None, None, None)) == 1
+    assert _forward(B.ffn_config(0, 64, 128), skip=0, ws=None, n=0) == 0    # no tokens
+    assert B.lib().moe_ffn_workspace_size(ctypes.byref(cfg), 0, None) == 1
+
+
+def test_ffn_binding_names_what_it_refuses():
+    with pytest.raises(ValueError, match="act"):
+        B.ffn_config(4, 8, 8, act="relu")
+    cfg = B.ffn_config(4, 8, 8)
+    z = torch.zeros(4, 8, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="CUDA"):
+        B.ffn_forward(cfg, z, z, z, z, ws=z)
+
+
+# ------------------------------------------------------------------ the formulas in 64 bits
+
+def act64(name, u):
+    """act, act', in 64 bits."""
+    if name == "silu":
+        s = torch.sigmoid(u)
+        return u * s, s * (1 + u * (1 - s))
+    c = (2 / torch.pi) ** 0.5
+    t = torch.tanh(c * (u + 0.044715 * u ** 3))
+    return 0.5 * u * (1 + t), 0.5 * (1 + t) + 0.5 * u * (1 - t * t) * c * (1 + 3 * 0.044715 * u * u)
+
+
+def reference(v, act, half):
+    """The outputs and their elementwise bounds (see the top of the file)."""
+    x, wg, wu, wd, dy = (v[k].double() for k in ("x", "w_gate", "w_up", "w_down", "dy"))
+    ax, awg, awu, awd, ady = (t.abs() for t in (x, wg, wu, wd, dy))
+    u, up = x @ wg.T, x @ wu.T
+    au, dau = act64(act, u)
+    a = au * up
+    e_u, e_v = ACC * (ax @ awg.T), ACC * (ax @ awu.T)
+    e_a = 1.2 * up.abs() * e_u + au.abs() * e_v + half * a.abs() + ACC * a.abs()
+    out, tol = {"y": a @ wd.T}, {}
+    tol["y"] = e_a @ awd.T + ACC * (a.abs() @ awd.T)
+    # the backward pass takes u, v with one rounding more
+    k_u, k_v = e_u + half * u.abs(), e_v + half * up.abs()
+    r = dy @ wd
+    e_r = ACC * (ady @ awd)
+    du, dv = r * up * dau, r * au
+    e_du = e_r * (up * dau).abs() + (r * dau).abs() * k_v + 0.8 * (r * up).abs() * k_u + (half + ACC) * du.abs()
+    e_dv = e_r * au.abs() + 1.2 * r.abs() * k_u + (half + ACC) * dv.abs()
+    out |= {"dx": du @ wg + dv @ wu, "dw_gate": du.T @ x, "dw_up": dv.T @ x, "dw_down": dy.T @ a}
+    tol["dx"] = e_du @ awg + e_dv @ awu + ACC * (du.abs() @ awg + dv.abs() @ awu)
+    tol["dw_gate"] = (e_du + ACC * du.abs()).T @ ax
+    tol["dw_up"] = (e_dv + ACC * dv.abs()).T @ ax
+    tol["dw_down"] = ady.T @ (e_a + ACC * a.abs())
+    return out, {k: 1.05 * t + half * out[k].abs() for k, t in tol.items()}
+
+
+# roundings on the way to each output: y: a, y; dw_down: a, itself; the others: u, v, du or dv, themselves
+ROUNDINGS = {"y": 2, "dw_down": 2, "dx": 4, "dw_gate": 4, "dw_up": 3}
+
+
+def make(T, d, h, dtype, seed=0, scale=1.0, device="cuda"):
+    g = torch.Generator(device=device).manual_seed(seed + T + 3 * d + 7 * h)
+
+    def n(*s, std=1.0):
+        return (torch.randn(*s, generator=g, device=device) * std).to(TORCH[dtype])
+
+    return {"x": n(T, d, std=scale), "w_gate": n(h, d, std=d ** -0.5), "w_up": n(h, d, std=d ** -0.5),
+            "w_down": n(d, h, std=h ** -0.5), "dy": n(T, d)}
+
+
+def check(name, got, want, tol, half):
+    err = (got.double() - want).abs()
+    tiny = float(torch.finfo(got.dtype).tiny) if got.dtype == torch.bfloat16 else 2.0 ** -25 * 4   # fp16: subnormal steps
+    bad = err > tol + tiny
+    assert not bad.any(), f"{name}: {int(bad.sum())} of {bad.numel()} outside, worst {(err / (tol + tiny)).max():.2f} of the bound"
+    norm = want.norm()
+    if norm > 0 and got.numel() >= 64:
+        assert err.norm() <= (ROUNDINGS[name] * half + 8 * ACC) * norm, f"{name}: {float(err.norm() / norm):.2e} in norm"
+
+
+def run(cfg, v, ws=None):
+    args = (v["x"], v["w_gate"], v["w_up"], v["w_down"])
+    ws = B.alloc_ffn_workspace(cfg, train=True) if ws is None else ws
+    y = B.ffn_forward_train(cfg, *args, ws)
+    return {"y": y, **B.ffn_backward(cfg, *args, v["dy"], ws)}
+
+
+CASES = [
+    # (T, d, h, act, dtype): one token to several tiles, widths of part boxes, part K blocks and part tiles
+    (1, 64, 64, "silu", "bf16"), (1, 8, 8, "gelu_tanh", "f16"), (2, 640, 512, "silu", "f16"), (3, 200, 136, "silu", "bf16"),
+    (17, 72, 1000, "gelu_tanh", "bf16"), (31, 1000, 72, "silu", "f16"), (33, 256, 384, "gelu_tanh", "f16"),
+    (64, 512, 768, "silu", "bf16"), (100, 264, 520, "silu", "bf16"), (127, 128, 128, "gelu_tanh", "bf16"),
+    (128, 320, 896, "silu", "f16"), (129, 136, 264, "silu", "bf16"), (255, 640, 2048, "gelu_tanh", "bf16"),
+    (256, 256, 256, "silu", "f16"), (300, 512, 384, "silu", "bf16"), (513, 576, 648, "gelu_tanh", "f16"),
+    (1000, 1000, 2728, "silu", "bf16"), (2049, 264, 136, "silu", "f16"), (5000, 96, 200, "gelu_tanh", "bf16"),
+    (600, 2048, 1408, "silu", "bf16"), (1, 4096, 1032, "silu", "bf16"), (9, 1032, 4096, "gelu_tanh", "f16"),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,h,act,dtype", CASES)
+def test_step_matches_the_formulas(T, d, h, act, dtype):
+    v = make(T, d, h, dtype)
+    cfg = B.ffn_config(T, d, h, act=act, dtype=dtype)
+    half = torch.finfo(TORCH[dtype]).eps / 2
+    out, tol = reference(v, act, half)
+    got = run(cfg, v)
+    y = B.ffn_forward(cfg, v["x"], v["w_gate"], v["w_up"], v["w_down"])
+    torch.cuda.synchronize()
+    assert B.device_status() == 0
+    for k in ("y",) + GRADS:
+        check(k, got[k], out[k], tol[k], half)
+    check("y", y, out["y"], tol["y"], half)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_large_pre_activations(dtype):
+    """u of a hundred and more: both activations' flat and straight parts, and no overflow on the way.  The sums over
+    40 tokens of |a| up to 4e4 pass fp16's 65504 in places: there the rounded value is an infinity, and nowhere else."""
+    for act in ("silu", "gelu_tanh"):
+        v = make(40, 64, 128, dtype, scale=60.0)
+        half = torch.finfo(TORCH[dtype]).eps / 2
+        out, tol = reference(v, act, half)
+        got = run(B.ffn_config(40, 64, 128, act=act, dtype=dtype), v)
+        for k in ("y",) + GRADS:
+            top = torch.finfo(TORCH[dtype]).max
+            inside = out[k].abs() + tol[k] < top
+            assert (got[k].isfinite() | ~inside).all() and (got[k].isinf() | (out[k].abs() - tol[k] < top)).all()
+            check(k, torch.where(inside, got[k], 0), torch.where(inside, out[k], 0.0), tol[k], half)
+
+
+@pytest.mark.gpu
+def test_gradients_against_differences():
+    """dL/dx and dL/dW of L = sum(y * dy), taken from central differences of the formula in 64 bits."""
+    T, d, h = 3, 16, 24
+    v = make(T, d, h, "f16", device="cpu")
+    for act in ("silu", "gelu_tanh"):
+        got = run(B.ffn_config(T, d, h, act=act, dtype="f16"), {k: t.cuda() for k, t in v.items()})
+        vals = {k: t.double() for k, t in v.items()}
+
+        def loss():
+            a = act64(act, vals["x"] @ vals["w_gate"].T)[0] * (vals["x"] @ vals["w_up"].T)
+            return float(((a @ vals["w_down"].T) * vals["dy"]).sum())
+
+        half = 2.0 ** -11
+        _, tol = reference(v, act, half)
+        for key, name in (("x", "dx"), ("w_gate", "dw_gate"), ("w_up", "dw_up"), ("w_down", "dw_down")):
+            flat, g, t = vals[key].view(-1), got[name].cpu().double().view(-1), tol[name].view(-1)
+            for i in range(0, flat.numel(), 5):
+                keep = flat[i].item()
+                flat[i] = keep + 1e-4
+                up = loss()
+                flat[i] = keep - 1e-4
+                down = loss()
+                flat[i] = keep
+                # 1e-8 times a third derivative of order 10, and 64-bit rounding of L over the step
+                assert abs((up - down) / 2e-4 - float(g[i])) <= float(t[i]) + 1e-6, (name, i)
+
+
+@pytest.mark.gpu
+def test_rows_do_not_meet():
+    """A token's y and dx are its own: NaN in one token leaves the others' bits, at sizes of every path."""
+    for T, d, h in ((5, 256, 512), (200, 256, 512), (700, 512, 1024)):
+        v = make(T, d, h, "bf16")
+        cfg = B.ffn_config(T, d, h)
+        clean = run(cfg, v)
+        bad = dict(v, x=v["x"].clone(), dy=v["dy"].clone())
+        bad["x"][T // 2, 3] = float("nan")
+        got = run(cfg, bad)
+        rest = torch.arange(T, device="cuda") != T // 2
+        for k in ("y", "dx"):
+            assert torch.equal(got[k][rest], clean[k][rest]) and got[k][T // 2].isnan().all(), (k, T)
+
+
+@pytest.mark.gpu
+def test_nothing_outside_the_outputs_is_written():
+    """Outputs inside larger buffers: what lies around them stays as it was."""
+    for T, d, h in ((3, 72, 136), (130, 200, 264), (600, 264, 136)):
+        v = make(T, d, h, "bf16")
+        cfg = B.ffn_config(T, d, h)
+        n = B.ffn_workspace_size(cfg, True)
+        raw = torch.full((n + 512,), 0x55, dtype=torch.uint8, device="cuda")
+        ws = raw[:n]
+        bufs, grads = {}, {}
+        for k, shape in (("y", (T, d)), ("dx", (T, d)), ("dw_gate", (h, d)), ("dw_up", (h, d)), ("dw_down", (d, h))):
+            bufs[k] = torch.full((shape[0] * shape[1] + 256,), 7.0, dtype=torch.bfloat16, device="cuda")
+            grads[k] = bufs[k][128:128 + shape[0] * shape[1]].view(shape)
+        y = grads.pop("y")
+        args = (v["x"], v["w_gate"], v["w_up"], v["w_down"])
+        B.ffn_forward_train(cfg, *args, ws, y=y)
+        B.ffn_backward(cfg, *args, v["dy"], ws, grads=grads)
+        torch.cuda.synchronize()
+        assert (raw[n:] == 0x55).all()
+        for k, b in bufs.items():
+            assert (b[:128] == 7).all() and (b[-128:] == 7).all(), k
+
+
+@pytest.mark.gpu
+def test_backward_in_parts_and_again():
+    """Every subset of the gradients, and a second call on the same workspace with another dy, give the same bits."""
+    T, d, h = 150, 200, 328
+    v = make(T, d, h, "f16")
+    cfg = B.ffn_config(T, d, h, dtype="f16")
+    args = (v["x"], v["w_gate"], v["w_up"], v["w_down"])
+    ws = B.alloc_ffn_workspace(cfg, train=True)
+    B.ffn_forward_train(cfg, *args, ws)
+    full = {k: t.clone() for k, t in B.ffn_backward(cfg, *args, v["dy"], ws).items()}
+    B.ffn_backward(cfg, *args, v["dy"] * 2, ws)
+    for wanted in (("dx",), ("dw_gate",), ("dw_up",), ("dw_down",), ("dx", "dw_up"), ("dw_gate", "dw_down"), GRADS):
+        grads = {k: torch.full_like(full[k], 7.0) for k in wanted}
+        B.ffn_backward(cfg, *args, v["dy"], ws, grads=grads)
+        for k in wanted:
+            assert torch.equal(grads[k], full[k]), (wanted, k)
+
+
+@pytest.mark.gpu
+def test_no_tokens():
+    cfg = B.ffn_config(0, 64, 128)
+    v = make(0, 64, 128, "bf16")
+    ws = B.alloc_ffn_workspace(cfg, train=True)
+    args = (v["x"], v["w_gate"], v["w_up"], v["w_down"])
+    assert B.ffn_forward(cfg, *args).shape == (0, 64)
+    g = B.ffn_backward(cfg, *args, v["dy"], ws)
+    assert all((g[k] == 0).all() for k in ("dw_gate", "dw_up", "dw_down"))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [1, 40, 700])
+def test_captured_replayed_and_on_two_streams(T):
+    d, h = 512, 640
+    v, other = make(T, d, h, "bf16"), make(T, d, h, "bf16", seed=5)
+    cfg = B.ffn_config(T, d, h)
+    ws = B.alloc_ffn_workspace(cfg, train=True)
+    want = {k: t.clone() for k, t in run(cfg, v, ws).items()}
+    want2 = {k: t.clone() for k, t in run(cfg, other).items()}
+    # two streams at once, a workspace each
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        with torch.cuda.stream(side):
+            b = run(cfg, other)
+        a = run(cfg, v, ws)
+    torch.cuda.synchronize()
+    for k in want:
+        assert torch.equal(a[k], want[k]) and torch.equal(b[k], want2[k]), k
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run(cfg, v, ws)
+    for src, ref in ((v, want), (other, want2)):
+        for k in v:
+            v[k].copy_(src[k].clone())
+        graph.replay()
+        torch.cuda.synchronize()
+        for k in ref:
+            assert torch.equal(out[k], ref[k]), k
