@@ -393,6 +393,35 @@ moe_status moe_forward_q4(const moe_config *cfg, const moe_route_opts *opts, con
                           const void *sh_down, const void *w_shared_gate, void *y, void *ws,
                           size_t ws_bytes, void *stream);
 
+/* ---- 8-bit floating point (e4m3, largest value 448) with a scale per block of
+ * 128: a quantiser and the product of quantised operands, for linear layers
+ * whose weights are held in 8 bits ("Small MoE Architecture, in depth",
+ * "Running experts that do not fit: offloading and quantisation").
+ *
+ *   s = max|x| / 448 over a block (fp32),  q = e4m3(x / s), ties to even
+ *
+ * both quotients correctly rounded.  A block of zeros has scale 0 and codes 0,
+ * so has one whose scale underflows; a block with an infinity has scale inf, one
+ * with a NaN scale NaN: either makes the products that it enters NaN. */
+
+/* Quantises x [rows, cols] (MOE_BF16, MOE_F16 or MOE_F32) into q [rows, cols]
+ * e4m3 bytes and scales [ceil(rows / block_rows), ceil(cols / 128)] fp32.
+ * block_rows: 1 (activations) or 128 (weights); blocks at the edges are
+ * smaller.  cols a multiple of 16 (else MOE_ERR_UNSUPPORTED); x and q 16-byte
+ * aligned; rows = 0 is allowed. */
+moe_status moe_quantize_fp8(const void *x, int32_t dtype, int64_t rows, int32_t cols,
+                            int32_t block_rows, uint8_t *q, float *scales, void *stream);
+
+/* c [M, N] = the product of the values that a and b represent, b transposed:
+ *   c[m, n] = sum_k a[m, k] a_scales[m, k / 128] b[n, k] b_scales[n / 128, k / 128]
+ * a [M, K] with 1 x 128 blocks, b [N, K] with 128 x 128 blocks (as
+ * moe_quantize_fp8 writes them); c MOE_BF16, MOE_F16 or MOE_F32.  Products and
+ * sums are fp32, in a fixed order.  K a multiple of 16 and N of 8 (else
+ * MOE_ERR_UNSUPPORTED); a, b and c 16-byte aligned; M = 0 is allowed. */
+moe_status moe_gemm_fp8(int64_t M, int32_t N, int32_t K, const uint8_t *a, const float *a_scales,
+                        const uint8_t *b, const float *b_scales, void *c, int32_t c_dtype,
+                        void *stream);
+
 /* ---- layer norm and RMS norm of token rows, forward and backward: the norm in
  * front of the layer ("Tutorial 11", section 4: the decoder block normalises,
  * runs the MoE layer and adds the residual), with the residual addition and

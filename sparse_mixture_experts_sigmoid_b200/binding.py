@@ -28,7 +28,8 @@ EXPORTED = ["moe_status_string", "moe_validate", "moe_workspace_size", "moe_work
             "moe_forward_train", "moe_backward", "moe_quantize_q4", "moe_forward_q4",
             "moe_forward_host_workspace_size", "moe_forward_host",
             "moe_norm_workspace_size", "moe_norm_forward", "moe_norm_backward",
-            "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_forward_train", "moe_ffn_backward"]
+            "moe_ffn_workspace_size", "moe_ffn_forward", "moe_ffn_forward_train", "moe_ffn_backward",
+            "moe_quantize_fp8", "moe_gemm_fp8"]
 STAGES = ["route", "permute", "gate_up", "shared_gate_up", "down", "shared_down", "finalize"]
 
 
@@ -106,6 +107,9 @@ def lib() -> ctypes.CDLL:
             "moe_norm_workspace_size": ([N, ctypes.POINTER(S)], ctypes.c_int),
             "moe_norm_forward": ([N] + [P] * 9, ctypes.c_int),
             "moe_norm_backward": ([N] + [P] * 10 + [S, P], ctypes.c_int),
+            "moe_quantize_fp8": ([P, ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, P, P, P], ctypes.c_int),
+            "moe_gemm_fp8": ([ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, P, P, P, P, P, ctypes.c_int32, P],
+                             ctypes.c_int),
             "moe_ffn_workspace_size": ([F, ctypes.c_int32, ctypes.POINTER(S)], ctypes.c_int),
             "moe_ffn_forward": ([F] + [P] * 6 + [S, P], ctypes.c_int),
             "moe_ffn_forward_train": ([F] + [P] * 6 + [S, P], ctypes.c_int),
@@ -724,3 +728,41 @@ def ffn_backward(cfg: FfnConfig, x, w_gate, w_up, w_down, dy, ws, grads=None, st
                                   *(_ptr(grads.get(n), n, s, dt) for n, s in shapes.items()), _stream(stream)),
            "moe_ffn_backward")
     return grads
+
+
+# ----------------------------------------------------------------------------- 8-bit floating point, scales per block of 128
+
+_DTYPE_CODES = {t: c for c, t in _TORCH_DTYPES.items()}
+
+
+def _dtype_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype not in _DTYPE_CODES:
+        raise ValueError(f"{name} must be one of {sorted(map(str, _DTYPE_CODES))}, got {t.dtype}")
+    return _DTYPE_CODES[t.dtype]
+
+
+def quantize_fp8(x: torch.Tensor, block_rows: int = 1, stream=None):
+    """moe_quantize_fp8 of a [rows, cols] CUDA tensor: (codes float8_e4m3fn [rows, cols], scales float32
+    [ceil(rows / block_rows), ceil(cols / 128)]).  block_rows: 1 (activations) or 128 (weights)."""
+    if x.dim() != 2:
+        raise ValueError(f"x must have two dimensions, got {x.dim()}")
+    rows, cols = x.shape
+    q = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=x.device)
+    sc = torch.empty(-(-rows // max(block_rows, 1)), -(-cols // 128), dtype=torch.float32, device=x.device)
+    _check(lib().moe_quantize_fp8(_ptr(x, "x"), _dtype_code(x, "x"), rows, cols, int(block_rows), _ptr(q, "q"),
+                                  _ptr(sc, "scales"), _stream(stream)), "moe_quantize_fp8")
+    return q, sc
+
+
+def gemm_fp8(a, a_scales, b, b_scales, out_dtype="bf16", out=None, stream=None):
+    """moe_gemm_fp8: [M, N] = a b^T of quantised a [M, K] (1 x 128 blocks) and b [N, K] (128 x 128 blocks)."""
+    if a.dim() != 2 or b.dim() != 2:
+        raise ValueError("a and b must have two dimensions")
+    (M, K), N = a.shape, b.shape[0]
+    kb, f8 = -(-K // 128), torch.float8_e4m3fn
+    if out is None:
+        out = torch.empty(M, N, dtype=_TORCH_DTYPES[_choice(DTYPES, out_dtype, "out_dtype")], device=a.device)
+    _check(lib().moe_gemm_fp8(M, N, K, _ptr(a, "a", (M, K), f8), _ptr(a_scales, "a_scales", (M, kb), torch.float32),
+                              _ptr(b, "b", (N, K), f8), _ptr(b_scales, "b_scales", (-(-N // 128), kb), torch.float32),
+                              _ptr(out, "out", (M, N)), _dtype_code(out, "out"), _stream(stream)), "moe_gemm_fp8")
+    return out

@@ -1,0 +1,334 @@
+// C = A B^T in 8-bit floating point (e4m3) with one scale per row and 128
+// columns of A and one per 128 x 128 block of B, on two SMs per 256 x 256 tile
+// (tcgen05.mma.cta_group::2.kind::f8f6f4, fp32 accumulation):
+//
+//   C[m, n] = sum over K blocks kb of  sa[m, kb] sb[n / 128, kb] (A_kb B_kb^T)[m, n]
+//
+// A K block is 128 elements, one 128-byte row of shared memory, four MMAs.  The
+// tensor cores sum inside a block only; the blocks' products differ in scale, so
+// each is read back from TMEM and added to fp32 registers under its scale.  TMEM
+// holds two block products (2 x 256 columns): while the epilogue warps add one,
+// the MMAs write the other.  Per K block of a CTA the MMAs take 512 cycles at the
+// full rate, and the eight epilogue warps 128 x 256 multiply-adds (256 cycles of
+// the four schedulers) and as many TMEM words, so the tensor cores stay the
+// bound.  A warp owns 32 rows x 128 columns of the tile, one scale of B: a
+// thread's 128 sums have one scale per block, sa sb.
+//
+// Every mbarrier wait is bounded as in the grouped kernels.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "fp8.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace fp8 {
+namespace {
+
+using namespace tc;
+
+constexpr int kBM = 256, kBN = 256;
+constexpr int kStage = 128 * 128;          // this CTA's A (or B) of one K block: 128 rows x 128 bytes
+constexpr int kStages = 6;
+constexpr int kEpiWarps = 8;
+constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
+constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kTmemCols = 512;
+constexpr int kBox = 32 * 128;             // a store's box: 32 rows x 128 bytes
+constexpr int kAhead = 4;                  // K blocks whose scales are loaded at a time
+
+struct Ctrl {
+    uint64_t full[kStages];    // even CTA: operands of a K block landed (both CTAs)
+    uint64_t empty[kStages];   // both: the MMAs of a K block are done
+    uint64_t tfull[2];         // both: a block product is ready
+    uint64_t tempty[2];        // even CTA: it has been added by both epilogues
+    uint64_t done;             // both: all MMAs of the pair completed
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct Params {
+    int M, N, kb;              // kb: K blocks
+    int mt, nt;
+    const float *sa, *sb;
+    int c_dtype;
+    uint32_t *err;
+};
+
+__device__ __forceinline__ void mma2_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int c0, int c1) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
+                 ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(smem_u32(src))
+                 : "memory");
+}
+
+// Tile id -> (m, n): row tiles in groups of eight with the column tiles outside
+// them, so that the pairs at work at one time share rows of A and of B in L2.
+__device__ __forceinline__ void tile_of(int id, const Params &p, int &m, int &n) {
+    const int g = id / (8 * p.nt), first = 8 * g, size = min(p.mt - first, 8);
+    id -= g * 8 * p.nt;
+    n = id / size;
+    m = first + id - n * size;
+}
+
+__device__ __forceinline__ uint32_t pack16(float a, float b, bool bf16) {
+    uint32_t r;
+    if (bf16) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+        r = *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __half2 v = __floats2half2_rn(a, b);
+        r = *reinterpret_cast<const uint32_t *>(&v);
+    }
+    return r;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    fp8_pair_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const __grid_constant__ CUtensorMap tmC, Params p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sA = smem, *sB = sA + kStages * kStage, *sEpi = sB + kStages * kStage;
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(sEpi + kEpiWarps * kBox);
+    volatile int *abort = &ctrl->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const bool lead = rank == 0;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctrl->full[s], 1);
+            mbar_init(&ctrl->empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&ctrl->tfull[a], 1);
+            mbar_init(&ctrl->tempty[a], 2 * kEpiWarps);
+        }
+        mbar_init(&ctrl->done, 1);
+        ctrl->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc2(&ctrl->tmem_base, kTmemCols);
+    if (warp == kTmaWarp && lane == 0) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+        prefetch_tmap(&tmC);
+    }
+    pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync_all();   // both CTAs' barriers exist before any remote arrive
+    pdl_launch_dependents();
+
+    const uint32_t tmem = ctrl->tmem_base;
+    const int total = p.mt * p.nt, nk = p.kb;
+    const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            const uint32_t full_lead = mapa_shared(&ctrl->full[0], 0);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int id = pair; id < total && ok; id += npairs) {
+                int m, n;
+                tile_of(id, p, m, n);
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = it % kStages;
+                    if (!wait_bar(&ctrl->empty[s], ((it / kStages) & 1) ^ 1, abort, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    if (lead) mbar_expect_tx(&ctrl->full[s], 4u * kStage);   // A and B of both CTAs
+                    const uint32_t fb = full_lead + s * (uint32_t)sizeof(uint64_t);
+                    tma_load_2d_pair(&tmA, sA + s * kStage, fb, kb * kBlock, m * kBM + (int)rank * 128);
+                    tma_load_2d_pair(&tmB, sB + s * kStage, fb, kb * kBlock, n * kBN + (int)rank * 128);
+                }
+            }
+            if (!ok) {
+                // aborting: let this CTA's copies land before it leaves
+                for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j) {
+                    const uint64_t t0 = globaltimer();
+                    while (!mbar_try_wait(&ctrl->empty[j % kStages], (j / kStages) & 1) &&
+                           globaltimer() - t0 < 100000000ull) {
+                    }
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0 && lead) {
+            // e4m3 A and B (format 0), fp32 D, both K-major
+            constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+            uint32_t it = 0;
+            bool ok = true;
+            for (int id = pair; id < total && ok; id += npairs) {
+                for (int kb = 0; kb < nk; ++kb, ++it) {
+                    const int s = it % kStages;
+                    const uint32_t ph = (it / kStages) & 1, acc = it & 1;
+                    if (!wait_bar(&ctrl->tempty[acc], ((it >> 1) & 1) ^ 1, abort, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    bool got = mbar_try_wait_cluster(&ctrl->full[s], ph);
+                    if (!got) got = wait_bar(&ctrl->full[s], ph, abort, p.err) && mbar_try_wait_cluster(&ctrl->full[s], ph);
+                    if (!got) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t ad = smem_desc(sA + s * kStage), bd = smem_desc(sB + s * kStage);
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk) mma2_fp8(tmem + acc * kBN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk != 0);
+                    mma_commit2(&ctrl->empty[s], 0x3);
+                    mma_commit2(&ctrl->tfull[acc], 0x3);
+                }
+            }
+            mma_commit2(&ctrl->done, 0x3);
+        }
+    } else {
+        const uint32_t tempty_lead = mapa_shared(&ctrl->tempty[0], 0);
+        const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
+        const int cw = (warp >> 2) * 128;
+        uint8_t *box = sEpi + warp * kBox;
+        const int nb = (p.N + kBlock - 1) / kBlock;
+        uint32_t it = 0;
+        bool ok = true;
+        for (int id = pair; id < total && ok; id += npairs) {
+            int m, n;
+            tile_of(id, p, m, n);
+            const int r0 = m * kBM + (int)rank * 128 + (warp & 3) * 32, c0 = n * kBN + cw;
+            // rows and columns past the edge take the last ones' scales: their sums are not stored
+            const float *sa = p.sa + (int64_t)min(r0 + lane, p.M - 1) * nk;
+            const float *sb = p.sb + (int64_t)min(c0 / kBlock, nb - 1) * nk;
+            float acc[128];
+#pragma unroll
+            for (int i = 0; i < 128; ++i) acc[i] = 0.f;
+            float next[kAhead];
+            auto ask = [&](int kb) {
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) next[i] = kb + i < nk ? __ldg(sa + kb + i) * __ldg(sb + kb + i) : 0.f;
+            };
+            ask(0);
+#pragma unroll 1
+            for (int kb0 = 0; kb0 < nk && ok; kb0 += kAhead) {
+                float scale[kAhead];
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) scale[i] = next[i];
+                ask(kb0 + kAhead);
+#pragma unroll
+                for (int i = 0; i < kAhead; ++i) {
+                    if (kb0 + i >= nk || !ok) continue;
+                    const uint32_t b = it & 1;
+                    ok = wait_bar(&ctrl->tfull[b], (it >> 1) & 1, abort, p.err);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    const uint32_t tb = tmem + b * kBN + lane_base + cw;
+#pragma unroll
+                    for (int q = 0; q < 128; q += 32) {
+                        float v[2][16];
+                        tmem_ld16(tb + q, v[0]);
+                        tmem_ld16(tb + q + 16, v[1]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int z = 0; z < 32; ++z) acc[q + z] = fmaf(v[z >> 4][z & 15], scale[i], acc[q + z]);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (lead) mbar_arrive(&ctrl->tempty[b]);
+                        else mbar_arrive_remote(tempty_lead + b * (uint32_t)sizeof(uint64_t));
+                    }
+                    ++it;
+                }
+            }
+            if (!ok) break;
+            // 128 bytes of each row at a time: 64 columns of 16 bits, or 32 of fp32
+            const bool f32 = p.c_dtype == MOE_F32, bf16 = p.c_dtype == MOE_BF16;
+#pragma unroll
+            for (int q = 0; q < 128; q += 32) {
+                if (!f32 && (q & 32)) continue;
+                if (r0 >= p.M || c0 + q >= p.N) continue;
+                if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    uint4 w;
+                    if (f32) {
+                        const float *f = &acc[q + 4 * j];
+                        w = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                       __float_as_uint(f[3]));
+                    } else {
+                        const float *f = &acc[(q & 64) + 8 * j];
+                        w = make_uint4(pack16(f[0], f[1], bf16), pack16(f[2], f[3], bf16), pack16(f[4], f[5], bf16),
+                                       pack16(f[6], f[7], bf16));
+                    }
+                    *reinterpret_cast<uint4 *>(box + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) {
+                    tma_store_2d(&tmC, box, c0 + q, r0);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                }
+            }
+        }
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    }
+
+    // every MMA of the pair has completed (its arrivals on this CTA's barriers
+    // included) before the pair meets for the last time and frees TMEM
+    if (threadIdx.x == 0) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(&ctrl->done, 0) && globaltimer() - t0 < kWaitLimitNs) {
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc2(tmem, kTmemCols);
+}
+
+// A row-major matrix, boxes of 128 bytes (128-byte swizzle) by box_rows.
+bool make_map8(CUtensorMap *m, const void *base, CUtensorMapDataType type, int esize, int64_t rows, int64_t cols,
+               uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * esize};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / esize), box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, type, 2, const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_pair(const Gemm &g, cudaStream_t s) {
+    CUtensorMap mA, mB, mC;
+    const bool f32 = g.c_dtype == MOE_F32;
+    if (!make_map8(&mA, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.M, g.K, 128) ||
+        !make_map8(&mB, g.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.N, g.K, 128) ||
+        !make_map8(&mC, g.c, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, f32 ? 4 : 2, g.M,
+                   g.N, 32))
+        return cudaErrorInvalidValue;
+    Params p{(int)g.M, g.N, (g.K + kBlock - 1) / kBlock, (int)((g.M + kBM - 1) / kBM), (g.N + kBN - 1) / kBN,
+             g.sa, g.sb, g.c_dtype, g.err};
+    const size_t smem = 1024 + (size_t)kStages * 2 * kStage + kEpiWarps * kBox + sizeof(Ctrl);
+    cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2, (int64_t)p.mt * p.nt));
+    return launch_kernel_pair(fp8_pair_kernel, 2 * pairs, kThreads, smem, s, mA, mB, mC, p);
+}
+
+}  // namespace fp8
+}  // namespace moe

@@ -1,0 +1,171 @@
+// Quantisation to 8-bit floating point (e4m3) with one fp32 scale per block of
+// 128 columns by 1 row (activations) or 128 rows (weights), and the entry
+// points of the 8-bit product (contracts in include/moe.h).
+//
+//   s = max|x| / 448 over the block,  q = e4m3(x / s)     (448: the largest e4m3 value)
+//
+// Both quotients are correctly rounded, so the codes are a function of the
+// block alone.  The magnitudes are compared as integers, which puts a NaN above
+// every number: a block that holds one gets a NaN scale (and codes 0).
+//
+// Bound by memory: each element is read once and held in registers between the
+// maximum and the rounding.
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+
+#include "fp8.cuh"
+
+namespace moe {
+namespace fp8 {
+namespace {
+
+// Eight consecutive elements as fp32.
+__device__ __forceinline__ void load8_any(const void *p, int dtype, int64_t i, float (&v)[8]) {
+    if (dtype == MOE_F32) {
+        load8(static_cast<const float *>(p) + i, v);
+    } else if (dtype == MOE_BF16) {
+        load8(static_cast<const __nv_bfloat16 *>(p) + i, v);
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + i);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
+            v[2 * j] = f.x;
+            v[2 * j + 1] = f.y;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t max_bits(const float (&v)[8], uint32_t m) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    return m;
+}
+__device__ __forceinline__ float scale_of(uint32_t bits) { return __fdiv_rn(__uint_as_float(bits), 448.f); }
+
+// The codes of eight elements.  A scale of zero (a block of zeros, or of
+// magnitudes whose scale underflows) or NaN gives zeros.
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
+    const bool ok = s > 0.f;
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const float2 f = ok ? make_float2(__fdiv_rn(v[i], s), __fdiv_rn(v[i + 1], s)) : make_float2(0.f, 0.f);
+        w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (8 * (i & 2));
+    }
+    return make_uint2(w[0], w[1]);
+}
+
+// 1 x 128 blocks: sixteen lanes per block, eight elements a lane.
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const void *x, int dtype, int64_t rows, int cols, int kb,
+                                                            uint8_t *q, float *scales) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t total = rows * kb, step = (int64_t)gridDim.x * 16;
+    const int l = threadIdx.x & 15;
+    // whole warps stay in the loop: the two blocks of a warp reduce together
+    for (int64_t b0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; b0 < total; b0 += step) {
+        const int64_t b = b0 + ((threadIdx.x >> 4) & 1);
+        const int64_t r = b / kb;
+        const int c = (int)(b - r * kb) * kBlock + l * 8;
+        const bool in = b < total && c < cols;
+        float v[8] = {};
+        if (in) load8_any(x, dtype, r * cols + c, v);
+        uint32_t m = max_bits(v, 0);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const float s = scale_of(m);
+        if (in) *reinterpret_cast<uint2 *>(q + r * cols + c) = codes8(v, s);
+        if (b < total && l == 0) scales[b] = s;
+    }
+}
+
+// 128 x 128 blocks: one CTA per block, eight 16-byte pieces of 16-bit elements a thread.
+__global__ void __launch_bounds__(256) quantize_square_kernel(const void *x, int dtype, int64_t rows, int cols, int kb,
+                                                              uint8_t *q, float *scales) {
+    __shared__ uint32_t part[8];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int64_t br = blockIdx.x / kb;
+    const int bc = (int)(blockIdx.x - br * kb);
+    const int c = bc * kBlock + (threadIdx.x & 15) * 8;
+    const int64_t r0 = br * kBlock + (threadIdx.x >> 4);
+    float v[8][8];
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t r = r0 + 16 * j;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
+        if (r < rows && c < cols) load8_any(x, dtype, r * cols + c, v[j]);
+        m = max_bits(v[j], m);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max(m, part[j]);
+    const float s = scale_of(m);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int64_t r = r0 + 16 * j;
+        if (r < rows && c < cols) *reinterpret_cast<uint2 *>(q + r * cols + c) = codes8(v[j], s);
+    }
+    if (threadIdx.x == 0) scales[blockIdx.x] = s;
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+}  // namespace
+}  // namespace fp8
+}  // namespace moe
+
+using namespace moe;
+using namespace moe::fp8;
+
+extern "C" {
+
+moe_status moe_quantize_fp8(const void *x, int32_t dtype, int64_t rows, int32_t cols, int32_t block_rows, uint8_t *q,
+                            float *scales, void *stream) {
+    if (rows < 0 || cols < 1 || (block_rows != 1 && block_rows != kBlock)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_BF16 && dtype != MOE_F32 && dtype != MOE_F16) return MOE_ERR_INVALID_ARG;
+    if (cols % 16 || cols >= (1 << 30) || rows >= (int64_t)1 << 40 || rows * cols >= (int64_t)1 << 48)
+        return MOE_ERR_UNSUPPORTED;
+    const int kb = (cols + kBlock - 1) / kBlock;
+    const int64_t blocks = (rows + kBlock - 1) / kBlock * kb;
+    if (block_rows == kBlock && blocks >= (int64_t)1 << 31) return MOE_ERR_UNSUPPORTED;
+    if (rows == 0) return MOE_OK;
+    if (!x || !q || !scales || !aligned16(x) || !aligned16(q)) return MOE_ERR_INVALID_ARG;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (block_rows == 1) {
+        const int64_t want = (rows * kb + 15) / 16;
+        e = launch_kernel(quantize_rows_kernel, (unsigned)std::min<int64_t>(want, 16LL * num_sms()), 256, 0, s, x,
+                          (int)dtype, rows, (int)cols, kb, q, scales);
+    } else {
+        e = launch_kernel(quantize_square_kernel, (unsigned)blocks, 256, 0, s, x, (int)dtype, rows, (int)cols, kb, q,
+                          scales);
+    }
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+moe_status moe_gemm_fp8(int64_t M, int32_t N, int32_t K, const uint8_t *a, const float *a_scales, const uint8_t *b,
+                        const float *b_scales, void *c, int32_t c_dtype, void *stream) {
+    if (M < 0 || N < 1 || K < 1) return MOE_ERR_INVALID_ARG;
+    if (c_dtype != MOE_BF16 && c_dtype != MOE_F32 && c_dtype != MOE_F16) return MOE_ERR_INVALID_ARG;
+    if (K % 16 || N % 8 || K >= (1 << 30) || N >= (1 << 30) || M >= ((int64_t)1 << 31) - 256) return MOE_ERR_UNSUPPORTED;
+    if (M * (int64_t)(N > K ? N : K) >= (int64_t)1 << 40) return MOE_ERR_UNSUPPORTED;
+    if (M == 0) return MOE_OK;
+    if (!a || !a_scales || !b || !b_scales || !c || !aligned16(a) || !aligned16(b) || !aligned16(c))
+        return MOE_ERR_INVALID_ARG;
+    uint32_t *err = device_error_word();
+    if (!err) return MOE_ERR_CUDA;
+    const Gemm g{M, N, K, a, b, a_scales, b_scales, c, c_dtype, err};
+    const cudaError_t e = launch_pair(g, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+}  // extern "C"

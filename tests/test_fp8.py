@@ -1,0 +1,250 @@
+"""8-bit floating point: the quantiser bit for bit, the product against its formula in 64 bits.
+
+Quantiser: scale and code are correctly rounded quotients, so they equal the host's, bit for bit.
+
+Product: the codes and scales are its inputs, so nothing is lost before the sums.  e4m3 products are
+exact in fp32; the fp32 sums over K (128 at a time on the tensor cores, then a multiply-add per block)
+and the two roundings of the scale lose at most acc = 2^-17 of the sum of the terms' magnitudes, and
+the output is rounded once: finfo(dtype).eps / 2 of its value.
+"""
+import ctypes
+
+import pytest
+import torch
+
+from sparse_mixture_experts_sigmoid_b200 import binding as B
+
+TORCH = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+F8 = torch.float8_e4m3fn
+ACC = 2.0 ** -17
+FAKE = ctypes.c_void_p(0x10000)
+
+# ------------------------------------------------------------------ host checks (no GPU)
+
+
+def _quant(dtype=0, rows=4, cols=64, br=1, x=FAKE, q=FAKE, s=FAKE):
+    return B.lib().moe_quantize_fp8(x, dtype, rows, cols, br, q, s, None)
+
+
+def _gemm(M=4, N=64, K=64, dtype=0, **at):
+    p = {n: at.get(n, FAKE) for n in ("a", "sa", "b", "sb", "c")}
+    return B.lib().moe_gemm_fp8(M, N, K, p["a"], p["sa"], p["b"], p["sb"], p["c"], dtype, None)
+
+
+def test_fp8_arguments_are_checked():
+    off = ctypes.c_void_p(0x10008)
+    for kw, st in ((dict(dtype=3), 1), (dict(rows=-1), 1), (dict(cols=0), 1), (dict(br=2), 1), (dict(br=0), 1),
+                   (dict(cols=24), 2), (dict(cols=1 << 30), 2), (dict(rows=1 << 41), 2), (dict(x=None), 1),
+                   (dict(q=None), 1), (dict(s=None), 1), (dict(x=off), 1), (dict(q=off), 1)):
+        assert _quant(**kw) == st, kw
+    assert _quant(rows=0, x=None, q=None, s=None) == 0
+    for kw, st in ((dict(M=-1), 1), (dict(N=0), 1), (dict(K=0), 1), (dict(dtype=3), 1), (dict(K=24), 2), (dict(N=12), 2),
+                   (dict(M=1 << 31), 2), (dict(M=1 << 30, N=2048), 2), (dict(K=1 << 30), 2), (dict(a=None), 1),
+                   (dict(sa=None), 1), (dict(b=None), 1), (dict(sb=None), 1), (dict(c=None), 1), (dict(a=off), 1),
+                   (dict(b=off), 1), (dict(c=off), 1)):
+        assert _gemm(**kw) == st, kw
+    assert _gemm(M=0, a=None, c=None) == 0
+
+
+def test_fp8_binding_names_what_it_refuses():
+    z = torch.zeros(4, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="dimensions"):
+        B.quantize_fp8(z[0])
+    with pytest.raises(ValueError, match="CUDA"):
+        B.quantize_fp8(z)
+    with pytest.raises(ValueError, match="x must be"):
+        B.quantize_fp8(z.double())
+    q = z.to(F8)
+    with pytest.raises(ValueError, match="out_dtype"):
+        B.gemm_fp8(q, z, q, z, out_dtype="f64")
+
+
+# ------------------------------------------------------------------ quantiser
+
+def quantize_ref(x, br):
+    """(codes, scales) on the host, one block at a time."""
+    x = x.float().cpu()
+    rows, cols = x.shape
+    q = torch.empty(rows, cols, dtype=F8)
+    sc = torch.empty(-(-rows // br), -(-cols // 128))
+    for i in range(sc.shape[0]):
+        for j in range(sc.shape[1]):
+            b = x[i * br:(i + 1) * br, j * 128:(j + 1) * 128]
+            s = b.abs().amax() / torch.tensor(448.0)
+            sc[i, j] = s
+            v = (b / s).clamp(-448, 448) if s > 0 else torch.zeros_like(b)
+            q[i * br:(i + 1) * br, j * 128:(j + 1) * 128] = v.to(F8)
+    return q, sc
+
+
+def same_bits(a, b):
+    return torch.equal(a.cpu().view(torch.uint8), b.cpu().view(torch.uint8))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,cols,br", [(1, 16, 1), (1, 128, 1), (3, 144, 1), (33, 400, 1), (260, 1040, 1),
+                                          (1, 16, 128), (128, 128, 128), (129, 144, 128), (300, 400, 128), (5, 2048, 128)])
+def test_quantiser_is_the_host_s(dtype, rows, cols, br):
+    g = torch.Generator().manual_seed(rows * cols + br)
+    x = torch.randn(rows, cols, generator=g) * torch.exp(3 * torch.randn(rows, 1, generator=g))
+    x = x.to(TORCH[dtype])
+    q, s = B.quantize_fp8(x.cuda(), br)
+    q0, s0 = quantize_ref(x, br)
+    assert torch.equal(s.cpu(), s0) and same_bits(q, q0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("br", [1, 128])
+def test_quantiser_at_the_edges_of_the_numbers(br):
+    """Zeros, magnitudes whose scale underflows or is subnormal, the type's largest, infinities and NaN: of one block each."""
+    tiny = 2.0 ** -149
+    x = torch.zeros(12 * br, 128)
+    g = torch.Generator().manual_seed(3)
+    for i, top in enumerate((0.0, tiny, 100 * tiny, 448 * tiny, 1000 * tiny, 2.0 ** -126, 1.0, 3.0e38, 1.0, 1.0, 1.0)):
+        r = torch.rand(br, 128, generator=g) * 2 - 1
+        r[0, 5] = 1.0
+        x[i * br:(i + 1) * br] = r * top
+    x[8 * br, 7], x[9 * br, 9], x[10 * br, 0] = float("inf"), float("nan"), float("-inf")
+    x[11 * br:] = -0.0
+    q, s = B.quantize_fp8(x.cuda(), br)
+    q0, s0 = quantize_ref(x, br)
+    assert torch.equal(s.cpu().nan_to_num(-1.0), s0.nan_to_num(-1.0)) and s[9].isnan().all() and s[8].isinf().all()
+    finite = [i for i in range(12) if i not in (8, 9, 10)]
+    for i in finite:
+        assert torch.equal(q[i * br:(i + 1) * br].cpu().float(), q0[i * br:(i + 1) * br].float()), i
+    # an infinite block: its infinity is inf / inf, the rest 0; a NaN block: zeros under a NaN scale
+    assert q[8 * br, 7].float().isnan() and q[10 * br, 0].float().isnan() and (q[9 * br].float() == 0).all()
+    assert (q[8 * br, :7].float() == 0).all()
+    # no rows: nothing to do
+    e, es = B.quantize_fp8(torch.empty(0, 128, device="cuda"), br)
+    assert e.shape == (0, 128) and es.shape == (0, 1)
+
+
+# ------------------------------------------------------------------ product
+
+def values(q, s, br):
+    """What codes and scales represent, in 64 bits."""
+    s = s.double().repeat_interleave(128, 1)[:, :q.shape[1]]
+    return q.double() * (s if br == 1 else s.repeat_interleave(128, 0)[:q.shape[0]])
+
+
+def operands(M, N, K, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed + M + 3 * N + 7 * K)
+    x = torch.randn(M, K, generator=g, device="cuda") * torch.exp(torch.randn(M, 1, generator=g, device="cuda"))
+    w = torch.randn(N, K, generator=g, device="cuda") * torch.exp(torch.randn(N, 1, generator=g, device="cuda"))
+    return B.quantize_fp8(x, 1) + B.quantize_fp8(w, 128)
+
+
+def check(y, aq, sa, bq, sb, dtype):
+    a, b = values(aq, sa, 1), values(bq, sb, 128)
+    y0, mag = a @ b.T, a.abs() @ b.abs().T
+    half = 0.0 if dtype == "f32" else torch.finfo(TORCH[dtype]).eps / 2
+    tol = half * y0.abs() * 1.01 + ACC * mag + 2.0 ** -24
+    # where the value itself passes the type's largest (fp16's 65504), its rounding is an infinity
+    inside = y0.abs() + tol < torch.finfo(TORCH[dtype]).max
+    assert (y.isinf() | (y0.abs() - tol < torch.finfo(TORCH[dtype]).max)).all()
+    err = torch.where(inside, (y.double() - y0).abs(), 0.0)
+    assert y.dtype == TORCH[dtype] and (err <= tol).all(), f"worst {float((err / tol).max()):.2f} of the bound"
+
+
+PRODUCTS = [
+    (1, 64, 64), (1, 8, 16), (2, 136, 144), (7, 256, 512), (16, 1000, 1040), (17, 128, 128), (33, 264, 400), (64, 512, 2048),
+    (65, 2920, 272), (100, 96, 1152), (128, 256, 1024), (129, 520, 640), (200, 2056, 528), (256, 256, 256), (257, 248, 4096),
+    (513, 1024, 896), (1000, 1408, 2048), (3, 4096, 4096), (2500, 24, 48), (40, 14336, 512), (1, 2048, 14336),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", PRODUCTS)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_product_matches_the_formula(M, N, K, dtype):
+    ops = operands(M, N, K)
+    y = B.gemm_fp8(*ops, out_dtype=dtype)
+    again = B.gemm_fp8(*ops, out_dtype=dtype)
+    torch.cuda.synchronize()
+    assert B.device_status() == 0 and torch.equal(y, again)
+    check(y, *ops, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [5, 300])
+def test_scales_of_every_block_count(M):
+    """One block of ones at a time, every other code zero: its own pair of scales and no other's."""
+    N, K = 392, 528
+    kb, nb = -(-K // 128), -(-N // 128)
+    sa = torch.arange(1, M * kb + 1, device="cuda").float().view(M, kb)
+    sb = (2.0 ** torch.arange(nb * kb, device="cuda")).float().view(nb, kb) / 1024
+    b = torch.ones(N, K, device="cuda").to(F8)
+    for k in range(kb):
+        a = torch.zeros(M, K, device="cuda")
+        a[:, k * 128:(k + 1) * 128] = 1
+        y = B.gemm_fp8(a.to(F8), sa, b, sb, out_dtype="f32")
+        want = sa[:, k:k + 1] * sb[torch.arange(N, device="cuda") // 128, k] * min(128, K - 128 * k)
+        assert ((y - want).abs() <= 2 * 2.0 ** -24 * want).all(), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [5, 300])
+def test_nan_and_zero_scales(M):
+    """A NaN block makes its own row (or its 128 columns) NaN and nothing else; scales of zero add nothing."""
+    N, K = 400, 256
+    aq, sa, bq, sb = operands(M, N, K)
+    clean = B.gemm_fp8(aq, sa, bq, sb)
+    s2 = sa.clone()
+    s2[M // 2, 1] = float("nan")
+    y = B.gemm_fp8(aq, s2, bq, sb)
+    rest = torch.arange(M, device="cuda") != M // 2
+    assert y[M // 2].isnan().all() and torch.equal(y[rest], clean[rest])
+    s3 = sb.clone()
+    s3[1, 0] = float("nan")
+    y = B.gemm_fp8(aq, sa, bq, s3)
+    assert y[:, 128:256].isnan().all() and torch.equal(y[:, :128], clean[:, :128]) and torch.equal(y[:, 256:], clean[:, 256:])
+    assert (B.gemm_fp8(aq, torch.zeros_like(sa), bq, sb) == 0).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(3, 72, 144), (130, 264, 400), (300, 520, 272)])
+def test_nothing_outside_the_output_is_written(M, N, K):
+    ops = operands(M, N, K)
+    for dtype in ("bf16", "f32"):
+        buf = torch.full((M * N + 256,), 7.0, dtype=TORCH[dtype], device="cuda")
+        out = buf[128:128 + M * N].view(M, N)
+        assert B.gemm_fp8(*ops, out=out) is out
+        check(out, *ops, dtype)
+        assert (buf[:128] == 7).all() and (buf[-128:] == 7).all()
+
+
+@pytest.mark.gpu
+def test_no_rows():
+    ops = operands(0, 64, 64)
+    assert B.gemm_fp8(*ops).shape == (0, 64)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 40, 700])
+def test_captured_replayed_and_on_another_stream(M):
+    N, K = 640, 528
+    g = torch.Generator(device="cuda").manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda", dtype=torch.bfloat16)
+    w, sw = B.quantize_fp8(torch.randn(N, K, generator=g, device="cuda"), 128)
+
+    def linear():
+        q, s = B.quantize_fp8(x)
+        return B.gemm_fp8(q, s, w, sw)
+
+    want = linear().clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = linear()
+    side.synchronize()
+    assert torch.equal(other, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = linear()
+    graph.replay()
+    assert torch.equal(y, want)
+    x.mul_(-2)
+    graph.replay()
+    assert torch.equal(y, want * -2)   # a power of two: the same codes under twice the scales
