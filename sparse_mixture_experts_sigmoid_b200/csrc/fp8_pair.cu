@@ -33,7 +33,13 @@ constexpr int kStage = 128 * 128;          // this CTA's A (or B) of one K block
 constexpr int kStages = 6;
 constexpr int kEpiWarps = 8;
 constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
-constexpr int kThreads = (kEpiWarps + 2) * 32;
+constexpr int kThreads = (kEpiWarps + 4) * 32;   // three warpgroups: two of epilogue warps, one of the others (two idle)
+// Registers: the 128 sums of an epilogue thread and two TMEM reads want
+// more than an even share.  The block starts with kRegs a thread; the third
+// warpgroup gives some back and the epilogue warpgroups take them:
+// 2 * 128 * 208 + 128 * 88 = 384 * 168.
+constexpr int kRegs = 168, kEpiRegs = 208, kOtherRegs = 88;
+static_assert(2 * 128 * kEpiRegs + 128 * kOtherRegs <= kThreads * kRegs, "within the block's registers");
 constexpr int kTmemCols = 512;
 constexpr int kBox = 32 * 128;             // a store's box: 32 rows x 128 bytes
 constexpr int kAhead = 4;                  // K blocks whose scales are loaded at a time
@@ -53,6 +59,7 @@ struct Params {
     int mt, nt;
     const float *sa, *sb;
     int c_dtype;
+    bool wide;                 // rows of scales are whole 16-byte pieces
     uint32_t *err;
 };
 
@@ -67,6 +74,53 @@ __device__ __forceinline__ void mma2_fp8(uint32_t d, uint64_t a, uint64_t b, uin
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int c0, int c1) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                  ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(smem_u32(src))
+                 : "memory");
+}
+
+// wait_bar without a call: a called function has registers of its own number,
+// which the two halves of a block with setmaxnreg cannot agree on, and the
+// epilogue's 128 sums would have to be kept in memory across it.
+__device__ __forceinline__ bool wait_here(uint64_t *b, uint32_t parity, volatile int *abort, uint32_t *err) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !mbar_try_wait(b, parity); ++i) {
+        if ((i & 63) == 0) {
+            const uint64_t t = globaltimer();
+            if (t0 == 0) t0 = t;
+            if (*abort) return false;
+            if (t - t0 > kWaitLimitNs) {
+                *abort = 1;
+                atomicOr(err, kErrTimeout);
+                return false;
+            }
+        }
+    }
+    return true;
+}
+
+// An arrival that orders nothing: what it releases are TMEM columns whose reads
+// have completed (tcgen05.wait::ld).  With release semantics it waited for every
+// earlier memory operation of the thread to be visible across the cluster,
+// which took 0.4 us per K block (467 -> 302 us on M = K = 4096, N = 14336).
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t *b) {
+    asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+
+// tmem_ld16 whose values are defined once tmem_wait16 on them has returned (it
+// takes them as operands, so that their uses stay behind it while a later read
+// may be issued before those uses).
+__device__ __forceinline__ void tmem_ask16(uint32_t taddr, float (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait16(float (&v)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                   "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15])
+                 :
                  : "memory");
 }
 
@@ -133,67 +187,71 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int total = p.mt * p.nt, nk = p.kb;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
-    if (warp == kTmaWarp) {
-        if (lane == 0) {
-            const uint32_t full_lead = mapa_shared(&ctrl->full[0], 0);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int id = pair; id < total && ok; id += npairs) {
-                int m, n;
-                tile_of(id, p, m, n);
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = it % kStages;
-                    if (!wait_bar(&ctrl->empty[s], ((it / kStages) & 1) ^ 1, abort, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    if (lead) mbar_expect_tx(&ctrl->full[s], 4u * kStage);   // A and B of both CTAs
-                    const uint32_t fb = full_lead + s * (uint32_t)sizeof(uint64_t);
-                    tma_load_2d_pair(&tmA, sA + s * kStage, fb, kb * kBlock, m * kBM + (int)rank * 128);
-                    tma_load_2d_pair(&tmB, sB + s * kStage, fb, kb * kBlock, n * kBN + (int)rank * 128);
-                }
-            }
-            if (!ok) {
-                // aborting: let this CTA's copies land before it leaves
-                for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j) {
-                    const uint64_t t0 = globaltimer();
-                    while (!mbar_try_wait(&ctrl->empty[j % kStages], (j / kStages) & 1) &&
-                           globaltimer() - t0 < 100000000ull) {
+    if (warp >= kEpiWarps) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+        if (warp == kTmaWarp) {
+            if (lane == 0) {
+                const uint32_t full_lead = mapa_shared(&ctrl->full[0], 0);
+                uint32_t it = 0;
+                bool ok = true;
+                for (int id = pair; id < total && ok; id += npairs) {
+                    int m, n;
+                    tile_of(id, p, m, n);
+                    for (int kb = 0; kb < nk; ++kb, ++it) {
+                        const int s = it % kStages;
+                        if (!wait_here(&ctrl->empty[s], ((it / kStages) & 1) ^ 1, abort, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        if (lead) mbar_expect_tx(&ctrl->full[s], 4u * kStage);   // A and B of both CTAs
+                        const uint32_t fb = full_lead + s * (uint32_t)sizeof(uint64_t);
+                        tma_load_2d_pair(&tmA, sA + s * kStage, fb, kb * kBlock, m * kBM + (int)rank * 128);
+                        tma_load_2d_pair(&tmB, sB + s * kStage, fb, kb * kBlock, n * kBN + (int)rank * 128);
                     }
                 }
-            }
-        }
-    } else if (warp == kMmaWarp) {
-        if (lane == 0 && lead) {
-            // e4m3 A and B (format 0), fp32 D, both K-major
-            constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            uint32_t it = 0;
-            bool ok = true;
-            for (int id = pair; id < total && ok; id += npairs) {
-                for (int kb = 0; kb < nk; ++kb, ++it) {
-                    const int s = it % kStages;
-                    const uint32_t ph = (it / kStages) & 1, acc = it & 1;
-                    if (!wait_bar(&ctrl->tempty[acc], ((it >> 1) & 1) ^ 1, abort, p.err)) {
-                        ok = false;
-                        break;
+                if (!ok) {
+                    // aborting: let this CTA's copies land before it leaves
+                    for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j) {
+                        const uint64_t t0 = globaltimer();
+                        while (!mbar_try_wait(&ctrl->empty[j % kStages], (j / kStages) & 1) &&
+                               globaltimer() - t0 < 100000000ull) {
+                        }
                     }
-                    bool got = mbar_try_wait_cluster(&ctrl->full[s], ph);
-                    if (!got) got = wait_bar(&ctrl->full[s], ph, abort, p.err) && mbar_try_wait_cluster(&ctrl->full[s], ph);
-                    if (!got) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t ad = smem_desc(sA + s * kStage), bd = smem_desc(sB + s * kStage);
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) mma2_fp8(tmem + acc * kBN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk != 0);
-                    mma_commit2(&ctrl->empty[s], 0x3);
-                    mma_commit2(&ctrl->tfull[acc], 0x3);
                 }
             }
-            mma_commit2(&ctrl->done, 0x3);
+        } else if (warp == kMmaWarp) {
+            if (lane == 0 && lead) {
+                // e4m3 A and B (format 0), fp32 D, both K-major
+                constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+                uint32_t it = 0;
+                bool ok = true;
+                for (int id = pair; id < total && ok; id += npairs) {
+                    for (int kb = 0; kb < nk; ++kb, ++it) {
+                        const int s = it % kStages;
+                        const uint32_t ph = (it / kStages) & 1, acc = it & 1;
+                        if (!wait_here(&ctrl->tempty[acc], ((it >> 1) & 1) ^ 1, abort, p.err)) {
+                            ok = false;
+                            break;
+                        }
+                        bool got = mbar_try_wait_cluster(&ctrl->full[s], ph);
+                        if (!got) got = wait_here(&ctrl->full[s], ph, abort, p.err) && mbar_try_wait_cluster(&ctrl->full[s], ph);
+                        if (!got) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t ad = smem_desc(sA + s * kStage), bd = smem_desc(sB + s * kStage);
+    #pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) mma2_fp8(tmem + acc * kBN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk != 0);
+                        mma_commit2(&ctrl->empty[s], 0x3);
+                        mma_commit2(&ctrl->tfull[acc], 0x3);
+                    }
+                }
+                mma_commit2(&ctrl->done, 0x3);
+            }
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEpiRegs));
         const uint32_t tempty_lead = mapa_shared(&ctrl->tempty[0], 0);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int cw = (warp >> 2) * 128;
@@ -211,40 +269,57 @@ __global__ void __launch_bounds__(kThreads, 1)
             float acc[128];
 #pragma unroll
             for (int i = 0; i < 128; ++i) acc[i] = 0.f;
-            float next[kAhead];
+            // the scales of the next kAhead blocks, loaded while these are added
+            // (multiplied only then: a product would wait for its loads)
+            float4 na, nb4;
             auto ask = [&](int kb) {
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) next[i] = kb + i < nk ? __ldg(sa + kb + i) * __ldg(sb + kb + i) : 0.f;
+                if (p.wide) {   // whole 16-byte pieces
+                    if (kb < nk) {
+                        na = __ldg(reinterpret_cast<const float4 *>(sa + kb));
+                        nb4 = __ldg(reinterpret_cast<const float4 *>(sb + kb));
+                    }
+                } else {
+                    na.x = kb < nk ? __ldg(sa + kb) : 0.f;
+                    na.y = kb + 1 < nk ? __ldg(sa + kb + 1) : 0.f;
+                    na.z = kb + 2 < nk ? __ldg(sa + kb + 2) : 0.f;
+                    na.w = kb + 3 < nk ? __ldg(sa + kb + 3) : 0.f;
+                    nb4.x = kb < nk ? __ldg(sb + kb) : 0.f;
+                    nb4.y = kb + 1 < nk ? __ldg(sb + kb + 1) : 0.f;
+                    nb4.z = kb + 2 < nk ? __ldg(sb + kb + 2) : 0.f;
+                    nb4.w = kb + 3 < nk ? __ldg(sb + kb + 3) : 0.f;
+                }
             };
             ask(0);
 #pragma unroll 1
             for (int kb0 = 0; kb0 < nk && ok; kb0 += kAhead) {
-                float scale[kAhead];
-#pragma unroll
-                for (int i = 0; i < kAhead; ++i) scale[i] = next[i];
+                const float scale[kAhead] = {na.x * nb4.x, na.y * nb4.y, na.z * nb4.z, na.w * nb4.w};
                 ask(kb0 + kAhead);
 #pragma unroll
                 for (int i = 0; i < kAhead; ++i) {
                     if (kb0 + i >= nk || !ok) continue;
                     const uint32_t b = it & 1;
-                    ok = wait_bar(&ctrl->tfull[b], (it >> 1) & 1, abort, p.err);
+                    ok = wait_here(&ctrl->tfull[b], (it >> 1) & 1, abort, p.err);
                     if (!ok) continue;
                     tc_fence_after();
                     const uint32_t tb = tmem + b * kBN + lane_base + cw;
+                    // 16 columns are read while the 16 before them are added
+                    float v[2][16];
+                    tmem_ask16(tb, v[0]);
 #pragma unroll
-                    for (int q = 0; q < 128; q += 32) {
-                        float v[2][16];
-                        tmem_ld16(tb + q, v[0]);
-                        tmem_ld16(tb + q + 16, v[1]);
-                        tmem_wait_ld();
+                    for (int q = 0; q < 8; ++q) {
+                        tmem_wait16(v[q & 1]);
+                        if (q < 7) tmem_ask16(tb + 16 * (q + 1), v[(q + 1) & 1]);
+                        else {
+                            // the block product is in registers: release it
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if (lead) mbar_arrive_relaxed(&ctrl->tempty[b]);
+                                else mbar_arrive_remote_relaxed(tempty_lead + b * (uint32_t)sizeof(uint64_t));
+                            }
+                        }
 #pragma unroll
-                        for (int z = 0; z < 32; ++z) acc[q + z] = fmaf(v[z >> 4][z & 15], scale[i], acc[q + z]);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (lead) mbar_arrive(&ctrl->tempty[b]);
-                        else mbar_arrive_remote(tempty_lead + b * (uint32_t)sizeof(uint64_t));
+                        for (int z = 0; z < 16; ++z) acc[16 * q + z] = fmaf(v[q & 1][z], scale[i], acc[16 * q + z]);
                     }
                     ++it;
                 }
@@ -322,7 +397,8 @@ cudaError_t launch_pair(const Gemm &g, cudaStream_t s) {
                    g.N, 32))
         return cudaErrorInvalidValue;
     Params p{(int)g.M, g.N, (g.K + kBlock - 1) / kBlock, (int)((g.M + kBM - 1) / kBM), (g.N + kBN - 1) / kBN,
-             g.sa, g.sb, g.c_dtype, g.err};
+             g.sa, g.sb, g.c_dtype, false, g.err};
+    p.wide = p.kb % 4 == 0 && (reinterpret_cast<uintptr_t>(g.sa) & 15) == 0 && (reinterpret_cast<uintptr_t>(g.sb) & 15) == 0;
     const size_t smem = 1024 + (size_t)kStages * 2 * kStage + kEpiWarps * kBox + sizeof(Ctrl);
     cudaError_t e = cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
