@@ -7,6 +7,7 @@
 //             STORE  (dy^T a -> dW_down), STORE (du W_gate + dv W_up -> dx),
 //             STORE  (du^T x, dv^T x -> dW_gate, dW_up: one launch)
 #include "ffn.cuh"
+#include "skinny.cuh"
 
 namespace moe {
 namespace ffn {
@@ -70,6 +71,36 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t T = c->T, d = c->d, h = c->h;
     char *act = static_cast<char *>(ws) + L.act, *pre = static_cast<char *>(ws) + L.pre;
+    if (skinny::wants(T, c->h, c->d)) {
+        skinny::Product p{};
+        p.gated = true;
+        p.bf16 = c->dtype == MOE_BF16;
+        p.T = T;
+        p.N = c->h;
+        p.K = c->d;
+        p.x = x;
+        p.w0 = wg;
+        p.w1 = wu;
+        p.out = act;
+        p.out_dtype = c->dtype;
+        p.pre = train ? pre : nullptr;
+        p.act = c->act;
+        p.err = err;
+        cudaError_t e = skinny::launch(p, s);
+        if (e == cudaSuccess) {
+            p.gated = false;
+            p.N = c->d;
+            p.K = c->h;
+            p.x = act;
+            p.w0 = wd;
+            p.w1 = nullptr;
+            p.out = y;
+            p.pre = nullptr;
+            p.early = true;   // the kernel before is the one above
+            e = skinny::launch(p, s);
+        }
+        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+    }
     Gemm g = product(*c, GATED, false, false, T, c->h, d, err);
     g.a0 = {x, T, d, d};
     g.b0 = {wg, h, d, d};

@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) {
                 if (lead) mbar_arrive(&ctrl->tempty[acc]);
-                else mbar_arrive_remote(tempty_lead + acc * (uint32_t)sizeof(uint64_t));
+                else mbar_arrive_remote_relaxed(tempty_lead + acc * (uint32_t)sizeof(uint64_t));
             }
         }
         if (lane == 0) bulk_wait_all();

@@ -16,6 +16,7 @@
 #include <algorithm>
 
 #include "fp8.cuh"
+#include "skinny.cuh"
 
 namespace moe {
 namespace fp8 {
@@ -163,8 +164,25 @@ moe_status moe_gemm_fp8(int64_t M, int32_t N, int32_t K, const uint8_t *a, const
         return MOE_ERR_INVALID_ARG;
     uint32_t *err = device_error_word();
     if (!err) return MOE_ERR_CUDA;
-    const Gemm g{M, N, K, a, b, a_scales, b_scales, c, c_dtype, err};
-    const cudaError_t e = launch_pair(g, static_cast<cudaStream_t>(stream));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e;
+    if (skinny::wants(M, N, K)) {
+        skinny::Product p{};
+        p.fp8 = true;
+        p.T = M;
+        p.N = N;
+        p.K = K;
+        p.x = a;
+        p.w0 = b;
+        p.sx = a_scales;
+        p.sw = b_scales;
+        p.out = c;
+        p.out_dtype = c_dtype;
+        p.err = err;
+        e = skinny::launch(p, s);
+    } else {
+        e = launch_pair(Gemm{M, N, K, a, b, a_scales, b_scales, c, c_dtype, err}, s);
+    }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -1,0 +1,404 @@
+// Products of few token rows with a large weight, on the tensor cores:
+//
+//   STORE : out[t, n] = sum_k x[t, k] w[n, k]
+//   GATED : out[t, n] = act(u) v,  u = x w0^T, v = x w1^T  (u, v kept for training)
+//
+// for bf16 / fp16 operands, and (STORE) e4m3 operands with a scale per row and
+// 128 columns of x and per 128 x 128 block of w.
+//
+// Such a product reads each weight once and is bound by that: the kernel keeps
+// weight bytes in flight and does little else.  The weight rows are the M of the
+// MMA (128 of them a tile; for GATED 64 rows of w0 and the same 64 of w1) and the
+// tokens its N (16 to 128), so no tensor-core row is spent on padding tokens and
+// a stage of the ring is 16 KB of weights.  K is cut into S consecutive ranges,
+// one per CTA of a cluster, so that small weights too have enough CTAs to draw on
+// HBM; two CTAs fit on an SM, so one's set-up and ending run under the other's
+// loads.  Each CTA leaves its fp32 sums in its shared memory; after a cluster
+// barrier each adds 1/S of the tile's rows over the S ranges, in their order
+// (repeated calls give the same bits), through distributed shared memory, applies
+// the activation, and stores.
+//
+// Every mbarrier wait is bounded as in the grouped kernels.
+#include <cuda_fp16.h>
+
+#include <algorithm>
+
+#include "ffn.cuh"
+#include "skinny.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace skinny {
+namespace {
+
+using namespace tc;
+
+constexpr int kRows = 128;                 // weight rows of a tile
+constexpr int kWStage = kRows * 128;       // 16 KB: 128 bytes of K of each
+constexpr int kTmaWarp = 4, kMmaWarp = 5;  // epilogue warps 0 .. 3: one per TMEM lane quarter
+constexpr int kThreads = 6 * 32;
+constexpr int kMaxStages = 6;
+constexpr int kSmem = 113 * 1024;          // two CTAs per SM
+
+template <int NT>
+constexpr int stages() {
+    const int s = (kSmem - 1024 - 2048 - 4 * 2 * NT * 4) / (kWStage + NT * 128);
+    return s > kMaxStages ? kMaxStages : s;
+}
+
+struct Ctrl {
+    uint64_t full[kMaxStages], empty[kMaxStages];
+    uint64_t tfull[2];    // the sums (fp8: a block product) are ready
+    uint64_t tempty[2];   // fp8: a block product has been added
+    uint32_t tmem_base;
+    int abort;
+};
+
+struct Params {
+    int T, N, kb;         // kb: K blocks of 128 bytes
+    int S, mt;            // cluster size; weight tiles
+    const float *sx, *sw;
+    void *out;
+    int out_dtype;
+    void *pre;
+    int act;
+    uint32_t fmt;         // 16-bit operand format of the instruction descriptor: 0 fp16, 1 bf16
+    bool early;
+    uint32_t *err;
+};
+
+__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
+        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// A float of the shared memory of CTA `rank` of the cluster, at this CTA's address p.
+__device__ __forceinline__ float ld_cluster(const float *p, uint32_t rank) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(p, rank)) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_as(void *out, int64_t i, float v, int dtype) {
+    if (dtype == MOE_F32) static_cast<float *>(out)[i] = v;
+    else if (dtype == MOE_BF16) static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half *>(out)[i] = __float2half_rn(v);
+}
+
+template <bool FP8, bool GATED, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+    skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
+                  const __grid_constant__ CUtensorMap tmW1, Params p) {
+    constexpr int kStages = stages<NT>();
+    constexpr int kXStage = NT * 128;
+    constexpr int kBuf = NT < 32 ? 32 : NT;                // TMEM columns of one accumulator
+    constexpr int kTmemCols = FP8 ? 2 * kBuf : kBuf;
+    constexpr int kK = FP8 ? 128 : 64;                     // elements of a K block
+    constexpr int kOutRows = GATED ? kRows / 2 : kRows;
+    static_assert(kStages * (kWStage + kXStage) >= kRows * NT * 4, "the sums fit over the ring");
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sW = smem, *sX = sW + kStages * kWStage;
+    float *scales = reinterpret_cast<float *>(sX + kStages * kXStage);   // fp8: [4 warps][2][NT]
+    Ctrl *ctrl = reinterpret_cast<Ctrl *>(scales + (FP8 ? 4 * 2 * NT : 0));
+    float *sums = reinterpret_cast<float *>(smem);         // [NT][128], over the ring once it is drained
+    volatile int *abort = &ctrl->abort;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctrl->full[s], 1);
+            mbar_init(&ctrl->empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&ctrl->tfull[a], 1);
+            mbar_init(&ctrl->tempty[a], 4);
+        }
+        ctrl->abort = 0;
+        fence_barrier_init();
+    }
+    if (warp == kMmaWarp) tmem_alloc(&ctrl->tmem_base, kTmemCols);
+    if (warp == kTmaWarp && lane == 0) {
+        prefetch_tmap(&tmX);
+        prefetch_tmap(&tmW0);
+        if (GATED) prefetch_tmap(&tmW1);
+    }
+    if (!p.early) pdl_wait();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // early: only the producer goes ahead of the previous kernel's completion
+    if (warp != kTmaWarp) {
+        if (p.early) pdl_wait();
+        pdl_launch_dependents();
+    }
+
+    const uint32_t tmem = ctrl->tmem_base;
+    const int S = p.S, rank = S > 1 ? (int)cluster_rank() : 0;
+    const int tile = blockIdx.x / S, tt = tile / p.mt, m = tile - tt * p.mt;
+    const int t0 = tt * NT, n0 = m * kOutRows;
+    const int k0 = (int)((int64_t)p.kb * rank / S), k1 = (int)((int64_t)p.kb * (rank + 1) / S), nk = k1 - k0;
+
+    if (warp == kTmaWarp) {
+        if (lane == 0) {
+            const uint64_t policy = l2_evict_first_policy();   // a weight is read by this CTA only, or soon by few
+            auto weights = [&](int s, int kb) {
+                uint8_t *w = sW + s * kWStage;
+                const int k = (k0 + kb) * kK;
+                if constexpr (GATED) {
+                    tma_load_2d_hint(&tmW0, w, &ctrl->full[s], k, n0, policy);
+                    tma_load_2d_hint(&tmW1, w + kWStage / 2, &ctrl->full[s], k, n0, policy);
+                } else {
+                    tma_load_2d_hint(&tmW0, w, &ctrl->full[s], k, n0, policy);
+                }
+            };
+            auto tokens = [&](int s, int kb) {
+                tma_load_2d(&tmX, sX + s * kXStage, &ctrl->full[s], (k0 + kb) * kK, t0);
+            };
+            const int head = min(nk, kStages);
+            for (int kb = 0; kb < head; ++kb) {
+                mbar_expect_tx(&ctrl->full[kb], kWStage + kXStage);
+                weights(kb, kb);
+            }
+            if (p.early) pdl_wait();
+            for (int kb = 0; kb < head; ++kb) tokens(kb, kb);
+            bool ok = true;
+            int kb = head;
+            for (; kb < nk; ++kb) {
+                const int s = kb % kStages;
+                if (!wait_bar(&ctrl->empty[s], ((kb / kStages) & 1) ^ 1, abort, p.err)) {
+                    ok = false;
+                    break;
+                }
+                mbar_expect_tx(&ctrl->full[s], kWStage + kXStage);
+                weights(s, kb);
+                tokens(s, kb);
+            }
+            if (!ok) {
+                // aborting: let the copies land before the CTA leaves
+                for (int j = kb > kStages ? kb - kStages : 0; j < kb; ++j) {
+                    const uint64_t c = globaltimer();
+                    while (!mbar_try_wait(&ctrl->full[j % kStages], (j / kStages) & 1) && globaltimer() - c < 100000000ull) {
+                    }
+                }
+            }
+        }
+    } else if (warp == kMmaWarp) {
+        if (lane == 0) {
+            const uint32_t fmt = FP8 ? 0u : p.fmt;
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(NT >> 3) << 17) |
+                                   ((uint32_t)(kRows >> 4) << 24);
+            bool ok = true;
+            for (int kb = 0; kb < nk; ++kb) {
+                const int s = kb % kStages;
+                const uint32_t d = tmem + (FP8 ? (kb & 1) * kBuf : 0);
+                if (FP8 && !wait_bar(&ctrl->tempty[kb & 1], ((kb >> 1) & 1) ^ 1, abort, p.err)) {
+                    ok = false;
+                    break;
+                }
+                if (!wait_bar(&ctrl->full[s], (kb / kStages) & 1, abort, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint64_t ad = smem_desc(sW + s * kWStage), bd = smem_desc(sX + s * kXStage);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk) {
+                    if constexpr (FP8) mma_fp8(d, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
+                    else mma<__nv_bfloat16>(d, ad + 2 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
+                }
+                mma_commit(&ctrl->empty[s]);
+                if (FP8) mma_commit(&ctrl->tfull[kb & 1]);
+            }
+            // the sums are complete; aborting: this arrival follows whatever was issued
+            if (!FP8 || !ok) mma_commit(&ctrl->tfull[0]);
+        }
+    } else {
+        const uint32_t tb = tmem + ((uint32_t)(warp * 32) << 16);
+        const int row = warp * 32 + lane;
+        if constexpr (FP8) {
+            float acc[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) acc[t] = 0.f;
+            float *mine = scales + warp * 2 * NT;
+            const float *sw = p.sw + (int64_t)(n0 / kRows) * p.kb + k0;
+            // the scales of a block, one token a lane, requested one block ahead
+            constexpr int kPer = (NT + 31) / 32;
+            float next[kPer], next_w = 0.f;
+            auto ask = [&](int kb) {
+                if (kb >= nk) return;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j) {
+                    const int t = min(t0 + j * 32 + lane, p.T - 1);   // rows past the end are not stored
+                    next[j] = __ldg(p.sx + (int64_t)t * p.kb + k0 + kb);
+                }
+                next_w = __ldg(sw + kb);
+            };
+            ask(0);
+            for (int kb = 0; kb < nk; ++kb) {
+                float *sc = mine + (kb & 1) * NT;
+#pragma unroll
+                for (int j = 0; j < kPer; ++j)
+                    if (j * 32 + lane < NT) sc[j * 32 + lane] = next[j] * next_w;
+                __syncwarp();
+                ask(kb + 1);
+                if (!wait_bar(&ctrl->tfull[kb & 1], (kb >> 1) & 1, abort, p.err)) break;
+                tc_fence_after();
+                const uint32_t at = tb + (kb & 1) * kBuf;
+#pragma unroll
+                for (int q = 0; q < NT; q += 16) {
+                    float v[16];
+                    tmem_ld16(at + q, v);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int z = 0; z < 16; z += 4) {
+                        const float4 f = *reinterpret_cast<const float4 *>(sc + q + z);
+                        acc[q + z] = fmaf(v[z], f.x, acc[q + z]);
+                        acc[q + z + 1] = fmaf(v[z + 1], f.y, acc[q + z + 1]);
+                        acc[q + z + 2] = fmaf(v[z + 2], f.z, acc[q + z + 2]);
+                        acc[q + z + 3] = fmaf(v[z + 3], f.w, acc[q + z + 3]);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctrl->tempty[kb & 1]);
+            }
+            // every block product has been read, so every load of the ring has
+            // been consumed -- by all four warps, once they have met
+            asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+            for (int t = 0; t < NT; ++t) sums[t * kRows + row] = acc[t];
+        } else {
+            wait_bar(&ctrl->tfull[0], 0, abort, p.err);
+            tc_fence_after();
+#pragma unroll
+            for (int q = 0; q < NT; q += 16) {
+                float v[16];
+                tmem_ld16(tb + q, v);
+                tmem_wait_ld();
+#pragma unroll
+                for (int z = 0; z < 16; ++z) sums[(q + z) * kRows + row] = v[z];
+            }
+            tc_fence_before();
+        }
+    }
+    if (S > 1) cluster_sync_all();
+    else __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
+    if (warp == kTmaWarp) pdl_wait();   // (its other lanes) before anything is written
+
+    // 1 / S of the tile's rows, over the S ranges in their order
+    const int per = kOutRows / S, r0 = rank * per, nt = min(NT, p.T - t0);
+    for (int i = threadIdx.x; i < per * nt; i += kThreads) {
+        const int t = i / per, r = r0 + i - t * per, n = n0 + r;
+        if (n >= p.N) continue;
+        const float *at = sums + t * kRows + r;
+        float u = 0.f, v = 0.f;
+        for (int q = 0; q < S; ++q) {
+            u += S > 1 ? ld_cluster(at, q) : at[0];
+            if (GATED) v += S > 1 ? ld_cluster(at + kOutRows, q) : at[kOutRows];
+        }
+        const int64_t o = (int64_t)(t0 + t) * p.N + n;
+        if constexpr (GATED) {
+            if (p.pre) {
+                const int64_t b = (int64_t)(t0 + t) * 2 * p.N + n;
+                store_as(p.pre, b, u, p.out_dtype);
+                store_as(p.pre, b + p.N, v, p.out_dtype);
+            }
+            u = (p.act == MOE_ACT_SILU ? silu_f(u) : ffn::gelu_tanh_f(u)) * v;
+        }
+        store_as(p.out, o, u, p.out_dtype);
+    }
+    if (S > 1) cluster_sync_all();   // the others may still be reading this CTA's sums
+}
+
+// ------------------------------------------------------------------ host side
+
+// Rows of 128-byte K blocks (128-byte swizzle), box_rows of them a box.
+bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_t cols, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)cols * esize};
+    cuuint32_t box[2] = {(cuuint32_t)(128 / esize), box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool FP8, bool GATED, int NT>
+cudaError_t launch_nt(const Product &g, cudaStream_t s) {
+    constexpr int kOutRows = GATED ? kRows / 2 : kRows;
+    const int esize = FP8 ? 1 : 2;
+    CUtensorMap mX, mW0, mW1;
+    if (!make_rows(&mX, g.x, esize, g.T, g.K, NT) || !make_rows(&mW0, g.w0, esize, g.N, g.K, kOutRows))
+        return cudaErrorInvalidValue;
+    mW1 = mW0;
+    if (GATED && !make_rows(&mW1, g.w1, esize, g.N, g.K, kOutRows)) return cudaErrorInvalidValue;
+    Params p{};
+    p.T = (int)g.T;
+    p.N = g.N;
+    p.kb = (int)(((int64_t)g.K * esize + 127) / 128);
+    p.mt = (g.N + kOutRows - 1) / kOutRows;
+    p.sx = g.sx;
+    p.sw = g.sw;
+    p.out = g.out;
+    p.out_dtype = g.out_dtype;
+    p.pre = g.pre;
+    p.act = g.act;
+    p.fmt = g.bf16 ? 1u : 0u;
+    p.early = g.early;
+    p.err = g.err;
+    const int tiles = p.mt * (int)((g.T + NT - 1) / NT);
+    // K ranges: as many as fill two CTAs on every SM, with four K blocks each at least
+    p.S = 1;
+    while (p.S < 8 && tiles * p.S * 2 <= 2 * num_sms() && p.kb >= 8 * p.S) p.S *= 2;
+    const size_t smem = 1024 + (size_t)stages<NT>() * (kWStage + NT * 128) + (FP8 ? 4 * 2 * NT * 4 : 0) + sizeof(Ctrl);
+    auto kern = skinny_kernel<FP8, GATED, NT>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.S));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)p.S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = pdl_enabled() ? 2 : 1;
+    e = cudaLaunchKernelEx(&cfg, kern, mX, mW0, mW1, p);
+    note_launch();
+    return e;
+}
+
+template <bool FP8, bool GATED>
+cudaError_t launch_form(const Product &g, cudaStream_t s) {
+    if (g.T <= 16) return launch_nt<FP8, GATED, 16>(g, s);
+    if (g.T <= 32) return launch_nt<FP8, GATED, 32>(g, s);
+    if (g.T <= 64) return launch_nt<FP8, GATED, 64>(g, s);
+    return launch_nt<FP8, GATED, 128>(g, s);
+}
+
+}  // namespace
+
+bool wants(int64_t T, int N, int K) { return T <= 256; }
+
+cudaError_t launch(const Product &g, cudaStream_t s) {
+    if (g.fp8) return launch_form<true, false>(g, s);
+    return g.gated ? launch_form<false, true>(g, s) : launch_form<false, false>(g, s);
+}
+
+}  // namespace skinny
+}  // namespace moe
