@@ -75,17 +75,44 @@ __device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint
         ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
         : "memory");
 }
-// A float of the shared memory of CTA `rank` of the cluster, at this CTA's address p.
-__device__ __forceinline__ float ld_cluster(const float *p, uint32_t rank) {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(mapa_shared(p, rank)) : "memory");
+// Four floats of the shared memory of CTA `rank` of the cluster, at this CTA's address p.
+__device__ __forceinline__ float4 ld_cluster4(const float *p, uint32_t rank) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(mapa_shared(p, rank))
+                 : "memory");
     return v;
 }
+// The sum over the S CTAs of the cluster of the four floats at p.
+__device__ __forceinline__ void add_ranges(const float *p, int S, float (&o)[4]) {
+    float4 f[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        if (q < S) f[q] = S > 1 ? ld_cluster4(p, q) : *reinterpret_cast<const float4 *>(p);
+    o[0] = f[0].x;
+    o[1] = f[0].y;
+    o[2] = f[0].z;
+    o[3] = f[0].w;
+#pragma unroll
+    for (int q = 1; q < 8; ++q)
+        if (q < S) {
+            o[0] += f[q].x;
+            o[1] += f[q].y;
+            o[2] += f[q].z;
+            o[3] += f[q].w;
+        }
+}
 
-__device__ __forceinline__ void store_as(void *out, int64_t i, float v, int dtype) {
-    if (dtype == MOE_F32) static_cast<float *>(out)[i] = v;
-    else if (dtype == MOE_BF16) static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
-    else static_cast<__half *>(out)[i] = __float2half_rn(v);
+// Elements i .. i + 3 (i a multiple of 4) of a row-major tensor.
+__device__ __forceinline__ void store4(void *out, int64_t i, const float (&v)[4], int dtype) {
+    if (dtype == MOE_F32) {
+        *reinterpret_cast<float4 *>(static_cast<float *>(out) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+        const uint32_t fmt = dtype == MOE_BF16 ? 1u : 0u;
+        *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + i) =
+            make_uint2(ffn::pack2(v[0], v[1], fmt), ffn::pack2(v[2], v[3], fmt));
+    }
 }
 
 template <bool FP8, bool GATED, int NT>
@@ -292,27 +319,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
     if (warp == kTmaWarp) pdl_wait();   // (its other lanes) before anything is written
 
-    // 1 / S of the tile's rows, over the S ranges in their order
-    const int per = kOutRows / S, r0 = rank * per, nt = min(NT, p.T - t0);
-    for (int i = threadIdx.x; i < per * nt; i += kThreads) {
-        const int t = i / per, r = r0 + i - t * per, n = n0 + r;
-        if (n >= p.N) continue;
+    // 1 / S of the tile's rows, four of one token a step, over the S ranges in
+    // their order (all S reads are in flight before the first is added)
+    const int per = kOutRows / S, quads = per / 4, r0 = rank * per, nt = min(NT, p.T - t0);
+    for (int i = threadIdx.x; i < quads * nt; i += kThreads) {
+        const int t = i / quads, r = r0 + 4 * (i - t * quads), n = n0 + r;
+        if (n >= p.N) continue;   // N is a multiple of 8: four rows are in or out together
         const float *at = sums + t * kRows + r;
-        float u = 0.f, v = 0.f;
-        for (int q = 0; q < S; ++q) {
-            u += S > 1 ? ld_cluster(at, q) : at[0];
-            if (GATED) v += S > 1 ? ld_cluster(at + kOutRows, q) : at[kOutRows];
-        }
+        float u[4], v[4];
+        add_ranges(at, S, u);
+        if (GATED) add_ranges(at + kOutRows, S, v);
         const int64_t o = (int64_t)(t0 + t) * p.N + n;
         if constexpr (GATED) {
             if (p.pre) {
                 const int64_t b = (int64_t)(t0 + t) * 2 * p.N + n;
-                store_as(p.pre, b, u, p.out_dtype);
-                store_as(p.pre, b + p.N, v, p.out_dtype);
+                store4(p.pre, b, u, p.out_dtype);
+                store4(p.pre, b + p.N, v, p.out_dtype);
             }
-            u = (p.act == MOE_ACT_SILU ? silu_f(u) : ffn::gelu_tanh_f(u)) * v;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                u[j] = (p.act == MOE_ACT_SILU ? silu_f(u[j]) : ffn::gelu_tanh_f(u[j])) * v[j];
         }
-        store_as(p.out, o, u, p.out_dtype);
+        store4(p.out, o, u, p.out_dtype);
     }
     if (S > 1) cluster_sync_all();   // the others may still be reading this CTA's sums
 }
