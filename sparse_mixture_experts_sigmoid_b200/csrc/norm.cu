@@ -24,6 +24,7 @@
 // partial row each, and a second kernel adds the partial rows.  Every order is
 // fixed, so repeated calls give the same bits.
 #include <algorithm>
+#include <type_traits>
 
 #include <cuda_fp16.h>
 
@@ -46,119 +47,144 @@ template <> __device__ __forceinline__ float el_from<float>(float v) { return v;
 template <> __device__ __forceinline__ __nv_bfloat16 el_from<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half el_from<__half>(float v) { return __float2half_rn(v); }
 
-// The elements of a row that one thread holds: VPT words of E elements.  With
-// VEC word j is the 16-byte word j * G + i of the row (i the thread in its
-// group of G); without it (widths or addresses that are not whole words)
-// element e of word j is the row's element (j * E + e) * G + i, so that a
-// warp's loads are still of consecutive elements.
-template <typename T, int VPT, bool VEC>
-struct Row {
-    static constexpr int E = kElems<T>;
-    union Word {
-        uint4 w;
-        T e[E];
-    };
-    Word v[VPT];
-
-    __device__ __forceinline__ static int column(int i, int G, int j, int e) {
-        return VEC ? (j * G + i) * E + e : (j * E + e) * G + i;
-    }
-    __device__ __forceinline__ void load_word(const T *p, int i, int G, int d, int j) {
-        if constexpr (VEC) {
-            const int c = column(i, G, j, 0);
-            v[j].w = c < d ? *reinterpret_cast<const uint4 *>(p + c) : make_uint4(0, 0, 0, 0);
+// A word's elements as fp32, and back (rounded to nearest), two at a time.
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 &u, float (&o)[kElems<T>]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 4) {
+            o[k] = __uint_as_float(w[k]);
+        } else if constexpr (std::is_same_v<T, __half>) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+            o[2 * k] = f.x;
+            o[2 * k + 1] = f.y;
         } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int c = column(i, G, j, e);
-                v[j].e[e] = c < d ? p[c] : el_from<T>(0.f);
-            }
-        }
-    }
-    __device__ __forceinline__ void store_word(T *p, int i, int G, int d, int j) const {
-        if constexpr (VEC) {
-            const int c = column(i, G, j, 0);
-            if (c < d) *reinterpret_cast<uint4 *>(p + c) = v[j].w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int c = column(i, G, j, e);
-                if (c < d) p[c] = v[j].e[e];
-            }
-        }
-    }
-    __device__ __forceinline__ void load(const T *p, int i, int G, int d) {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) load_word(p, i, G, d, j);
-    }
-    __device__ __forceinline__ void store(T *p, int i, int G, int d) const {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) store_word(p, i, G, d, j);
-    }
-    __device__ __forceinline__ float get(int j, int e) const { return el_f32(v[j].e[e]); }
-    __device__ __forceinline__ void set(int j, int e, float f) { v[j].e[e] = el_from<T>(f); }
-};
-
-// Word j of the weight or bias vector (of type T, or fp32 when wf32) for this
-// thread's columns, as fp32.
-template <typename T, bool VEC>
-__device__ __forceinline__ void load_param(const void *p, bool wf32, int i, int G, int j, int d,
-                                           float (&o)[kElems<T>]) {
-    constexpr int E = kElems<T>;
-    if constexpr (VEC) {
-        const int c = (j * G + i) * E;
-        if (c >= d) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = 0.f;
-        } else if (wf32) {
-#pragma unroll
-            for (int q = 0; q < E / 4; ++q) {
-                const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c) + q);
-                o[4 * q] = f.x;
-                o[4 * q + 1] = f.y;
-                o[4 * q + 2] = f.z;
-                o[4 * q + 3] = f.w;
-            }
-        } else {
-            union {
-                uint4 w;
-                T e[E];
-            } u;
-            u.w = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + c));
-#pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = el_f32(u.e[e]);
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int c = (j * E + e) * G + i;
-            o[e] = c >= d ? 0.f : (wf32 ? static_cast<const float *>(p)[c] : el_f32(static_cast<const T *>(p)[c]));
+            o[2 * k] = __uint_as_float(w[k] << 16);
+            o[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
         }
     }
 }
+template <typename T>
+__device__ __forceinline__ uint4 pack(const float (&v)[kElems<T>]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        if constexpr (sizeof(T) == 4) {
+            w[k] = __float_as_uint(v[k]);
+        } else if constexpr (std::is_same_v<T, __half>) {
+            const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t *>(&h);
+        } else {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+            w[k] = *reinterpret_cast<const uint32_t *>(&h);
+        }
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The 16-byte words of a row that one thread holds: word j * G + i of the row
+// (i the thread in its group of G).  A row of a width that is not a multiple of
+// E starts `shift` elements into an aligned word; its words are counted from
+// there (SHIFT), the first and last are partly the row's, and what lies outside
+// the row is neither read nor written.  A group takes rows whose distance is a
+// multiple of E, so that its shift stays the same.
+template <typename T, int VPT, bool SHIFT>
+struct Row {
+    static constexpr int E = kElems<T>;
+    uint4 v[VPT];
+
+    // column of element 0 of word j (negative in the first word of a shifted row)
+    __device__ __forceinline__ static int first(int i, int G, int j, int shift) {
+        return (j * G + i) * E - (SHIFT ? shift : 0);
+    }
+    // p: the row's first element
+    __device__ __forceinline__ void load_word(const T *p, int i, int G, int d, int shift, int j) {
+        const int c = first(i, G, j, shift);
+        if (SHIFT ? c >= 0 && c + E <= d : c < d) {
+            v[j] = *reinterpret_cast<const uint4 *>(p + c);
+        } else {
+            v[j] = make_uint4(0, 0, 0, 0);
+            if constexpr (SHIFT) {
+                T e[E];
+#pragma unroll
+                for (int k = 0; k < E; ++k) e[k] = c + k >= 0 && c + k < d ? p[c + k] : el_from<T>(0.f);
+                v[j] = *reinterpret_cast<const uint4 *>(e);
+            }
+        }
+    }
+    __device__ __forceinline__ void load(const T *p, int i, int G, int d, int shift) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) load_word(p, i, G, d, shift, j);
+    }
+    __device__ __forceinline__ static void store_word(T *p, int i, int G, int d, int shift, int j, const uint4 &w) {
+        const int c = first(i, G, j, shift);
+        if (SHIFT ? c >= 0 && c + E <= d : c < d) {
+            *reinterpret_cast<uint4 *>(p + c) = w;
+        } else if constexpr (SHIFT) {
+            const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+            for (int k = 0; k < E; ++k)
+                if (c + k >= 0 && c + k < d) p[c + k] = e[k];
+        }
+    }
+};
 
 template <typename T>
 __device__ __forceinline__ float param(const void *p, bool wf32, int c) {
     return wf32 ? __ldg(static_cast<const float *>(p) + c) : el_f32(static_cast<const T *>(p)[c]);
 }
+// E elements of the weight or bias vector (of type T, or fp32 when wf32) from
+// column c, as fp32; zeros outside the row.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void load_param(const void *p, bool wf32, int c, int d, float (&o)[kElems<T>]) {
+    constexpr int E = kElems<T>;
+    if constexpr (SHIFT) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = c + e >= 0 && c + e < d ? param<T>(p, wf32, c + e) : 0.f;
+    } else if (c >= d) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = 0.f;
+    } else if (wf32) {
+#pragma unroll
+        for (int q = 0; q < E / 4; ++q) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c) + q);
+            o[4 * q] = f.x;
+            o[4 * q + 1] = f.y;
+            o[4 * q + 2] = f.z;
+            o[4 * q + 3] = f.w;
+        }
+    } else {
+        unpack<T>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + c)), o);
+    }
+}
 
-// Sums over the W warps of a row's group.  `slot` is the group's buffer of
-// 2 x W values of this type, used in turn: a warp writes half `turn` again
-// only after a barrier that every warp reaches after it has read that half.
+__device__ __forceinline__ float add_of(float a, float b) { return a + b; }
+__device__ __forceinline__ float2 add_of(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
+__device__ __forceinline__ float shfl_of(float v, int o) { return __shfl_xor_sync(0xffffffffu, v, o); }
+__device__ __forceinline__ float2 shfl_of(float2 v, int o) {
+    return make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o));
+}
+
+// Sums over the threads of a group of W warps (at most 16; w: this thread's
+// warp in it), in a fixed order.  `slot` is the group's buffer of 2 x 16 values
+// of this type, used in turn: a warp writes half `turn` again only after a
+// barrier that every warp reaches after it has read that half.
 template <typename V>
-__device__ __forceinline__ V group_sum(V v, V *slot, int &turn, int W, int bar, V (*add)(V, V)) {
+__device__ __forceinline__ V group_sum(V v, V *slot, int &turn, int w, int W, int bar) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = add_of(v, shfl_of(v, o));
     if (W == 1) return v;
-    V *s = slot + turn * W;
-    turn ^= 1;
-    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) % W;
+    V *s = slot + turn;
+    turn ^= 16;
+    const int lane = threadIdx.x & 31;
     if (lane == 0) s[w] = v;
     asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(W * 32) : "memory");
-    V r = s[0];
-    for (int k = 1; k < W; ++k) r = add(r, s[k]);
-    return r;
+    v = (lane & 15) < W ? s[lane & 15] : V{};
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) v = add_of(v, shfl_of(v, o));
+    return v;
 }
-__device__ __forceinline__ float add1(float a, float b) { return a + b; }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return make_float2(a.x + b.x, a.y + b.y); }
 
 struct NormFwd {
     const void *x, *residual, *weight, *bias;
@@ -170,72 +196,101 @@ struct NormFwd {
     float eps;
 };
 
-template <typename T, int VPT, bool VEC>
-__global__ void __launch_bounds__(VPT == 3 ? 256 : 512) norm_fwd_kernel(NormFwd a) {
+// Registers: three blocks of 256 threads on an SM where the rows are whole words
+// of up to two a thread, so that enough loads are in flight.
+template <int VPT, bool SHIFT, int THREADS>
+constexpr int kFwdBlocks = THREADS == 256 && !SHIFT ? (VPT <= 2 ? 3 : 2) : 1;
+
+template <typename T, int VPT, bool SHIFT, int THREADS>
+__global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm_fwd_kernel(NormFwd a) {
     constexpr int E = kElems<T>;
-    __shared__ float red[2 * kMaxWarps];
+    using R = Row<T, VPT, SHIFT>;
+    __shared__ float red[8 * 32];
     const int W = a.W, G = W * 32, d = a.d;
-    const int group = threadIdx.x / G, i = threadIdx.x % G;
-    float *slot = red + 2 * W * group;
+    const int group = threadIdx.x / G, i = threadIdx.x - group * G, w = i >> 5;
+    float *slot = red + 32 * group;
     int turn = 0;
-    const float df = (float)d;
-    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
+    const float df = (float)d, inv = 1.f / df;
     const int64_t step = (int64_t)gridDim.x * a.groups;
     int64_t r = (int64_t)blockIdx.x * a.groups + group;
+    const int shift = SHIFT ? (int)(r * d % E) : 0;
+    const bool add = a.residual != nullptr, bias = a.bias != nullptr, wf32 = a.wf32;
+    const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
+    int64_t o = r * d;                  // the row's first element
+    const int64_t jump = step * d;
     pdl_wait();
     pdl_launch_dependents();
-    Row<T, VPT, VEC> nx, nr;
+    R nx, nr;
     if (r < a.T) {
-        nx.load(x + r * d, i, G, d);
-        if (res) nr.load(res + r * d, i, G, d);
+        nx.load(x + o, i, G, d, shift);
+        if (add) nr.load(res + o, i, G, d, shift);
     }
     for (; r < a.T; r += step) {
-        Row<T, VPT, VEC> c = nx;
-        if (res) {
+        float c[VPT][E];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
+        for (int j = 0; j < VPT; ++j) unpack<T>(nx.v[j], c[j]);
+        if (add) {
 #pragma unroll
-                for (int e = 0; e < E; ++e) c.set(j, e, c.get(j, e) + nr.get(j, e));
+            for (int j = 0; j < VPT; ++j) {
+                float z[E];
+                unpack<T>(nr.v[j], z);
+#pragma unroll
+                for (int e = 0; e < E; ++e) c[j][e] += z[e];
+                const uint4 u = pack<T>(c[j]);
+                R::store_word(static_cast<T *>(a.h) + o, i, G, d, shift, j, u);
+                unpack<T>(u, c[j]);   // the norm is of the rows as they are stored
+            }
         }
         if (r + step < a.T) {
-            nx.load(x + (r + step) * d, i, G, d);
-            if (res) nr.load(res + (r + step) * d, i, G, d);
+            nx.load(x + o + jump, i, G, d, shift);
+            if (add) nr.load(res + o + jump, i, G, d, shift);
         }
-        if (res) c.store(static_cast<T *>(a.h) + r * d, i, G, d);
+        // elements outside the row are zeros in every sum
         float mean = 0.f;
         if (a.layer) {
             float s = 0.f;
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int e = 0; e < E; ++e) s += c.get(j, e);
-            mean = group_sum(warp_sum(s), slot, turn, W, 1 + group, add1) / df;
+                for (int e = 0; e < E; ++e) s += c[j][e];
+            s = group_sum(s, slot, turn, w, W, 1 + group);
+            mean = s * inv;
+            mean = fmaf(fmaf(-mean, df, s), inv, mean);   // the quotient s / d, rounded once
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int c0 = R::first(i, G, j, shift);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    c[j][e] = (SHIFT ? c0 + e >= 0 && c0 + e < d : c0 < d) ? c[j][e] - mean : 0.f;
+            }
         }
         float q = 0.f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float z = Row<T, VPT, VEC>::column(i, G, j, e) < d ? c.get(j, e) - mean : 0.f;
-                q = fmaf(z, z, q);
-            }
-        const float rstd = rsqrtf(group_sum(warp_sum(q), slot, turn, W, 1 + group, add1) / df + a.eps);
+            for (int e = 0; e < E; ++e) q = fmaf(c[j][e], c[j][e], q);
+        const float rstd = rsqrtf(group_sum(q, slot, turn, w, W, 1 + group) * inv + a.eps);
         if (i == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
         }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            float w[E], b[E];
-            load_param<T, VEC>(a.weight, a.wf32, i, G, j, d, w);
-            if (a.bias) load_param<T, VEC>(a.bias, a.wf32, i, G, j, d, b);
+            const int c0 = R::first(i, G, j, shift);
+            float g[E];
+            load_param<T, SHIFT>(a.weight, wf32, c0, d, g);
+            if (bias) {
+                float b[E];
+                load_param<T, SHIFT>(a.bias, wf32, c0, d, b);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float z = (c.get(j, e) - mean) * rstd;
-                c.set(j, e, a.bias ? fmaf(z, w[e], b[e]) : z * w[e]);
+                for (int e = 0; e < E; ++e) c[j][e] = fmaf(c[j][e] * rstd, g[e], b[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < E; ++e) c[j][e] = c[j][e] * rstd * g[e];
             }
+            R::store_word(static_cast<T *>(a.y) + o, i, G, d, shift, j, pack<T>(c[j]));
         }
-        c.store(static_cast<T *>(a.y) + r * d, i, G, d);
+        o += jump;
     }
 }
 
@@ -249,111 +304,133 @@ struct NormBwd {
     bool wf32, want_db;
 };
 
-template <typename T, int VPT, bool VEC>
-__global__ void __launch_bounds__(VPT == 3 ? 256 : 512) norm_bwd_kernel(NormBwd a) {
-    // up to three words a thread are held between the two passes over a row
-    // (and the next row's requested); of wider rows only the gradients' sums
-    // stay in registers, and the second pass reads the row again, from L1
-    constexpr bool HOLD = VPT <= 3;
+// Up to two words a thread, a row's words are held between its two passes and
+// the next row's are requested meanwhile; of wider rows only the gradients' sums
+// stay in registers, and the second pass reads the row again, from L1.
+template <typename T, int VPT, bool SHIFT, bool DB, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) norm_bwd_kernel(NormBwd a) {
+    constexpr bool HOLD = VPT <= 2;
     constexpr int E = kElems<T>;
-    __shared__ float2 red[2 * kMaxWarps];
+    using R = Row<T, VPT, SHIFT>;
+    __shared__ float2 red[8 * 32];
     extern __shared__ float cols[];     // groups > 1: [2, d]
     const int W = a.W, G = W * 32, d = a.d;
-    const int group = threadIdx.x / G, i = threadIdx.x % G;
-    float2 *slot = red + 2 * W * group;
+    const int group = threadIdx.x / G, i = threadIdx.x - group * G, wi = i >> 5;
+    float2 *slot = red + 32 * group;
     int turn = 0;
-    const float df = (float)d;
-    const T *h = static_cast<const T *>(a.h), *dy = static_cast<const T *>(a.dy), *dh = static_cast<const T *>(a.dh);
+    const float inv = 1.f / (float)d;
     const int64_t step = (int64_t)gridDim.x * a.groups;
     int64_t r = (int64_t)blockIdx.x * a.groups + group;
-    float dw[VPT][E], db[VPT][E];
+    const int shift = SHIFT ? (int)(r * d % E) : 0;
+    const bool layer = a.mean != nullptr, more = a.dh != nullptr, wf32 = a.wf32;
+    const T *h = static_cast<const T *>(a.h), *dy = static_cast<const T *>(a.dy), *dh = static_cast<const T *>(a.dh);
+    int64_t o = r * d;                  // the row's first element
+    const int64_t jump = step * d;
+    float dw[VPT][E], db[DB ? VPT : 1][E];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) dw[j][e] = db[j][e] = 0.f;
+        for (int e = 0; e < E; ++e) {
+            dw[j][e] = 0.f;
+            if (DB) db[j][e] = 0.f;
+        }
     pdl_wait();
     pdl_launch_dependents();
-    Row<T, VPT, VEC> nh, ny;
-    if (HOLD && r < a.T) {
-        nh.load(h + r * d, i, G, d);
-        ny.load(dy + r * d, i, G, d);
+    R nh, ny;
+    float nm = 0.f, ns = 0.f;
+    if (r < a.T) {
+        if constexpr (HOLD) {
+            nh.load(h + o, i, G, d, shift);
+            ny.load(dy + o, i, G, d, shift);
+        }
+        if (layer) nm = a.mean[r];
+        ns = a.rstd[r];
     }
     for (; r < a.T; r += step) {
-        Row<T, VPT, VEC> ch, cy, cd;
+        R ch, cy, cd;
+        const float mean = nm, rstd = ns;
         if constexpr (HOLD) {
             ch = nh;
             cy = ny;
-            if (dh) cd.load(dh + r * d, i, G, d);
+            if (more) cd.load(dh + o, i, G, d, shift);
+            if (r + step < a.T) {
+                nh.load(h + o + jump, i, G, d, shift);
+                ny.load(dy + o + jump, i, G, d, shift);
+            }
         }
-        if (HOLD && r + step < a.T) {
-            nh.load(h + (r + step) * d, i, G, d);
-            ny.load(dy + (r + step) * d, i, G, d);
+        if (r + step < a.T) {
+            if (layer) nm = a.mean[r + step];
+            ns = a.rstd[r + step];
         }
-        const float mean = a.mean ? a.mean[r] : 0.f, rstd = a.rstd[r];
         float2 s = make_float2(0.f, 0.f);   // sums of g and g * xhat
+        // elements outside the row have dy = 0: they add nothing to any sum
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            float w[E];
-            load_param<T, VEC>(a.weight, a.wf32, i, G, j, d, w);
+            float w[E], x[E], y[E];
+            load_param<T, SHIFT>(a.weight, wf32, R::first(i, G, j, shift), d, w);
             if constexpr (!HOLD) {
-                ch.load_word(h + r * d, i, G, d, j);
-                cy.load_word(dy + r * d, i, G, d, j);
+                ch.load_word(h + o, i, G, d, shift, j);
+                cy.load_word(dy + o, i, G, d, shift, j);
             }
+            unpack<T>(ch.v[j], x);
+            unpack<T>(cy.v[j], y);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                // columns past d hold dy = 0: they add nothing to any sum
-                const float xh = (ch.get(j, e) - mean) * rstd, y = cy.get(j, e);
-                const float g = y * w[e];
+                const float xh = (x[e] - mean) * rstd, g = y[e] * w[e];
                 s.x += g;
                 s.y = fmaf(g, xh, s.y);
-                dw[j][e] = fmaf(y, xh, dw[j][e]);
-                db[j][e] += y;
+                dw[j][e] = fmaf(y[e], xh, dw[j][e]);
+                if (DB) db[j][e] += y[e];
             }
         }
-        s.x = warp_sum(s.x);
-        s.y = warp_sum(s.y);
-        s = group_sum(s, slot, turn, W, 1 + group, add2);
-        const float c1 = a.mean ? s.x / df : 0.f, c2 = s.y / df;
+        s = group_sum(s, slot, turn, wi, W, 1 + group);
+        // dx = rstd g - rstd avg(g) - xhat rstd avg(g xhat)
+        const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * (s.y * inv);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            float w[E];
-            load_param<T, VEC>(a.weight, a.wf32, i, G, j, d, w);
+            float w[E], x[E], y[E];
+            load_param<T, SHIFT>(a.weight, wf32, R::first(i, G, j, shift), d, w);
             if constexpr (!HOLD) {
-                ch.load_word(h + r * d, i, G, d, j);
-                cy.load_word(dy + r * d, i, G, d, j);
-                if (dh) cd.load_word(dh + r * d, i, G, d, j);
+                ch.load_word(h + o, i, G, d, shift, j);
+                cy.load_word(dy + o, i, G, d, shift, j);
+                if (more) cd.load_word(dh + o, i, G, d, shift, j);
             }
+            unpack<T>(ch.v[j], x);
+            unpack<T>(cy.v[j], y);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float xh = (ch.get(j, e) - mean) * rstd;
-                const float g = rstd * (fmaf(cy.get(j, e), w[e], -c1) - xh * c2);
-                ch.set(j, e, dh ? g + cd.get(j, e) : g);
+            for (int e = 0; e < E; ++e)
+                x[e] = fmaf((x[e] - mean) * rstd, c2, fmaf(y[e] * w[e], rstd, c1));
+            if (more) {
+                unpack<T>(cd.v[j], y);
+#pragma unroll
+                for (int e = 0; e < E; ++e) x[e] += y[e];
             }
-            ch.store_word(static_cast<T *>(a.dx) + r * d, i, G, d, j);
+            R::store_word(static_cast<T *>(a.dx) + o, i, G, d, shift, j, pack<T>(x));
         }
+        o += jump;
     }
     if (!a.part) return;
     float *out = a.part + (int64_t)blockIdx.x * 2 * d;
     // the block's groups add their columns one after another
-    for (int g = 0; g < a.groups; ++g) {
-        if (group == g) {
+    for (int k = 0; k < a.groups; ++k) {
+        if (group == k) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const int c = Row<T, VPT, VEC>::column(i, G, j, e);
-                    if (c >= d) continue;
-                    float sw = dw[j][e], sb = db[j][e];
-                    if (g > 0) {
+                    const int c = R::first(i, G, j, shift) + e;
+                    if (c < 0 || c >= d) continue;
+                    float sw = dw[j][e], sb = DB ? db[j][e] : 0.f;
+                    if (k > 0) {
                         sw += cols[c];
-                        sb += cols[d + c];
+                        if (DB) sb += cols[d + c];
                     }
-                    if (g + 1 < a.groups) {
+                    if (k + 1 < a.groups) {
                         cols[c] = sw;
-                        cols[d + c] = sb;
+                        if (DB) cols[d + c] = sb;
                     } else {
                         out[c] = sw;
-                        if (a.want_db) out[d + c] = sb;
+                        if (DB) out[d + c] = sb;
                     }
                 }
         }
@@ -363,18 +440,20 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512) norm_bwd_kernel(NormBwd 
 
 // Any width and alignment: one block per row at a time, its columns strided
 // over the threads and read once per pass (from L1 or L2 after the first).
-// Serves the rows that do not fit the register kernels: widths or addresses
-// that are not whole 16-byte words, beyond kMaxWarps * 32 threads' elements.
+// Serves what the register kernels do not: tensors that do not start on a
+// 16-byte boundary, and the widest rows when they are not whole words.
 constexpr int kGenThreads = 512;
 
 template <typename V>
-__device__ __forceinline__ V block_sum(V v, V *s, V (*add)(V, V)) {
+__device__ __forceinline__ V block_sum(V v, V *s) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = add_of(v, shfl_of(v, o));
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     __syncthreads();   // the previous sum has been read
     if (lane == 0) s[w] = v;
     __syncthreads();
     V r = s[0];
-    for (int k = 1; k < kGenThreads / 32; ++k) r = add(r, s[k]);
+    for (int k = 1; k < kGenThreads / 32; ++k) r = add_of(r, s[k]);
     return r;
 }
 
@@ -397,14 +476,14 @@ __global__ void __launch_bounds__(kGenThreads) norm_fwd_general_kernel(NormFwd a
         if (a.layer) {
             float s = 0.f;
             for (int c = threadIdx.x; c < d; c += kGenThreads) s += el_f32(x[c]);
-            mean = block_sum(warp_sum(s), red, add1) / df;
+            mean = block_sum(s, red) / df;
         }
         float q = 0.f;
         for (int c = threadIdx.x; c < d; c += kGenThreads) {
             const float z = el_f32(x[c]) - mean;
             q = fmaf(z, z, q);
         }
-        const float rstd = rsqrtf(block_sum(warp_sum(q), red, add1) / df + a.eps);
+        const float rstd = rsqrtf(block_sum(q, red) / df + a.eps);
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
@@ -441,9 +520,7 @@ __global__ void __launch_bounds__(kGenThreads) norm_bwd_general_kernel(NormBwd a
             cols[c] = fmaf(y, xh, cols[c]);
             cols[d + c] += y;
         }
-        s.x = warp_sum(s.x);
-        s.y = warp_sum(s.y);
-        s = block_sum(s, red, add2);
+        s = block_sum(s, red);
         const float c1 = a.mean ? s.x / df : 0.f, c2 = s.y / df;
         for (int c = threadIdx.x; c < d; c += kGenThreads) {
             const float xh = (el_f32(h[c]) - mean) * rstd;
@@ -470,8 +547,10 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float *part, int
     pdl_wait();
     pdl_launch_dependents();
     float v = 0.f;
-    if (c < d)
+    if (c < d) {
+#pragma unroll 5
         for (int k = warp; k < parts; k += 32) v += p[(int64_t)k * 2 * d + c];
+    }
     s[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < d) {
@@ -484,70 +563,96 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float *part, int
 }
 
 // How a row is spread: VPT words per thread, W warps per row, `groups` rows
-// per block; vpt = 0 is the general kernel.  Whole words: a short row (up to
-// three words a lane) stays in one warp, which needs no barrier; a longer one
-// takes as many warps as hold it at two words a thread, at four (eight) where
-// more than 16 warps would be needed.  Single elements: as many warps as hold
-// the row at eight elements a thread, else the general kernel.
+// per block; vpt = 0 is the general kernel.  Of one, two and (forward) three
+// words a thread, the one that leaves the fewest words of its warps idle, and
+// of those the one with the fewest warps: one warp needs no barrier.  Four
+// (eight) words where more than 16 warps would be needed.
 struct Spread {
     int vpt, W, groups;
+    bool shift;
 };
-Spread spread(int d, int elems, bool vec) {
-    Spread s;
-    if (vec) {
-        const int words = (d + elems - 1) / elems;
-        if (words <= 96) {
-            s.vpt = (words + 31) / 32;
-            s.W = 1;
-        } else {
-            s.vpt = words <= 64 * kMaxWarps ? 2 : (words <= 128 * kMaxWarps ? 4 : 8);
-            s.W = (words + 32 * s.vpt - 1) / (32 * s.vpt);
-        }
+Spread spread(int d, int elems, bool aligned, bool forward) {
+    const bool shift = d % elems != 0;
+    const int words = (d + (shift ? elems - 1 : 0) + elems - 1) / elems;
+    const int most = (shift ? 2 : (elems == 4 ? 8 : 4)) * 32 * kMaxWarps;
+    if (!aligned || words > most) return Spread{0, kGenThreads / 32, 1, false};
+    Spread s{0, 0, 0, shift};
+    if (words > 64 * kMaxWarps) {
+        s.vpt = words <= 128 * kMaxWarps ? 4 : 8;
+        s.W = (words + 32 * s.vpt - 1) / (32 * s.vpt);
     } else {
-        s.vpt = 8 / elems;
-        s.W = (d + 255) / 256;
-        if (s.W > kMaxWarps) return Spread{0, kGenThreads / 32, 1};
+        for (int v = 1; v <= (forward && words <= 96 ? 3 : 2); ++v) {
+            const int w = (words + 32 * v - 1) / (32 * v);
+            if (w <= kMaxWarps && (!s.vpt || w * v <= s.W * s.vpt)) {
+                s.vpt = v;
+                s.W = w;
+            }
+        }
     }
     s.groups = std::max(1, 8 / s.W);
     return s;
 }
+// Blocks for T rows, `most` at most: the rows in flight a multiple of eight when
+// rows are shifted (see Row).
+int blocks_for(const Spread &s, int64_t T, int most) {
+    const int64_t want = (T + s.groups - 1) / s.groups;
+    if (want <= 8 || !s.shift) return (int)std::min<int64_t>(want, most);
+    return (int)std::min<int64_t>((want + 7) / 8 * 8, most / 8 * 8);
+}
 
 int elem_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
-// Blocks of the backward pass, and so partial rows of the weight's gradient:
-// two per SM, fewer when there are fewer rows.
-constexpr int kBwdBlocks = 296;
+// Blocks of the backward pass at most, and so partial rows of the weight's
+// gradient: three per SM.
+constexpr int kBwdBlocks = 444;
+
+// Blocks of `kern` that the SMs hold at a time: the kernels stride over the rows,
+// so more would only wait.
+template <typename K>
+int resident_blocks(K kern, int threads, size_t smem) {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, smem) != cudaSuccess || n < 1) n = 1;
+    return n * num_sms();
+}
+
+// Partial rows that the workspace has room for (blocks_for rounds up to eight).
+size_t part_rows(int64_t T) { return (size_t)std::min<int64_t>(kBwdBlocks, (T + 7) / 8 * 8); }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// The kernel for a type and spread (see spread()).
-template <typename T>
-auto fwd_kernel(int vpt, bool vec) -> void (*)(NormFwd) {
-    if (vpt == 0) return norm_fwd_general_kernel<T>;
-    if (!vec) return norm_fwd_kernel<T, 8 / kElems<T>, false>;
-    switch (vpt) {
-        case 1: return norm_fwd_kernel<T, 1, true>;
-        case 2: return norm_fwd_kernel<T, 2, true>;
-        case 3: return norm_fwd_kernel<T, 3, true>;
-        case 4: return norm_fwd_kernel<T, 4, true>;
-        default:   // fp32 only: a 16-bit row needs four words at most
-            if constexpr (sizeof(T) == 4) return norm_fwd_kernel<T, 8, true>;
-            else return nullptr;
+// The kernel for a type and spread (see spread()): blocks of up to 256 threads,
+// or of up to 512 for rows of more than eight warps.
+template <typename T, bool SHIFT>
+auto fwd_words(const Spread &s) -> void (*)(NormFwd) {
+    if (s.vpt == 1) return s.W <= 8 ? norm_fwd_kernel<T, 1, SHIFT, 256> : norm_fwd_kernel<T, 1, SHIFT, 512>;
+    if (s.vpt == 2) return s.W <= 8 ? norm_fwd_kernel<T, 2, SHIFT, 256> : norm_fwd_kernel<T, 2, SHIFT, 512>;
+    if (s.vpt == 3) return norm_fwd_kernel<T, 3, SHIFT, 256>;
+    if constexpr (!SHIFT) {   // wider: whole words only, eight of fp32 only
+        if (s.vpt == 4) return norm_fwd_kernel<T, 4, false, 512>;
+        if constexpr (sizeof(T) == 4) return norm_fwd_kernel<T, 8, false, 512>;
     }
+    return nullptr;
 }
 template <typename T>
-auto bwd_kernel(int vpt, bool vec) -> void (*)(NormBwd) {
-    if (vpt == 0) return norm_bwd_general_kernel<T>;
-    if (!vec) return norm_bwd_kernel<T, 8 / kElems<T>, false>;
-    switch (vpt) {
-        case 1: return norm_bwd_kernel<T, 1, true>;
-        case 2: return norm_bwd_kernel<T, 2, true>;
-        case 3: return norm_bwd_kernel<T, 3, true>;
-        case 4: return norm_bwd_kernel<T, 4, true>;
-        default:
-            if constexpr (sizeof(T) == 4) return norm_bwd_kernel<T, 8, true>;
-            else return nullptr;
+auto fwd_kernel(const Spread &s) -> void (*)(NormFwd) {
+    if (s.vpt == 0) return norm_fwd_general_kernel<T>;
+    return s.shift ? fwd_words<T, true>(s) : fwd_words<T, false>(s);
+}
+template <typename T, bool SHIFT, bool DB>
+auto bwd_words(const Spread &s) -> void (*)(NormBwd) {
+    if (s.vpt == 1) return s.W <= 8 ? norm_bwd_kernel<T, 1, SHIFT, DB, 256> : norm_bwd_kernel<T, 1, SHIFT, DB, 512>;
+    if (s.vpt == 2) return s.W <= 8 ? norm_bwd_kernel<T, 2, SHIFT, DB, 256> : norm_bwd_kernel<T, 2, SHIFT, DB, 512>;
+    if constexpr (!SHIFT) {
+        if (s.vpt == 4) return norm_bwd_kernel<T, 4, false, DB, 512>;
+        if constexpr (sizeof(T) == 4) return norm_bwd_kernel<T, 8, false, DB, 512>;
     }
+    return nullptr;
+}
+template <typename T>
+auto bwd_kernel(const Spread &s, bool db) -> void (*)(NormBwd) {
+    if (s.vpt == 0) return norm_bwd_general_kernel<T>;
+    if (s.shift) return db ? bwd_words<T, true, true>(s) : bwd_words<T, true, false>(s);
+    return db ? bwd_words<T, false, true>(s) : bwd_words<T, false, false>(s);
 }
 
 moe_status check(const moe_norm_config *c) {
@@ -572,7 +677,7 @@ moe_status moe_norm_workspace_size(const moe_norm_config *c, size_t *bytes) {
     if (!bytes) return MOE_ERR_INVALID_ARG;
     const moe_status st = check(c);
     if (st != MOE_OK) return st;
-    *bytes = (size_t)std::min<int64_t>(kBwdBlocks, c->T) * 2 * (size_t)c->d * sizeof(float);
+    *bytes = part_rows(c->T) * 2 * (size_t)c->d * sizeof(float);
     return MOE_OK;
 }
 
@@ -585,17 +690,16 @@ moe_status moe_norm_forward(const moe_norm_config *c, const void *x, const void 
     if (!x || !weight || !y) return MOE_ERR_INVALID_ARG;
     if (!device_error_word()) return MOE_ERR_CUDA;
     const int E = 16 / elem_size(c->dtype);
-    const bool vec = c->d % E == 0 && aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(bias) &&
-                     aligned16(h) && aligned16(y);
-    const Spread sp = spread(c->d, E, vec);
+    const bool aligned = aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(bias) && aligned16(h) &&
+                         aligned16(y);
+    const Spread sp = spread(c->d, E, aligned, true);
     const NormFwd a{x, residual, weight, bias, h, y, mean, rstd, c->T, c->d, sp.W, sp.groups,
                     c->kind == MOE_NORM_LAYER, c->w_dtype == MOE_F32, c->eps};
     const int threads = sp.groups * sp.W * 32;
-    const int64_t rows = (c->T + sp.groups - 1) / sp.groups;
-    const int grid = (int)std::min<int64_t>(rows, (int64_t)num_sms() * std::max(1, 2048 / threads));
-    auto kern = c->dtype == MOE_BF16  ? fwd_kernel<__nv_bfloat16>(sp.vpt, vec)
-                : c->dtype == MOE_F16 ? fwd_kernel<__half>(sp.vpt, vec)
-                                      : fwd_kernel<float>(sp.vpt, vec);
+    auto kern = c->dtype == MOE_BF16  ? fwd_kernel<__nv_bfloat16>(sp)
+                : c->dtype == MOE_F16 ? fwd_kernel<__half>(sp)
+                                      : fwd_kernel<float>(sp);
+    const int grid = blocks_for(sp, c->T, resident_blocks(kern, threads, 0));
     const cudaError_t e = launch_kernel(kern, grid, threads, 0, static_cast<cudaStream_t>(stream), a);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -615,10 +719,9 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     if (!h || !weight || !rstd || !dy || !dx || layer != (mean != nullptr)) return MOE_ERR_INVALID_ARG;
     const bool params = dweight || dbias;
     const int E = 16 / elem_size(c->dtype);
-    const bool vec = c->d % E == 0 && aligned16(h) && aligned16(weight) && aligned16(dy) && aligned16(dh) && aligned16(dx);
-    const Spread sp = spread(c->d, E, vec);
-    const int blocks = (int)std::min<int64_t>(kBwdBlocks, (c->T + sp.groups - 1) / sp.groups);
-    if (params && (!ws || ws_bytes < (size_t)std::min<int64_t>(kBwdBlocks, c->T) * 2 * (size_t)c->d * sizeof(float) ||
+    const bool aligned = aligned16(h) && aligned16(weight) && aligned16(dy) && aligned16(dh) && aligned16(dx);
+    const Spread sp = spread(c->d, E, aligned, false);
+    if (params && (!ws || ws_bytes < part_rows(c->T) * 2 * (size_t)c->d * sizeof(float) ||
                    (reinterpret_cast<uintptr_t>(ws) & 255)))
         return MOE_ERR_WORKSPACE;
     if (!device_error_word()) return MOE_ERR_CUDA;
@@ -626,12 +729,14 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     const NormBwd a{h, weight, dy, dh, mean, rstd, dx, part, c->T, c->d, sp.W, sp.groups, c->w_dtype == MOE_F32,
                     dbias != nullptr};
     const size_t smem = sp.groups > 1 || sp.vpt == 0 ? 2 * sizeof(float) * (size_t)c->d : 0;
-    auto kern = c->dtype == MOE_BF16  ? bwd_kernel<__nv_bfloat16>(sp.vpt, vec)
-                : c->dtype == MOE_F16 ? bwd_kernel<__half>(sp.vpt, vec)
-                                      : bwd_kernel<float>(sp.vpt, vec);
+    auto kern = c->dtype == MOE_BF16  ? bwd_kernel<__nv_bfloat16>(sp, dbias != nullptr)
+                : c->dtype == MOE_F16 ? bwd_kernel<__half>(sp, dbias != nullptr)
+                                      : bwd_kernel<float>(sp, dbias != nullptr);
     cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e == cudaSuccess) e = launch_kernel(kern, blocks, sp.groups * sp.W * 32, smem, s, a);
+    const int threads = sp.groups * sp.W * 32;
+    const int blocks = blocks_for(sp, c->T, std::min(kBwdBlocks, resident_blocks(kern, threads, smem)));
+    if (e == cudaSuccess) e = launch_kernel(kern, blocks, threads, smem, s, a);
     if (e == cudaSuccess && params)
         e = launch_kernel(norm_param_kernel, dim3((c->d + 31) / 32, dbias ? 2 : 1), 1024, 0, s,
                           static_cast<const float *>(part), blocks, (int)c->d, dweight, dbias);

@@ -152,6 +152,11 @@ FORWARD = [
     # more rows than one round of the grid
     ("layer", "bf16", "bf16", 20011, 24, False, True), ("rms", "f32", "f32", 5003, 301, True, False),
     ("layer", "f16", "f16", 3001, 1032, True, True),
+    # widths whose rows start at every offset from a 16-byte boundary, in every spread of the row
+    ("layer", "bf16", "bf16", 9, 761, True, True), ("rms", "f16", "f16", 21, 762, False, False),
+    ("layer", "bf16", "f32", 700, 2052, True, True), ("rms", "bf16", "bf16", 40, 8185, True, False),
+    ("layer", "f32", "f32", 33, 385, True, True), ("layer", "f32", "f32", 77, 4093, False, True),
+    ("rms", "f32", "f32", 10, 4098, True, False), ("layer", "bf16", "bf16", 3, 16383, False, True),
 ]
 
 
