@@ -83,6 +83,36 @@ __device__ __forceinline__ uint4 pack(const float (&v)[kElems<T>]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The word of a row of d elements that starts at its column c, address p.  With
+// SHIFT c may be negative and the word may pass the row's end: only what lies in
+// the row is read (the rest is zero) or written.
+template <typename T, bool SHIFT>
+__device__ __forceinline__ uint4 load_word(const T *p, int c, int d) {
+    constexpr int E = kElems<T>;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    if (SHIFT ? c >= 0 && c + E <= d : c < d) {
+        w = *reinterpret_cast<const uint4 *>(p);
+    } else if constexpr (SHIFT) {
+        T e[E];
+#pragma unroll
+        for (int k = 0; k < E; ++k) e[k] = c + k >= 0 && c + k < d ? p[k] : el_from<T>(0.f);
+        w = *reinterpret_cast<const uint4 *>(e);
+    }
+    return w;
+}
+template <typename T, bool SHIFT>
+__device__ __forceinline__ void store_word(T *p, int c, int d, const uint4 &w) {
+    constexpr int E = kElems<T>;
+    if (SHIFT ? c >= 0 && c + E <= d : c < d) {
+        *reinterpret_cast<uint4 *>(p) = w;
+    } else if constexpr (SHIFT) {
+        const T *e = reinterpret_cast<const T *>(&w);
+#pragma unroll
+        for (int k = 0; k < E; ++k)
+            if (c + k >= 0 && c + k < d) p[k] = e[k];
+    }
+}
+
 // The 16-byte words of a row that one thread holds: word j * G + i of the row
 // (i the thread in its group of G).  A row of a width that is not a multiple of
 // E starts `shift` elements into an aligned word; its words are counted from
@@ -99,33 +129,11 @@ struct Row {
         return (j * G + i) * E - (SHIFT ? shift : 0);
     }
     // p: the row's first element
-    __device__ __forceinline__ void load_word(const T *p, int i, int G, int d, int shift, int j) {
-        const int c = first(i, G, j, shift);
-        if (SHIFT ? c >= 0 && c + E <= d : c < d) {
-            v[j] = *reinterpret_cast<const uint4 *>(p + c);
-        } else {
-            v[j] = make_uint4(0, 0, 0, 0);
-            if constexpr (SHIFT) {
-                T e[E];
-#pragma unroll
-                for (int k = 0; k < E; ++k) e[k] = c + k >= 0 && c + k < d ? p[c + k] : el_from<T>(0.f);
-                v[j] = *reinterpret_cast<const uint4 *>(e);
-            }
-        }
-    }
     __device__ __forceinline__ void load(const T *p, int i, int G, int d, int shift) {
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) load_word(p, i, G, d, shift, j);
-    }
-    __device__ __forceinline__ static void store_word(T *p, int i, int G, int d, int shift, int j, const uint4 &w) {
-        const int c = first(i, G, j, shift);
-        if (SHIFT ? c >= 0 && c + E <= d : c < d) {
-            *reinterpret_cast<uint4 *>(p + c) = w;
-        } else if constexpr (SHIFT) {
-            const T *e = reinterpret_cast<const T *>(&w);
-#pragma unroll
-            for (int k = 0; k < E; ++k)
-                if (c + k >= 0 && c + k < d) p[c + k] = e[k];
+        for (int j = 0; j < VPT; ++j) {
+            const int c = first(i, G, j, shift);
+            v[j] = load_word<T, SHIFT>(p + c, c, d);
         }
     }
 };
@@ -237,7 +245,8 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
 #pragma unroll
                 for (int e = 0; e < E; ++e) c[j][e] += z[e];
                 const uint4 u = pack<T>(c[j]);
-                R::store_word(static_cast<T *>(a.h) + o, i, G, d, shift, j, u);
+                const int c0 = R::first(i, G, j, shift);
+                store_word<T, SHIFT>(static_cast<T *>(a.h) + o + c0, c0, d, u);
                 unpack<T>(u, c[j]);   // the norm is of the rows as they are stored
             }
         }
@@ -288,7 +297,7 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
 #pragma unroll
                 for (int e = 0; e < E; ++e) c[j][e] = c[j][e] * rstd * g[e];
             }
-            R::store_word(static_cast<T *>(a.y) + o, i, G, d, shift, j, pack<T>(c[j]));
+            store_word<T, SHIFT>(static_cast<T *>(a.y) + o + c0, c0, d, pack<T>(c[j]));
         }
         o += jump;
     }
@@ -311,7 +320,6 @@ template <typename T, int VPT, bool SHIFT, bool DB, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) norm_bwd_kernel(NormBwd a) {
     constexpr bool HOLD = VPT <= 2;
     constexpr int E = kElems<T>;
-    using R = Row<T, VPT, SHIFT>;
     __shared__ float2 red[8 * 32];
     extern __shared__ float cols[];     // groups > 1: [2, d]
     const int W = a.W, G = W * 32, d = a.d;
@@ -323,9 +331,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
     int64_t r = (int64_t)blockIdx.x * a.groups + group;
     const int shift = SHIFT ? (int)(r * d % E) : 0;
     const bool layer = a.mean != nullptr, more = a.dh != nullptr, wf32 = a.wf32;
-    const T *h = static_cast<const T *>(a.h), *dy = static_cast<const T *>(a.dy), *dh = static_cast<const T *>(a.dh);
-    int64_t o = r * d;                  // the row's first element
+    // this thread's first word of the row in each tensor
+    const int64_t o = r * d + i * E - shift;
+    const T *h = static_cast<const T *>(a.h) + o, *dy = static_cast<const T *>(a.dy) + o;
+    const T *dh = more ? static_cast<const T *>(a.dh) + o : nullptr;
+    T *dx = static_cast<T *>(a.dx) + o;
     const int64_t jump = step * d;
+    const int c0 = i * E - shift, cj = G * E;   // its column, and from one word to the next
     float dw[VPT][E], db[DB ? VPT : 1][E];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
@@ -336,78 +348,92 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
         }
     pdl_wait();
     pdl_launch_dependents();
-    R nh, ny;
+    uint4 nh[HOLD ? VPT : 1], ny[HOLD ? VPT : 1];
     float nm = 0.f, ns = 0.f;
     if (r < a.T) {
         if constexpr (HOLD) {
-            nh.load(h + o, i, G, d, shift);
-            ny.load(dy + o, i, G, d, shift);
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                nh[j] = load_word<T, SHIFT>(h + j * cj, c0 + j * cj, d);
+                ny[j] = load_word<T, SHIFT>(dy + j * cj, c0 + j * cj, d);
+            }
         }
         if (layer) nm = a.mean[r];
         ns = a.rstd[r];
     }
     for (; r < a.T; r += step) {
-        R ch, cy, cd;
+        uint4 cd[HOLD ? VPT : 1];
         const float mean = nm, rstd = ns;
-        if constexpr (HOLD) {
-            ch = nh;
-            cy = ny;
-            if (more) cd.load(dh + o, i, G, d, shift);
-            if (r + step < a.T) {
-                nh.load(h + o + jump, i, G, d, shift);
-                ny.load(dy + o + jump, i, G, d, shift);
-            }
+        const bool next = r + step < a.T;
+        if (HOLD && more) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) cd[j] = load_word<T, SHIFT>(dh + j * cj, c0 + j * cj, d);
         }
-        if (r + step < a.T) {
+        if (next) {
             if (layer) nm = a.mean[r + step];
             ns = a.rstd[r + step];
         }
-        float2 s = make_float2(0.f, 0.f);   // sums of g and g * xhat
+        float z[HOLD ? VPT : 1][E], g[HOLD ? VPT : 1][E];
+        float2 s = make_float2(0.f, 0.f);   // sums of g and of g (h - mean)
         // elements outside the row have dy = 0: they add nothing to any sum
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            float w[E], x[E], y[E];
-            load_param<T, SHIFT>(a.weight, wf32, R::first(i, G, j, shift), d, w);
-            if constexpr (!HOLD) {
-                ch.load_word(h + o, i, G, d, shift, j);
-                cy.load_word(dy + o, i, G, d, shift, j);
-            }
-            unpack<T>(ch.v[j], x);
-            unpack<T>(cy.v[j], y);
+            constexpr bool kHold = HOLD;
+            const int q = kHold ? j : 0, c = c0 + j * cj;
+            float w[E], y[E];
+            load_param<T, SHIFT>(a.weight, wf32, c, d, w);
+            unpack<T>(kHold ? nh[q] : load_word<T, SHIFT>(h + j * cj, c, d), z[q]);
+            unpack<T>(kHold ? ny[q] : load_word<T, SHIFT>(dy + j * cj, c, d), y);
 #pragma unroll
             for (int e = 0; e < E; ++e) {
-                const float xh = (x[e] - mean) * rstd, g = y[e] * w[e];
-                s.x += g;
-                s.y = fmaf(g, xh, s.y);
-                dw[j][e] = fmaf(y[e], xh, dw[j][e]);
+                z[q][e] -= mean;
+                g[q][e] = y[e] * w[e];
+                s.x += g[q][e];
+                s.y = fmaf(g[q][e], z[q][e], s.y);
+                dw[j][e] = fmaf(y[e] * rstd, z[q][e], dw[j][e]);
                 if (DB) db[j][e] += y[e];
             }
         }
+        if (HOLD && next) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                nh[j] = load_word<T, SHIFT>(h + jump + j * cj, c0 + j * cj, d);
+                ny[j] = load_word<T, SHIFT>(dy + jump + j * cj, c0 + j * cj, d);
+            }
+        }
         s = group_sum(s, slot, turn, wi, W, 1 + group);
-        // dx = rstd g - rstd avg(g) - xhat rstd avg(g xhat)
-        const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * (s.y * inv);
+        // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
+        const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            float w[E], x[E], y[E];
-            load_param<T, SHIFT>(a.weight, wf32, R::first(i, G, j, shift), d, w);
+            constexpr bool kHold = HOLD;
+            const int q = kHold ? j : 0, c = c0 + j * cj;
             if constexpr (!HOLD) {
-                ch.load_word(h + o, i, G, d, shift, j);
-                cy.load_word(dy + o, i, G, d, shift, j);
-                if (more) cd.load_word(dh + o, i, G, d, shift, j);
-            }
-            unpack<T>(ch.v[j], x);
-            unpack<T>(cy.v[j], y);
+                float w[E];
+                load_param<T, SHIFT>(a.weight, wf32, c, d, w);
+                unpack<T>(load_word<T, SHIFT>(h + j * cj, c, d), z[0]);
+                unpack<T>(load_word<T, SHIFT>(dy + j * cj, c, d), g[0]);
+                if (more) cd[0] = load_word<T, SHIFT>(dh + j * cj, c, d);
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                x[e] = fmaf((x[e] - mean) * rstd, c2, fmaf(y[e] * w[e], rstd, c1));
+                for (int e = 0; e < E; ++e) {
+                    z[0][e] -= mean;
+                    g[0][e] *= w[e];
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[q][e] = fmaf(z[q][e], c2, fmaf(g[q][e], rstd, c1));
             if (more) {
-                unpack<T>(cd.v[j], y);
+                float y[E];
+                unpack<T>(cd[q], y);
 #pragma unroll
-                for (int e = 0; e < E; ++e) x[e] += y[e];
+                for (int e = 0; e < E; ++e) z[q][e] += y[e];
             }
-            R::store_word(static_cast<T *>(a.dx) + o, i, G, d, shift, j, pack<T>(x));
+            store_word<T, SHIFT>(dx + j * cj, c, d, pack<T>(z[q]));
         }
-        o += jump;
+        h += jump;
+        dy += jump;
+        if (more) dh += jump;
+        dx += jump;
     }
     if (!a.part) return;
     float *out = a.part + (int64_t)blockIdx.x * 2 * d;
@@ -418,7 +444,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    const int c = R::first(i, G, j, shift) + e;
+                    const int c = c0 + j * cj + e;
                     if (c < 0 || c >= d) continue;
                     float sw = dw[j][e], sb = DB ? db[j][e] : 0.f;
                     if (k > 0) {
@@ -563,7 +589,7 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(const float *part, int
 }
 
 // How a row is spread: VPT words per thread, W warps per row, `groups` rows
-// per block; vpt = 0 is the general kernel.  Of one, two and (forward) three
+// per block; vpt = 0 is the general kernel.  Of one, two and (forward, whole words) three
 // words a thread, the one that leaves the fewest words of its warps idle, and
 // of those the one with the fewest warps: one warp needs no barrier.  Four
 // (eight) words where more than 16 warps would be needed.
@@ -581,7 +607,7 @@ Spread spread(int d, int elems, bool aligned, bool forward) {
         s.vpt = words <= 128 * kMaxWarps ? 4 : 8;
         s.W = (words + 32 * s.vpt - 1) / (32 * s.vpt);
     } else {
-        for (int v = 1; v <= (forward && words <= 96 ? 3 : 2); ++v) {
+        for (int v = 1; v <= (forward && !shift && words <= 96 ? 3 : 2); ++v) {
             const int w = (words + 32 * v - 1) / (32 * v);
             if (w <= kMaxWarps && (!s.vpt || w * v <= s.W * s.vpt)) {
                 s.vpt = v;
@@ -626,7 +652,8 @@ template <typename T, bool SHIFT>
 auto fwd_words(const Spread &s) -> void (*)(NormFwd) {
     if (s.vpt == 1) return s.W <= 8 ? norm_fwd_kernel<T, 1, SHIFT, 256> : norm_fwd_kernel<T, 1, SHIFT, 512>;
     if (s.vpt == 2) return s.W <= 8 ? norm_fwd_kernel<T, 2, SHIFT, 256> : norm_fwd_kernel<T, 2, SHIFT, 512>;
-    if (s.vpt == 3) return norm_fwd_kernel<T, 3, SHIFT, 256>;
+    if constexpr (!SHIFT)
+        if (s.vpt == 3) return norm_fwd_kernel<T, 3, false, 256>;
     if constexpr (!SHIFT) {   // wider: whole words only, eight of fp32 only
         if (s.vpt == 4) return norm_fwd_kernel<T, 4, false, 512>;
         if constexpr (sizeof(T) == 4) return norm_fwd_kernel<T, 8, false, 512>;
