@@ -47,37 +47,62 @@ template <> __device__ __forceinline__ float el_from<float>(float v) { return v;
 template <> __device__ __forceinline__ __nv_bfloat16 el_from<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half el_from<__half>(float v) { return __float2half_rn(v); }
 
-// A word's elements as fp32, and back (rounded to nearest), two at a time.
+// Two fp32 operations an instruction (sm_100's packed fp32), which halves what
+// these kernels issue per element besides the conversions.
+__device__ __forceinline__ unsigned long long bits2(float2 v) { return *reinterpret_cast<unsigned long long *>(&v); }
+__device__ __forceinline__ float2 from2(unsigned long long b) { return *reinterpret_cast<float2 *>(&b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
+    return from2(r);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from2(r);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
+    return from2(r);
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
+// A word's elements as pairs of fp32, and back (rounded to nearest).
 template <typename T>
-__device__ __forceinline__ void unpack(const uint4 &u, float (&o)[kElems<T>]) {
+constexpr int kPairs = kElems<T> / 2;
+template <typename T>
+__device__ __forceinline__ void unpack(const uint4 &u, float2 (&o)[kPairs<T>]) {
     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    if constexpr (sizeof(T) == 4) {
+        o[0] = make_float2(__uint_as_float(w[0]), __uint_as_float(w[1]));
+        o[1] = make_float2(__uint_as_float(w[2]), __uint_as_float(w[3]));
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(T) == 4) {
-            o[k] = __uint_as_float(w[k]);
-        } else if constexpr (std::is_same_v<T, __half>) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
-            o[2 * k] = f.x;
-            o[2 * k + 1] = f.y;
-        } else {
-            o[2 * k] = __uint_as_float(w[k] << 16);
-            o[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (std::is_same_v<T, __half>) o[k] = __half22float2(*reinterpret_cast<const __half2 *>(&w[k]));
+            else o[k] = make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
         }
     }
 }
 template <typename T>
-__device__ __forceinline__ uint4 pack(const float (&v)[kElems<T>]) {
+__device__ __forceinline__ uint4 pack(const float2 (&v)[kPairs<T>]) {
     uint32_t w[4];
+    if constexpr (sizeof(T) == 4) {
+        w[0] = __float_as_uint(v[0].x);
+        w[1] = __float_as_uint(v[0].y);
+        w[2] = __float_as_uint(v[1].x);
+        w[3] = __float_as_uint(v[1].y);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(T) == 4) {
-            w[k] = __float_as_uint(v[k]);
-        } else if constexpr (std::is_same_v<T, __half>) {
-            const __half2 h = __floats2half2_rn(v[2 * k], v[2 * k + 1]);
-            w[k] = *reinterpret_cast<const uint32_t *>(&h);
-        } else {
-            const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
-            w[k] = *reinterpret_cast<const uint32_t *>(&h);
+        for (int k = 0; k < 4; ++k) {
+            if constexpr (std::is_same_v<T, __half>) {
+                const __half2 h = __floats2half2_rn(v[k].x, v[k].y);
+                w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[k].x, v[k].y);
+                w[k] = *reinterpret_cast<const uint32_t *>(&h);
+            }
         }
     }
     return make_uint4(w[0], w[1], w[2], w[3]);
@@ -143,24 +168,23 @@ __device__ __forceinline__ float param(const void *p, bool wf32, int c) {
     return wf32 ? __ldg(static_cast<const float *>(p) + c) : el_f32(static_cast<const T *>(p)[c]);
 }
 // E elements of the weight or bias vector (of type T, or fp32 when wf32) from
-// column c, as fp32; zeros outside the row.
+// column c, as pairs of fp32; zeros outside the row.
 template <typename T, bool SHIFT>
-__device__ __forceinline__ void load_param(const void *p, bool wf32, int c, int d, float (&o)[kElems<T>]) {
-    constexpr int E = kElems<T>;
+__device__ __forceinline__ void load_param(const void *p, bool wf32, int c, int d, float2 (&o)[kPairs<T>]) {
+    constexpr int P = kPairs<T>;
     if constexpr (SHIFT) {
+        auto at = [&](int k) { return k >= 0 && k < d ? param<T>(p, wf32, k) : 0.f; };
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = c + e >= 0 && c + e < d ? param<T>(p, wf32, c + e) : 0.f;
+        for (int k = 0; k < P; ++k) o[k] = make_float2(at(c + 2 * k), at(c + 2 * k + 1));
     } else if (c >= d) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = 0.f;
+        for (int k = 0; k < P; ++k) o[k] = make_float2(0.f, 0.f);
     } else if (wf32) {
 #pragma unroll
-        for (int q = 0; q < E / 4; ++q) {
-            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c) + q);
-            o[4 * q] = f.x;
-            o[4 * q + 1] = f.y;
-            o[4 * q + 2] = f.z;
-            o[4 * q + 3] = f.w;
+        for (int k = 0; k < P / 2; ++k) {
+            const float4 f = __ldg(reinterpret_cast<const float4 *>(static_cast<const float *>(p) + c) + k);
+            o[2 * k] = make_float2(f.x, f.y);
+            o[2 * k + 1] = make_float2(f.z, f.w);
         }
     } else {
         unpack<T>(__ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(p) + c)), o);
@@ -211,7 +235,7 @@ constexpr int kFwdBlocks = THREADS == 256 && !SHIFT ? (VPT <= 2 ? 3 : 2) : 1;
 
 template <typename T, int VPT, bool SHIFT, int THREADS>
 __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm_fwd_kernel(NormFwd a) {
-    constexpr int E = kElems<T>;
+    constexpr int E = kElems<T>, P = kPairs<T>;
     using R = Row<T, VPT, SHIFT>;
     __shared__ float red[8 * 32];
     const int W = a.W, G = W * 32, d = a.d;
@@ -234,16 +258,16 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
         if (add) nr.load(res + o, i, G, d, shift);
     }
     for (; r < a.T; r += step) {
-        float c[VPT][E];
+        float2 c[VPT][P];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) unpack<T>(nx.v[j], c[j]);
         if (add) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                float z[E];
+                float2 z[P];
                 unpack<T>(nr.v[j], z);
 #pragma unroll
-                for (int e = 0; e < E; ++e) c[j][e] += z[e];
+                for (int k = 0; k < P; ++k) c[j][k] = add2(c[j][k], z[k]);
                 const uint4 u = pack<T>(c[j]);
                 const int c0 = R::first(i, G, j, shift);
                 store_word<T, SHIFT>(static_cast<T *>(a.h) + o + c0, c0, d, u);
@@ -257,28 +281,35 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
         // elements outside the row are zeros in every sum
         float mean = 0.f;
         if (a.layer) {
-            float s = 0.f;
+            float2 s = both(0.f);
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int e = 0; e < E; ++e) s += c[j][e];
-            s = group_sum(s, slot, turn, w, W, 1 + group);
-            mean = s * inv;
-            mean = fmaf(fmaf(-mean, df, s), inv, mean);   // the quotient s / d, rounded once
+                for (int k = 0; k < P; ++k) s = add2(s, c[j][k]);
+            const float t = group_sum(s.x + s.y, slot, turn, w, W, 1 + group);
+            mean = t * inv;
+            mean = fmaf(fmaf(-mean, df, t), inv, mean);   // the quotient t / d, rounded once
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
                 const int c0 = R::first(i, G, j, shift);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    c[j][e] = (SHIFT ? c0 + e >= 0 && c0 + e < d : c0 < d) ? c[j][e] - mean : 0.f;
+                for (int k = 0; k < P; ++k) {
+                    const float2 z = add2(c[j][k], both(-mean));
+                    if constexpr (SHIFT) {
+                        const int q = c0 + 2 * k;
+                        c[j][k] = make_float2(q >= 0 && q < d ? z.x : 0.f, q + 1 >= 0 && q + 1 < d ? z.y : 0.f);
+                    } else {
+                        c[j][k] = c0 < d ? z : both(0.f);
+                    }
+                }
             }
         }
-        float q = 0.f;
+        float2 q = both(0.f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
-            for (int e = 0; e < E; ++e) q = fmaf(c[j][e], c[j][e], q);
-        const float rstd = rsqrtf(group_sum(q, slot, turn, w, W, 1 + group) * inv + a.eps);
+            for (int k = 0; k < P; ++k) q = fma2(c[j][k], c[j][k], q);
+        const float rstd = rsqrtf(group_sum(q.x + q.y, slot, turn, w, W, 1 + group) * inv + a.eps);
         if (i == 0) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
@@ -286,16 +317,18 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int c0 = R::first(i, G, j, shift);
-            float g[E];
+            float2 g[P];
             load_param<T, SHIFT>(a.weight, wf32, c0, d, g);
+#pragma unroll
+            for (int k = 0; k < P; ++k) c[j][k] = mul2(c[j][k], both(rstd));
             if (bias) {
-                float b[E];
+                float2 b[P];
                 load_param<T, SHIFT>(a.bias, wf32, c0, d, b);
 #pragma unroll
-                for (int e = 0; e < E; ++e) c[j][e] = fmaf(c[j][e] * rstd, g[e], b[e]);
+                for (int k = 0; k < P; ++k) c[j][k] = fma2(c[j][k], g[k], b[k]);
             } else {
 #pragma unroll
-                for (int e = 0; e < E; ++e) c[j][e] = c[j][e] * rstd * g[e];
+                for (int k = 0; k < P; ++k) c[j][k] = mul2(c[j][k], g[k]);
             }
             store_word<T, SHIFT>(static_cast<T *>(a.y) + o + c0, c0, d, pack<T>(c[j]));
         }
@@ -319,7 +352,7 @@ struct NormBwd {
 template <typename T, int VPT, bool SHIFT, bool DB, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) norm_bwd_kernel(NormBwd a) {
     constexpr bool HOLD = VPT <= 2;
-    constexpr int E = kElems<T>;
+    constexpr int E = kElems<T>, P = kPairs<T>;
     __shared__ float2 red[8 * 32];
     extern __shared__ float cols[];     // groups > 1: [2, d]
     const int W = a.W, G = W * 32, d = a.d;
@@ -338,13 +371,13 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
     T *dx = static_cast<T *>(a.dx) + o;
     const int64_t jump = step * d;
     const int c0 = i * E - shift, cj = G * E;   // its column, and from one word to the next
-    float dw[VPT][E], db[DB ? VPT : 1][E];
+    float2 dw[VPT][P], db[DB ? VPT : 1][P];
 #pragma unroll
     for (int j = 0; j < VPT; ++j)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            dw[j][e] = 0.f;
-            if (DB) db[j][e] = 0.f;
+        for (int k = 0; k < P; ++k) {
+            dw[j][k] = both(0.f);
+            if (DB) db[j][k] = both(0.f);
         }
     pdl_wait();
     pdl_launch_dependents();
@@ -373,25 +406,25 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
             if (layer) nm = a.mean[r + step];
             ns = a.rstd[r + step];
         }
-        float z[HOLD ? VPT : 1][E], g[HOLD ? VPT : 1][E];
-        float2 s = make_float2(0.f, 0.f);   // sums of g and of g (h - mean)
+        float2 z[HOLD ? VPT : 1][P], g[HOLD ? VPT : 1][P];
+        float2 sg = both(0.f), sz = both(0.f);   // sums of g and of g (h - mean)
         // elements outside the row have dy = 0: they add nothing to any sum
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             constexpr bool kHold = HOLD;
             const int q = kHold ? j : 0, c = c0 + j * cj;
-            float w[E], y[E];
+            float2 w[P], y[P];
             load_param<T, SHIFT>(a.weight, wf32, c, d, w);
             unpack<T>(kHold ? nh[q] : load_word<T, SHIFT>(h + j * cj, c, d), z[q]);
             unpack<T>(kHold ? ny[q] : load_word<T, SHIFT>(dy + j * cj, c, d), y);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                z[q][e] -= mean;
-                g[q][e] = y[e] * w[e];
-                s.x += g[q][e];
-                s.y = fmaf(g[q][e], z[q][e], s.y);
-                dw[j][e] = fmaf(y[e] * rstd, z[q][e], dw[j][e]);
-                if (DB) db[j][e] += y[e];
+            for (int k = 0; k < P; ++k) {
+                z[q][k] = add2(z[q][k], both(-mean));
+                g[q][k] = mul2(y[k], w[k]);
+                sg = add2(sg, g[q][k]);
+                sz = fma2(g[q][k], z[q][k], sz);
+                dw[j][k] = fma2(mul2(y[k], both(rstd)), z[q][k], dw[j][k]);
+                if (DB) db[j][k] = add2(db[j][k], y[k]);
             }
         }
         if (HOLD && next) {
@@ -401,7 +434,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
                 ny[j] = load_word<T, SHIFT>(dy + jump + j * cj, c0 + j * cj, d);
             }
         }
-        s = group_sum(s, slot, turn, wi, W, 1 + group);
+        const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), slot, turn, wi, W, 1 + group);
         // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
         const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
 #pragma unroll
@@ -409,24 +442,24 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
             constexpr bool kHold = HOLD;
             const int q = kHold ? j : 0, c = c0 + j * cj;
             if constexpr (!HOLD) {
-                float w[E];
+                float2 w[P];
                 load_param<T, SHIFT>(a.weight, wf32, c, d, w);
                 unpack<T>(load_word<T, SHIFT>(h + j * cj, c, d), z[0]);
                 unpack<T>(load_word<T, SHIFT>(dy + j * cj, c, d), g[0]);
                 if (more) cd[0] = load_word<T, SHIFT>(dh + j * cj, c, d);
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    z[0][e] -= mean;
-                    g[0][e] *= w[e];
+                for (int k = 0; k < P; ++k) {
+                    z[0][k] = add2(z[0][k], both(-mean));
+                    g[0][k] = mul2(g[0][k], w[k]);
                 }
             }
 #pragma unroll
-            for (int e = 0; e < E; ++e) z[q][e] = fmaf(z[q][e], c2, fmaf(g[q][e], rstd, c1));
+            for (int k = 0; k < P; ++k) z[q][k] = fma2(z[q][k], both(c2), fma2(g[q][k], both(rstd), both(c1)));
             if (more) {
-                float y[E];
+                float2 y[P];
                 unpack<T>(cd[q], y);
 #pragma unroll
-                for (int e = 0; e < E; ++e) z[q][e] += y[e];
+                for (int k = 0; k < P; ++k) z[q][k] = add2(z[q][k], y[k]);
             }
             store_word<T, SHIFT>(dx + j * cj, c, d, pack<T>(z[q]));
         }
@@ -446,7 +479,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
                 for (int e = 0; e < E; ++e) {
                     const int c = c0 + j * cj + e;
                     if (c < 0 || c >= d) continue;
-                    float sw = dw[j][e], sb = DB ? db[j][e] : 0.f;
+                    float sw = e & 1 ? dw[j][e / 2].y : dw[j][e / 2].x;
+                    float sb = DB ? (e & 1 ? db[j][e / 2].y : db[j][e / 2].x) : 0.f;
                     if (k > 0) {
                         sw += cols[c];
                         if (DB) sb += cols[d + c];
