@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include "moe_internal.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -344,7 +345,53 @@ struct NormBwd {
     int64_t T;
     int d, W, groups;
     bool wf32, want_db;
+    uint32_t *err;
 };
+
+// The block's partial sums: its groups add their columns one after another in
+// `cols` ([2, d], groups > 1), the last one writes them out.  Whole words: eight
+// (four) consecutive columns of a thread at a time.
+template <typename T, int VPT, bool SHIFT, bool DB>
+__device__ __forceinline__ void write_part(const NormBwd &a, float *cols, int group, int c0, int cj,
+                                           const float2 (&dw)[VPT][kPairs<T>],
+                                           const float2 (&db)[DB ? VPT : 1][kPairs<T>]) {
+    constexpr int P = kPairs<T>;
+    const int d = a.d;
+    float *out = a.part + (int64_t)blockIdx.x * 2 * d;
+    for (int k = 0; k < a.groups; ++k) {
+        if (group == k) {
+            const bool last = k + 1 == a.groups;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+#pragma unroll
+                for (int h = 0; h < (DB ? 2 : 1); ++h) {
+                    const int c = c0 + j * cj;
+                    float *to = (last ? out : cols) + h * d, *from = cols + h * d;
+                    if constexpr (SHIFT) {
+#pragma unroll
+                        for (int e = 0; e < 2 * P; ++e) {
+                            if (c + e < 0 || c + e >= d) continue;
+                            const float2 v = h ? db[DB ? j : 0][e / 2] : dw[j][e / 2];
+                            to[c + e] = (e & 1 ? v.y : v.x) + (k ? from[c + e] : 0.f);
+                        }
+                    } else if (c < d) {
+#pragma unroll
+                        for (int q = 0; q < P; q += 2) {
+                            const float2 u = h ? db[DB ? j : 0][q] : dw[j][q], v = h ? db[DB ? j : 0][q + 1] : dw[j][q + 1];
+                            float4 f = make_float4(u.x, u.y, v.x, v.y);
+                            if (k) {
+                                const float4 b = *reinterpret_cast<const float4 *>(from + c + 2 * q);
+                                f = make_float4(f.x + b.x, f.y + b.y, f.z + b.z, f.w + b.w);
+                            }
+                            *reinterpret_cast<float4 *>(to + c + 2 * q) = f;
+                        }
+                    }
+                }
+            }
+        }
+        if (a.groups > 1) __syncthreads();
+    }
+}
 
 // Up to two words a thread, a row's words are held between its two passes and
 // the next row's are requested meanwhile; of wider rows only the gradients' sums
@@ -468,34 +515,131 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
         if (more) dh += jump;
         dx += jump;
     }
-    if (!a.part) return;
-    float *out = a.part + (int64_t)blockIdx.x * 2 * d;
-    // the block's groups add their columns one after another
-    for (int k = 0; k < a.groups; ++k) {
-        if (group == k) {
+    if (a.part) write_part<T, VPT, SHIFT, DB>(a, cols, group, c0, cj, dw, db);
+}
+
+// The backward pass of whole-word rows of up to two words a thread.  Its inputs
+// come through a ring of kRing rows per group in shared memory, each row a bulk
+// copy that one thread requests kRing - 1 rows ahead: with loads into registers
+// (one row ahead, which is all that fits beside the sums) each row waited for
+// HBM, 41 us at T = 8192, d = 2048 and 44 us at T = 30001, d = 640.
+constexpr int kRing = 4;
+
+template <typename T, int VPT, bool DB>
+__global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(NormBwd a) {
+    constexpr int E = kElems<T>, P = kPairs<T>;
+    __shared__ float2 red[8 * 32];
+    __shared__ uint64_t landed[8][kRing];
+    __shared__ int gave_up;
+    extern __shared__ __align__(16) uint8_t ring[];   // [group][kRing][h | dy | dh]; then the columns' sums [2, d]
+    const int W = a.W, G = W * 32, d = a.d;
+    const int group = threadIdx.x / G, i = threadIdx.x - group * G, wi = i >> 5;
+    const bool layer = a.mean != nullptr, more = a.dh != nullptr, wf32 = a.wf32;
+    const uint32_t bytes = (uint32_t)d * sizeof(T), stage = bytes * (more ? 3 : 2);
+    uint8_t *mine = ring + (size_t)group * kRing * stage;
+    float2 *slot = red + 32 * group;
+    int turn = 0;
+    const float inv = 1.f / (float)d;
+    const int64_t step = (int64_t)gridDim.x * a.groups;
+    int64_t r = (int64_t)blockIdx.x * a.groups + group;
+    const int c0 = i * E, cj = G * E;   // this thread's first column, and from one word to the next
+    T *dx = static_cast<T *>(a.dx) + r * d + c0;
+    float2 dw[VPT][P], db[DB ? VPT : 1][P];
 #pragma unroll
-            for (int j = 0; j < VPT; ++j)
+    for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const int c = c0 + j * cj + e;
-                    if (c < 0 || c >= d) continue;
-                    float sw = e & 1 ? dw[j][e / 2].y : dw[j][e / 2].x;
-                    float sb = DB ? (e & 1 ? db[j][e / 2].y : db[j][e / 2].x) : 0.f;
-                    if (k > 0) {
-                        sw += cols[c];
-                        if (DB) sb += cols[d + c];
-                    }
-                    if (k + 1 < a.groups) {
-                        cols[c] = sw;
-                        if (DB) cols[d + c] = sb;
-                    } else {
-                        out[c] = sw;
-                        if (DB) out[d + c] = sb;
-                    }
-                }
+        for (int k = 0; k < P; ++k) {
+            dw[j][k] = both(0.f);
+            if (DB) db[j][k] = both(0.f);
         }
-        if (a.groups > 1) __syncthreads();
+    if (i == 0)
+        for (int k = 0; k < kRing; ++k) tc::mbar_init(&landed[group][k], 1);
+    if (threadIdx.x == 0) gave_up = 0;
+    tc::fence_barrier_init();
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    auto request = [&](int64_t row, int k) {
+        uint64_t *bar = &landed[group][k];
+        uint8_t *to = mine + k * stage;
+        tc::mbar_expect_tx(bar, stage);
+        tc::bulk_load(to, static_cast<const T *>(a.h) + row * d, bytes, bar);
+        tc::bulk_load(to + bytes, static_cast<const T *>(a.dy) + row * d, bytes, bar);
+        if (more) tc::bulk_load(to + 2 * bytes, static_cast<const T *>(a.dh) + row * d, bytes, bar);
+    };
+    if (i == 0)
+        for (int k = 0; k < kRing - 1; ++k)
+            if (r + k * step < a.T) request(r + k * step, k);
+    float nm[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};   // the statistics of the next two rows
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (r + k * step < a.T) {
+            if (layer) nm[k] = a.mean[r + k * step];
+            ns[k] = a.rstd[r + k * step];
+        }
+    int k = 0;                 // ring position
+    uint32_t phase = 0;
+    for (; r < a.T; r += step) {
+        const float mean = nm[0], rstd = ns[0];
+        nm[0] = nm[1];
+        ns[0] = ns[1];
+        if (r + 2 * step < a.T) {
+            if (layer) nm[1] = a.mean[r + 2 * step];
+            ns[1] = a.rstd[r + 2 * step];
+        }
+        float2 w[VPT][P];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) load_param<T, false>(a.weight, wf32, c0 + j * cj, d, w[j]);
+        // a wait that runs out is reported; the pass goes on, so that its barriers end
+        tc::wait_bar(&landed[group][k], phase, &gave_up, a.err);
+        const uint4 *h = reinterpret_cast<const uint4 *>(mine + k * stage) + i;
+        const uint4 *dy = reinterpret_cast<const uint4 *>(mine + k * stage + bytes) + i;
+        float2 z[VPT][P], g[VPT][P];
+        float2 sg = both(0.f), sz = both(0.f);   // sums of g and of g (h - mean)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const bool in = c0 + j * cj < d;
+            float2 y[P];
+            unpack<T>(in ? h[j * G] : make_uint4(0, 0, 0, 0), z[j]);
+            unpack<T>(in ? dy[j * G] : make_uint4(0, 0, 0, 0), y);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                z[j][q] = add2(z[j][q], both(-mean));
+                g[j][q] = mul2(y[q], w[j][q]);
+                sg = add2(sg, g[j][q]);
+                sz = fma2(g[j][q], z[j][q], sz);
+                dw[j][q] = fma2(mul2(y[q], both(rstd)), z[j][q], dw[j][q]);
+                if (DB) db[j][q] = add2(db[j][q], y[q]);
+            }
+        }
+        const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), slot, turn, wi, W, 1 + group);
+        // every thread of the group is past the row before this one: its place is free
+        if (i == 0 && r + (kRing - 1) * step < a.T) request(r + (kRing - 1) * step, k == 0 ? kRing - 1 : k - 1);
+        // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
+        const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
+        const uint4 *dh = reinterpret_cast<const uint4 *>(mine + k * stage + 2 * bytes) + i;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const bool in = c0 + j * cj < d;
+#pragma unroll
+            for (int q = 0; q < P; ++q) z[j][q] = fma2(z[j][q], both(c2), fma2(g[j][q], both(rstd), both(c1)));
+            if (more) {
+                float2 y[P];
+                unpack<T>(in ? dh[j * G] : make_uint4(0, 0, 0, 0), y);
+#pragma unroll
+                for (int q = 0; q < P; ++q) z[j][q] = add2(z[j][q], y[q]);
+            }
+            if (in) *reinterpret_cast<uint4 *>(dx + j * cj) = pack<T>(z[j]);
+        }
+        dx += step * d;
+        if (++k == kRing) {
+            k = 0;
+            phase ^= 1;
+        }
     }
+    if (!a.part) return;
+    __syncthreads();           // the ring is drained: its memory holds the columns' sums
+    write_part<T, VPT, false, DB>(a, reinterpret_cast<float *>(ring), group, c0, cj, dw, db);
 }
 
 // Any width and alignment: one block per row at a time, its columns strided
@@ -596,29 +740,47 @@ __global__ void __launch_bounds__(kGenThreads) norm_bwd_general_kernel(NormBwd a
     }
 }
 
-// dw and db: the sums of the blocks' partial rows [parts, 2, d].  A block
-// takes 32 columns (of dw, or of db in the grid's second half); warp k adds
-// every 32nd part from part k, and the 32 sums are added in order.
-__global__ void __launch_bounds__(1024) norm_param_kernel(const float *part, int parts, int d, float *dw, float *db) {
-    __shared__ float s[32][33];
+// dw and db: the sums of the blocks' partial rows [parts, 2, d].  A block takes
+// 32 columns (of dw, or of db in the grid's second half): eight lanes of a warp
+// read one part's, the warp four parts at a time, and 16 warps share the parts;
+// the 64 sums of a column are added in order.
+constexpr int kParamWarps = 16;
+__global__ void __launch_bounds__(32 * kParamWarps) norm_param_kernel(const float *part, int parts, int d, float *dw,
+                                                                       float *db) {
+    __shared__ float s[4 * kParamWarps][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + lane;
-    const float *p = part + (blockIdx.y ? d : 0);
+    const int c = blockIdx.x * 32 + (lane & 7) * 4, k0 = warp * 4 + (lane >> 3);
+    const float *p = part + (blockIdx.y ? d : 0) + c;
+    const bool whole = d % 4 == 0;   // (the workspace is aligned)
     pdl_wait();
     pdl_launch_dependents();
-    float v = 0.f;
-    if (c < d) {
-#pragma unroll 5
-        for (int k = warp; k < parts; k += 32) v += p[(int64_t)k * 2 * d + c];
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = k0; k < parts; k += 4 * kParamWarps) {
+        const float *q = p + (int64_t)k * 2 * d;
+        if (whole) {
+            if (c < d) {
+                const float4 f = *reinterpret_cast<const float4 *>(q);
+                v[0] += f.x;
+                v[1] += f.y;
+                v[2] += f.z;
+                v[3] += f.w;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < d) v[e] += q[e];
+        }
     }
-    s[warp][lane] = v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[k0][(lane & 7) * 4 + e] = v[e];
     __syncthreads();
-    if (warp == 0 && c < d) {
+    if (warp == 0 && blockIdx.x * 32 + lane < d) {
         float r = 0.f;
 #pragma unroll
-        for (int k = 0; k < 32; ++k) r += s[k][lane];
+        for (int k = 0; k < 4 * kParamWarps; ++k) r += s[k][lane];
         float *o = blockIdx.y ? db : dw;
-        if (o) o[c] = r;
+        if (o) o[blockIdx.x * 32 + lane] = r;
     }
 }
 
@@ -663,8 +825,9 @@ int blocks_for(const Spread &s, int64_t T, int most) {
 int elem_size(int dtype) { return dtype == MOE_F32 ? 4 : 2; }
 
 // Blocks of the backward pass at most, and so partial rows of the weight's
-// gradient: three per SM.
-constexpr int kBwdBlocks = 444;
+// gradient: of rows spread over few warps four per SM, else (the partial rows
+// are long then) two.
+int bwd_most(int d) { return d <= 2048 ? 592 : 296; }
 
 // Blocks of `kern` that the SMs hold at a time: the kernels stride over the rows,
 // so more would only wait.
@@ -676,7 +839,7 @@ int resident_blocks(K kern, int threads, size_t smem) {
 }
 
 // Partial rows that the workspace has room for (blocks_for rounds up to eight).
-size_t part_rows(int64_t T) { return (size_t)std::min<int64_t>(kBwdBlocks, (T + 7) / 8 * 8); }
+size_t part_rows(const moe_norm_config &c) { return (size_t)std::min<int64_t>(bwd_most(c.d), (c.T + 7) / 8 * 8); }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
@@ -699,21 +862,29 @@ auto fwd_kernel(const Spread &s) -> void (*)(NormFwd) {
     if (s.vpt == 0) return norm_fwd_general_kernel<T>;
     return s.shift ? fwd_words<T, true>(s) : fwd_words<T, false>(s);
 }
-template <typename T, bool SHIFT, bool DB>
+template <typename T, bool DB>
 auto bwd_words(const Spread &s) -> void (*)(NormBwd) {
-    if (s.vpt == 1) return s.W <= 8 ? norm_bwd_kernel<T, 1, SHIFT, DB, 256> : norm_bwd_kernel<T, 1, SHIFT, DB, 512>;
-    if (s.vpt == 2) return s.W <= 8 ? norm_bwd_kernel<T, 2, SHIFT, DB, 256> : norm_bwd_kernel<T, 2, SHIFT, DB, 512>;
-    if constexpr (!SHIFT) {
-        if (s.vpt == 4) return norm_bwd_kernel<T, 4, false, DB, 512>;
-        if constexpr (sizeof(T) == 4) return norm_bwd_kernel<T, 8, false, DB, 512>;
+    if (s.shift) {
+        if (s.vpt == 1) return s.W <= 8 ? norm_bwd_kernel<T, 1, true, DB, 256> : norm_bwd_kernel<T, 1, true, DB, 512>;
+        return s.W <= 8 ? norm_bwd_kernel<T, 2, true, DB, 256> : norm_bwd_kernel<T, 2, true, DB, 512>;
     }
+    if (s.vpt == 1) return norm_bwd_ring_kernel<T, 1, DB>;
+    if (s.vpt == 2) return norm_bwd_ring_kernel<T, 2, DB>;
+    if (s.vpt == 4) return norm_bwd_kernel<T, 4, false, DB, 512>;
+    if constexpr (sizeof(T) == 4) return norm_bwd_kernel<T, 8, false, DB, 512>;
     return nullptr;
 }
 template <typename T>
 auto bwd_kernel(const Spread &s, bool db) -> void (*)(NormBwd) {
     if (s.vpt == 0) return norm_bwd_general_kernel<T>;
-    if (s.shift) return db ? bwd_words<T, true, true>(s) : bwd_words<T, true, false>(s);
-    return db ? bwd_words<T, false, true>(s) : bwd_words<T, false, false>(s);
+    return db ? bwd_words<T, true>(s) : bwd_words<T, false>(s);
+}
+// Dynamic shared memory of that kernel: the columns' sums of a block's groups,
+// or the ring, whose memory the sums take when it is drained.
+size_t bwd_smem(const Spread &s, int d, int elem, bool more) {
+    const size_t sums = s.groups > 1 || s.vpt == 0 ? 2 * sizeof(float) * (size_t)d : 0;
+    if (s.vpt == 0 || s.shift || s.vpt > 2) return sums;
+    return std::max(sums, (size_t)s.groups * kRing * (more ? 3 : 2) * (size_t)d * elem);
 }
 
 moe_status check(const moe_norm_config *c) {
@@ -738,7 +909,7 @@ moe_status moe_norm_workspace_size(const moe_norm_config *c, size_t *bytes) {
     if (!bytes) return MOE_ERR_INVALID_ARG;
     const moe_status st = check(c);
     if (st != MOE_OK) return st;
-    *bytes = part_rows(c->T) * 2 * (size_t)c->d * sizeof(float);
+    *bytes = part_rows(*c) * 2 * (size_t)c->d * sizeof(float);
     return MOE_OK;
 }
 
@@ -782,24 +953,25 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     const int E = 16 / elem_size(c->dtype);
     const bool aligned = aligned16(h) && aligned16(weight) && aligned16(dy) && aligned16(dh) && aligned16(dx);
     const Spread sp = spread(c->d, E, aligned, false);
-    if (params && (!ws || ws_bytes < part_rows(c->T) * 2 * (size_t)c->d * sizeof(float) ||
+    if (params && (!ws || ws_bytes < part_rows(*c) * 2 * (size_t)c->d * sizeof(float) ||
                    (reinterpret_cast<uintptr_t>(ws) & 255)))
         return MOE_ERR_WORKSPACE;
-    if (!device_error_word()) return MOE_ERR_CUDA;
+    uint32_t *err = device_error_word();
+    if (!err) return MOE_ERR_CUDA;
     float *part = params ? static_cast<float *>(ws) : nullptr;
     const NormBwd a{h, weight, dy, dh, mean, rstd, dx, part, c->T, c->d, sp.W, sp.groups, c->w_dtype == MOE_F32,
-                    dbias != nullptr};
-    const size_t smem = sp.groups > 1 || sp.vpt == 0 ? 2 * sizeof(float) * (size_t)c->d : 0;
+                    dbias != nullptr, err};
+    const size_t smem = bwd_smem(sp, c->d, elem_size(c->dtype), dh != nullptr);
     auto kern = c->dtype == MOE_BF16  ? bwd_kernel<__nv_bfloat16>(sp, dbias != nullptr)
                 : c->dtype == MOE_F16 ? bwd_kernel<__half>(sp, dbias != nullptr)
                                       : bwd_kernel<float>(sp, dbias != nullptr);
     cudaError_t e = cudaSuccess;
     if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     const int threads = sp.groups * sp.W * 32;
-    const int blocks = blocks_for(sp, c->T, std::min(kBwdBlocks, resident_blocks(kern, threads, smem)));
+    const int blocks = blocks_for(sp, c->T, std::min(bwd_most(c->d), resident_blocks(kern, threads, smem)));
     if (e == cudaSuccess) e = launch_kernel(kern, blocks, threads, smem, s, a);
     if (e == cudaSuccess && params)
-        e = launch_kernel(norm_param_kernel, dim3((c->d + 31) / 32, dbias ? 2 : 1), 1024, 0, s,
+        e = launch_kernel(norm_param_kernel, dim3((c->d + 31) / 32, dbias ? 2 : 1), 32 * kParamWarps, 0, s,
                           static_cast<const float *>(part), blocks, (int)c->d, dweight, dbias);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
