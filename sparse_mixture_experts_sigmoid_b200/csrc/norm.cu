@@ -518,7 +518,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
     if (a.part) write_part<T, VPT, SHIFT, DB>(a, cols, group, c0, cj, dw, db);
 }
 
-// The backward pass of whole-word rows of up to two words a thread.  Its inputs
+// The backward pass of whole-word rows of up to two words a thread (three in a
+// one-warp row without a bias gradient).  Its inputs
 // come through a ring of kRing rows per group in shared memory, each row a bulk
 // copy that one thread requests kRing - 1 rows ahead: with loads into registers
 // (one row ahead, which is all that fits beside the sums) each row waited for
@@ -570,6 +571,9 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(NormBwd a) {
     if (i == 0)
         for (int k = 0; k < kRing - 1; ++k)
             if (r + k * step < a.T) request(r + k * step, k);
+    float2 w[VPT][P];          // this thread's weights, for all its rows
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) load_param<T, false>(a.weight, wf32, c0 + j * cj, d, w[j]);
     float nm[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};   // the statistics of the next two rows
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -587,11 +591,8 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(NormBwd a) {
             if (layer) nm[1] = a.mean[r + 2 * step];
             ns[1] = a.rstd[r + 2 * step];
         }
-        float2 w[VPT][P];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) load_param<T, false>(a.weight, wf32, c0 + j * cj, d, w[j]);
         // a wait that runs out is reported; the pass goes on, so that its barriers end
-        tc::wait_bar(&landed[group][k], phase, &gave_up, a.err);
+        if (!tc::mbar_try_wait(&landed[group][k], phase)) tc::wait_bar(&landed[group][k], phase, &gave_up, a.err);
         const uint4 *h = reinterpret_cast<const uint4 *>(mine + k * stage) + i;
         const uint4 *dy = reinterpret_cast<const uint4 *>(mine + k * stage + bytes) + i;
         float2 z[VPT][P], g[VPT][P];
@@ -785,7 +786,7 @@ __global__ void __launch_bounds__(32 * kParamWarps) norm_param_kernel(const floa
 }
 
 // How a row is spread: VPT words per thread, W warps per row, `groups` rows
-// per block; vpt = 0 is the general kernel.  Of one, two and (forward, whole words) three
+// per block; vpt = 0 is the general kernel.  Of one, two and (`three`, whole words) three
 // words a thread, the one that leaves the fewest words of its warps idle, and
 // of those the one with the fewest warps: one warp needs no barrier.  Four
 // (eight) words where more than 16 warps would be needed.
@@ -793,7 +794,7 @@ struct Spread {
     int vpt, W, groups;
     bool shift;
 };
-Spread spread(int d, int elems, bool aligned, bool forward) {
+Spread spread(int d, int elems, bool aligned, bool three) {
     const bool shift = d % elems != 0;
     const int words = (d + (shift ? elems - 1 : 0) + elems - 1) / elems;
     const int most = (shift ? 2 : (elems == 4 ? 8 : 4)) * 32 * kMaxWarps;
@@ -803,7 +804,7 @@ Spread spread(int d, int elems, bool aligned, bool forward) {
         s.vpt = words <= 128 * kMaxWarps ? 4 : 8;
         s.W = (words + 32 * s.vpt - 1) / (32 * s.vpt);
     } else {
-        for (int v = 1; v <= (forward && !shift && words <= 96 ? 3 : 2); ++v) {
+        for (int v = 1; v <= (three && !shift && words <= 96 ? 3 : 2); ++v) {
             const int w = (words + 32 * v - 1) / (32 * v);
             if (w <= kMaxWarps && (!s.vpt || w * v <= s.W * s.vpt)) {
                 s.vpt = v;
@@ -870,6 +871,8 @@ auto bwd_words(const Spread &s) -> void (*)(NormBwd) {
     }
     if (s.vpt == 1) return norm_bwd_ring_kernel<T, 1, DB>;
     if (s.vpt == 2) return norm_bwd_ring_kernel<T, 2, DB>;
+    if constexpr (!DB)
+        if (s.vpt == 3) return norm_bwd_ring_kernel<T, 3, false>;
     if (s.vpt == 4) return norm_bwd_kernel<T, 4, false, DB, 512>;
     if constexpr (sizeof(T) == 4) return norm_bwd_kernel<T, 8, false, DB, 512>;
     return nullptr;
@@ -883,7 +886,7 @@ auto bwd_kernel(const Spread &s, bool db) -> void (*)(NormBwd) {
 // or the ring, whose memory the sums take when it is drained.
 size_t bwd_smem(const Spread &s, int d, int elem, bool more) {
     const size_t sums = s.groups > 1 || s.vpt == 0 ? 2 * sizeof(float) * (size_t)d : 0;
-    if (s.vpt == 0 || s.shift || s.vpt > 2) return sums;
+    if (s.vpt == 0 || s.shift || s.vpt > 3) return sums;
     return std::max(sums, (size_t)s.groups * kRing * (more ? 3 : 2) * (size_t)d * elem);
 }
 
@@ -952,7 +955,7 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     const bool params = dweight || dbias;
     const int E = 16 / elem_size(c->dtype);
     const bool aligned = aligned16(h) && aligned16(weight) && aligned16(dy) && aligned16(dh) && aligned16(dx);
-    const Spread sp = spread(c->d, E, aligned, false);
+    const Spread sp = spread(c->d, E, aligned, dbias == nullptr);
     if (params && (!ws || ws_bytes < part_rows(*c) * 2 * (size_t)c->d * sizeof(float) ||
                    (reinterpret_cast<uintptr_t>(ws) & 255)))
         return MOE_ERR_WORKSPACE;
