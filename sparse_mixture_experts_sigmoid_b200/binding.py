@@ -163,11 +163,13 @@ def _elem_dtype(cfg: MoEConfig):
     return torch.float32 if cfg.dtype == 1 else torch.bfloat16
 
 
-def _ptr(t: torch.Tensor | None, name: str, shape=None, dtype=None):
+def _ptr(t: torch.Tensor | None, name: str, shape=None, dtype=None, dev=None):
     if t is None:
         return None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, it is on {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -177,9 +179,16 @@ def _ptr(t: torch.Tensor | None, name: str, shape=None, dtype=None):
     return t.data_ptr()
 
 
+def _here(t: torch.Tensor):
+    """The current device, for _ptr to hold the tensors of a call to (a host tensor is refused there)."""
+    return torch.cuda.current_device() if t.is_cuda else None
+
+
 def _stream(stream=None):
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # torch.cuda.current_stream().cuda_stream without the Stream object (3 us of a small call's 17)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def validate(cfg: MoEConfig) -> int:
@@ -634,16 +643,17 @@ def norm_forward(cfg: NormConfig, x, weight, bias=None, residual=None, y=None, h
     """moe_norm_forward: (y[T,d], h[T,d] | None, mean[T] | None, rstd[T] | None).  h = x + residual with a
     residual (allocated unless given); mean (layer norm) and rstd with want_stats."""
     dt, wt = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype]
-    rows, dev = (cfg.T, cfg.d), x.device
+    rows, dev = (cfg.T, cfg.d), _here(x)
+    px = _ptr(x, "x", rows, dt, dev)
     if y is None:
-        y = torch.empty(rows, dtype=dt, device=dev)
+        y = torch.empty_like(x)
     if h is None and residual is not None:
-        h = torch.empty(rows, dtype=dt, device=dev)
-    mean = torch.empty(cfg.T, dtype=torch.float32, device=dev) if want_stats and cfg.kind == 0 else None
-    rstd = torch.empty(cfg.T, dtype=torch.float32, device=dev) if want_stats else None
-    _check(lib().moe_norm_forward(ctypes.byref(cfg), _ptr(x, "x", rows, dt), _ptr(residual, "residual", rows, dt),
-                                  _ptr(weight, "weight", (cfg.d,), wt), _ptr(bias, "bias", (cfg.d,), wt),
-                                  _ptr(h, "h", rows, dt), _ptr(y, "y", rows, dt), _ptr(mean, "mean"),
+        h = torch.empty_like(x)
+    mean = x.new_empty(cfg.T, dtype=torch.float32) if want_stats and cfg.kind == 0 else None
+    rstd = x.new_empty(cfg.T, dtype=torch.float32) if want_stats else None
+    _check(lib().moe_norm_forward(ctypes.byref(cfg), px, _ptr(residual, "residual", rows, dt, dev),
+                                  _ptr(weight, "weight", (cfg.d,), wt, dev), _ptr(bias, "bias", (cfg.d,), wt, dev),
+                                  _ptr(h, "h", rows, dt, dev), _ptr(y, "y", rows, dt, dev), _ptr(mean, "mean"),
                                   _ptr(rstd, "rstd"), _stream(stream)), "moe_norm_forward")
     return y, h, mean, rstd
 
@@ -654,19 +664,21 @@ def norm_backward(cfg: NormConfig, h, weight, mean, rstd, dy, dh=None, dx=None, 
     normalised; mean (None for an RMS norm) and rstd from norm_forward; dh: the gradient that reaches h by other
     paths, added to dx."""
     dt, wt = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype]
-    rows, dev = (cfg.T, cfg.d), h.device
+    rows, dev = (cfg.T, cfg.d), _here(h)
+    ph = _ptr(h, "h", rows, dt, dev)
     if dx is None:
-        dx = torch.empty(rows, dtype=dt, device=dev)
-    dweight = torch.empty(cfg.d, dtype=torch.float32, device=dev) if want_weight else None
-    dbias = torch.empty(cfg.d, dtype=torch.float32, device=dev) if want_bias else None
+        dx = torch.empty_like(h)
+    dweight = h.new_empty(cfg.d, dtype=torch.float32) if want_weight else None
+    dbias = h.new_empty(cfg.d, dtype=torch.float32) if want_bias else None
     if ws is None and (want_weight or want_bias):
-        ws = torch.empty(max(norm_workspace_size(cfg), 1), dtype=torch.uint8, device=dev)
-    _check(lib().moe_norm_backward(ctypes.byref(cfg), _ptr(h, "h", rows, dt), _ptr(weight, "weight", (cfg.d,), wt),
-                                   _ptr(mean, "mean", (cfg.T,), torch.float32),
-                                   _ptr(rstd, "rstd", (cfg.T,), torch.float32), _ptr(dy, "dy", rows, dt),
-                                   _ptr(dh, "dh", rows, dt), _ptr(dx, "dx", rows, dt), _ptr(dweight, "dweight"),
-                                   _ptr(dbias, "dbias"), _ptr(ws, "ws", dtype=torch.uint8),
-                                   0 if ws is None else ws.numel(), _stream(stream)), "moe_norm_backward")
+        ws = h.new_empty(max(norm_workspace_size(cfg), 1), dtype=torch.uint8)
+    f32 = torch.float32
+    _check(lib().moe_norm_backward(ctypes.byref(cfg), ph, _ptr(weight, "weight", (cfg.d,), wt, dev),
+                                   _ptr(mean, "mean", (cfg.T,), f32, dev), _ptr(rstd, "rstd", (cfg.T,), f32, dev),
+                                   _ptr(dy, "dy", rows, dt, dev), _ptr(dh, "dh", rows, dt, dev),
+                                   _ptr(dx, "dx", rows, dt, dev), _ptr(dweight, "dweight"), _ptr(dbias, "dbias"),
+                                   _ptr(ws, "ws", dtype=torch.uint8, dev=dev), 0 if ws is None else ws.numel(),
+                                   _stream(stream)), "moe_norm_backward")
     return dx, dweight, dbias
 
 
@@ -692,20 +704,22 @@ def alloc_ffn_workspace(cfg: FfnConfig, train: bool = False, device=None) -> tor
 
 
 def _ffn_forward(name, cfg, x, w_gate, w_up, w_down, y, ws, stream):
-    dt = _TORCH_DTYPES[cfg.dtype]
+    dt, T, d, h = _TORCH_DTYPES[cfg.dtype], cfg.T, cfg.d, cfg.h
+    dev = _here(x)
+    px = _ptr(x, "x", (T, d), dt, dev)
     if y is None:
-        y = torch.empty(cfg.T, cfg.d, dtype=dt, device=x.device)
-    _check(getattr(lib(), name)(ctypes.byref(cfg), _ptr(x, "x", (cfg.T, cfg.d), dt),
-                                _ptr(w_gate, "w_gate", (cfg.h, cfg.d), dt), _ptr(w_up, "w_up", (cfg.h, cfg.d), dt),
-                                _ptr(w_down, "w_down", (cfg.d, cfg.h), dt), _ptr(y, "y", (cfg.T, cfg.d), dt),
-                                _ptr(ws, "ws", dtype=torch.uint8), ws.numel(), _stream(stream)), name)
+        y = torch.empty_like(x)
+    if ws is None:
+        ws = alloc_ffn_workspace(cfg, device=x.device)
+    _check(getattr(lib(), name)(ctypes.byref(cfg), px, _ptr(w_gate, "w_gate", (h, d), dt, dev),
+                                _ptr(w_up, "w_up", (h, d), dt, dev), _ptr(w_down, "w_down", (d, h), dt, dev),
+                                _ptr(y, "y", (T, d), dt, dev), _ptr(ws, "ws", dtype=torch.uint8, dev=dev), ws.numel(),
+                                _stream(stream)), name)
     return y
 
 
 def ffn_forward(cfg: FfnConfig, x, w_gate, w_up, w_down, y=None, ws=None, stream=None):
     """moe_ffn_forward: y[T,d] of the dense gated block (allocated unless given); ws is allocated if not given."""
-    if ws is None:
-        ws = alloc_ffn_workspace(cfg, device=x.device)
     return _ffn_forward("moe_ffn_forward", cfg, x, w_gate, w_up, w_down, y, ws, stream)
 
 
@@ -717,15 +731,19 @@ def ffn_forward_train(cfg: FfnConfig, x, w_gate, w_up, w_down, ws, y=None, strea
 def ffn_backward(cfg: FfnConfig, x, w_gate, w_up, w_down, dy, ws, grads=None, stream=None) -> dict:
     """moe_ffn_backward after ffn_forward_train(cfg, x, ..., ws): the gradients dx, dw_gate, dw_up and dw_down, all
     allocated, or those that ``grads`` holds (one that is absent or None there is not computed)."""
-    dt = _TORCH_DTYPES[cfg.dtype]
-    shapes = {"dx": (cfg.T, cfg.d), "dw_gate": (cfg.h, cfg.d), "dw_up": (cfg.h, cfg.d), "dw_down": (cfg.d, cfg.h)}
+    dt, T, d, h = _TORCH_DTYPES[cfg.dtype], cfg.T, cfg.d, cfg.h
+    dev, rows, up, down = _here(x), (T, d), (h, d), (d, h)
+    px, pdy = _ptr(x, "x", rows, dt, dev), _ptr(dy, "dy", rows, dt, dev)
+    pg, pu, pd = (_ptr(w_gate, "w_gate", up, dt, dev), _ptr(w_up, "w_up", up, dt, dev),
+                  _ptr(w_down, "w_down", down, dt, dev))
     if grads is None:
-        grads = {n: torch.empty(s, dtype=dt, device=dy.device) for n, s in shapes.items()}
-    _check(lib().moe_ffn_backward(ctypes.byref(cfg), _ptr(x, "x", shapes["dx"], dt),
-                                  _ptr(w_gate, "w_gate", shapes["dw_gate"], dt), _ptr(w_up, "w_up", shapes["dw_up"], dt),
-                                  _ptr(w_down, "w_down", shapes["dw_down"], dt), _ptr(dy, "dy", shapes["dx"], dt),
-                                  _ptr(ws, "ws", dtype=torch.uint8), ws.numel(),
-                                  *(_ptr(grads.get(n), n, s, dt) for n, s in shapes.items()), _stream(stream)),
+        grads = {"dx": torch.empty_like(x), "dw_gate": torch.empty_like(w_gate), "dw_up": torch.empty_like(w_up),
+                 "dw_down": torch.empty_like(w_down)}
+    _check(lib().moe_ffn_backward(ctypes.byref(cfg), px, pg, pu, pd, pdy, _ptr(ws, "ws", dtype=torch.uint8, dev=dev),
+                                  ws.numel(), _ptr(grads.get("dx"), "dx", rows, dt, dev),
+                                  _ptr(grads.get("dw_gate"), "dw_gate", up, dt, dev),
+                                  _ptr(grads.get("dw_up"), "dw_up", up, dt, dev),
+                                  _ptr(grads.get("dw_down"), "dw_down", down, dt, dev), _stream(stream)),
            "moe_ffn_backward")
     return grads
 
@@ -746,11 +764,14 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, stream=None):
     [ceil(rows / block_rows), ceil(cols / 128)]).  block_rows: 1 (activations) or 128 (weights)."""
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {x.dim()}")
+    if block_rows not in (1, 128):
+        raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
+    code, px = _dtype_code(x, "x"), _ptr(x, "x", dev=_here(x))
     rows, cols = x.shape
-    q = torch.empty(rows, cols, dtype=torch.float8_e4m3fn, device=x.device)
-    sc = torch.empty(-(-rows // max(block_rows, 1)), -(-cols // 128), dtype=torch.float32, device=x.device)
-    _check(lib().moe_quantize_fp8(_ptr(x, "x"), _dtype_code(x, "x"), rows, cols, int(block_rows), _ptr(q, "q"),
-                                  _ptr(sc, "scales"), _stream(stream)), "moe_quantize_fp8")
+    q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
+    sc = x.new_empty((-(-rows // block_rows), -(-cols // 128)), dtype=torch.float32)
+    _check(lib().moe_quantize_fp8(px, code, rows, cols, block_rows, q.data_ptr(), sc.data_ptr(), _stream(stream)),
+           "moe_quantize_fp8")
     return q, sc
 
 
@@ -759,10 +780,12 @@ def gemm_fp8(a, a_scales, b, b_scales, out_dtype="bf16", out=None, stream=None):
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b must have two dimensions")
     (M, K), N = a.shape, b.shape[0]
-    kb, f8 = -(-K // 128), torch.float8_e4m3fn
+    kb, f8, f32 = -(-K // 128), torch.float8_e4m3fn, torch.float32
     if out is None:
-        out = torch.empty(M, N, dtype=_TORCH_DTYPES[_choice(DTYPES, out_dtype, "out_dtype")], device=a.device)
-    _check(lib().moe_gemm_fp8(M, N, K, _ptr(a, "a", (M, K), f8), _ptr(a_scales, "a_scales", (M, kb), torch.float32),
-                              _ptr(b, "b", (N, K), f8), _ptr(b_scales, "b_scales", (-(-N // 128), kb), torch.float32),
-                              _ptr(out, "out", (M, N)), _dtype_code(out, "out"), _stream(stream)), "moe_gemm_fp8")
+        out = a.new_empty((M, N), dtype=_TORCH_DTYPES[_choice(DTYPES, out_dtype, "out_dtype")])
+    dev = _here(a)
+    _check(lib().moe_gemm_fp8(M, N, K, _ptr(a, "a", (M, K), f8, dev), _ptr(a_scales, "a_scales", (M, kb), f32, dev),
+                              _ptr(b, "b", (N, K), f8, dev), _ptr(b_scales, "b_scales", (-(-N // 128), kb), f32, dev),
+                              _ptr(out, "out", (M, N), None, dev), _dtype_code(out, "out"), _stream(stream)),
+           "moe_gemm_fp8")
     return out
