@@ -22,15 +22,34 @@ namespace moe {
 namespace fp8 {
 namespace {
 
-// Eight consecutive elements as fp32.
-__device__ __forceinline__ void load8_any(const void *p, int dtype, int64_t i, float (&v)[8]) {
+// Eight consecutive elements as they lie in memory (16 bytes, or 32 of fp32).
+struct Raw {
+    uint4 a, b;
+};
+__device__ __forceinline__ Raw load_raw(const void *p, int dtype, int64_t i) {
+    Raw r;
     if (dtype == MOE_F32) {
-        load8(static_cast<const float *>(p) + i, v);
-    } else if (dtype == MOE_BF16) {
-        load8(static_cast<const __nv_bfloat16 *>(p) + i, v);
+        const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(p) + i);
+        r.a = q[0];
+        r.b = q[1];
     } else {
-        const uint4 u = *reinterpret_cast<const uint4 *>(static_cast<const __half *>(p) + i);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        r.a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+        r.b = make_uint4(0, 0, 0, 0);
+    }
+    return r;
+}
+__device__ __forceinline__ void values_of(const Raw &r, int dtype, float (&v)[8]) {
+    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
+    if (dtype == MOE_F32) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+    } else if (dtype == MOE_BF16) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            v[2 * j] = __uint_as_float(w[j] << 16);
+            v[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
+        }
+    } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[j]));
@@ -39,29 +58,63 @@ __device__ __forceinline__ void load8_any(const void *p, int dtype, int64_t i, f
         }
     }
 }
-
-__device__ __forceinline__ uint32_t max_bits(const float (&v)[8], uint32_t m) {
+// The largest magnitude's bits: a NaN is above every number.  16-bit types are
+// compared two at a time in their own bits (their order is that of the values).
+__device__ __forceinline__ uint32_t max_bits(const Raw &r, int dtype, uint32_t m) {
+    if (dtype == MOE_F32) {
+        const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    return m;
+        for (int j = 0; j < 8; ++j) m = max(m, w[j] & 0x7fffffffu);
+        return m;
+    }
+    constexpr uint32_t k = 0x7fff7fffu;
+    return __vmaxu2(m, __vmaxu2(__vmaxu2(r.a.x & k, r.a.y & k), __vmaxu2(r.a.z & k, r.a.w & k)));
 }
-__device__ __forceinline__ float scale_of(uint32_t bits) { return __fdiv_rn(__uint_as_float(bits), 448.f); }
+// The magnitude as fp32 from what max_bits left, after the lanes have met.
+__device__ __forceinline__ float magnitude(uint32_t m, int dtype) {
+    if (dtype == MOE_F32) return __uint_as_float(m);
+    m = max(m & 0xffffu, m >> 16);
+    if (dtype == MOE_BF16) return __uint_as_float(m << 16);
+    return __half2float(__ushort_as_half((unsigned short)m));
+}
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b, int dtype) {
+    return dtype == MOE_F32 ? max(a, b) : __vmaxu2(a, b);
+}
 
 // The codes of eight elements.  A scale of zero (a block of zeros, or of
-// magnitudes whose scale underflows) or NaN gives zeros.
+// magnitudes whose scale underflows) or NaN gives zeros.  For scales away from
+// the ends of the range the quotient x / s comes from r = 1 / s, rounded to
+// nearest, and one correction by the exact remainder x - (x r) s, which gives the
+// correctly rounded quotient (Markstein's theorem, IBM J. Res. Dev. 34, 1990;
+// its exception, a divisor whose significand is all ones, is divided): three
+// operations an element where the division took the kernel's time (19 us for
+// 4096 x 4096).
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
-    const bool ok = s > 0.f;
+    float q[8];
+    const uint32_t sb = __float_as_uint(s);
+    if (s >= 0x1p-60f && s <= 0x1p60f && (sb & 0x7fffffu) != 0x7fffffu) {
+        const float r = __frcp_rn(s);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float q0 = v[i] * r;
+            q[i] = fmaf(fmaf(-q0, s, v[i]), r, q0);
+        }
+    } else {
+        const bool ok = s > 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q[i] = ok ? __fdiv_rn(v[i], s) : 0.f;
+    }
     uint32_t w[2] = {0, 0};
 #pragma unroll
-    for (int i = 0; i < 8; i += 2) {
-        const float2 f = ok ? make_float2(__fdiv_rn(v[i], s), __fdiv_rn(v[i + 1], s)) : make_float2(0.f, 0.f);
-        w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3) << (8 * (i & 2));
-    }
+    for (int i = 0; i < 8; i += 2)
+        w[i >> 2] |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(q[i], q[i + 1]), __NV_SATFINITE, __NV_E4M3)
+                     << (8 * (i & 2));
     return make_uint2(w[0], w[1]);
 }
 
 // 1 x 128 blocks: sixteen lanes per block, eight elements a lane.
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const void *x, int dtype, int64_t rows, int cols, int kb,
+template <int dtype>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const void *x, int64_t rows, int cols, int kb,
                                                             uint8_t *q, float *scales) {
     pdl_wait();
     pdl_launch_dependents();
@@ -73,19 +126,22 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const void *x, int d
         const int64_t r = b / kb;
         const int c = (int)(b - r * kb) * kBlock + l * 8;
         const bool in = b < total && c < cols;
-        float v[8] = {};
-        if (in) load8_any(x, dtype, r * cols + c, v);
-        uint32_t m = max_bits(v, 0);
+        Raw raw{};
+        if (in) raw = load_raw(x, dtype, r * cols + c);
+        uint32_t m = max_bits(raw, dtype, 0);
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const float s = scale_of(m);
+        for (int o = 8; o > 0; o >>= 1) m = max_pair(m, __shfl_xor_sync(0xffffffffu, m, o), dtype);
+        const float s = __fdiv_rn(magnitude(m, dtype), 448.f);
+        float v[8];
+        values_of(raw, dtype, v);
         if (in) *reinterpret_cast<uint2 *>(q + r * cols + c) = codes8(v, s);
         if (b < total && l == 0) scales[b] = s;
     }
 }
 
 // 128 x 128 blocks: one CTA per block, eight 16-byte pieces of 16-bit elements a thread.
-__global__ void __launch_bounds__(256) quantize_square_kernel(const void *x, int dtype, int64_t rows, int cols, int kb,
+template <int dtype>
+__global__ void __launch_bounds__(256) quantize_square_kernel(const void *x, int64_t rows, int cols, int kb,
                                                               uint8_t *q, float *scales) {
     __shared__ uint32_t part[8];
     pdl_wait();
@@ -94,26 +150,31 @@ __global__ void __launch_bounds__(256) quantize_square_kernel(const void *x, int
     const int bc = (int)(blockIdx.x - br * kb);
     const int c = bc * kBlock + (threadIdx.x & 15) * 8;
     const int64_t r0 = br * kBlock + (threadIdx.x >> 4);
-    float v[8][8];
+    Raw raw[8];
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int64_t r = r0 + 16 * j;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[j][i] = 0.f;
-        if (r < rows && c < cols) load8_any(x, dtype, r * cols + c, v[j]);
-        m = max_bits(v[j], m);
+        raw[j] = Raw{};
+        if (r < rows && c < cols) raw[j] = load_raw(x, dtype, r * cols + c);
     }
-    m = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = max_bits(raw[j], dtype, m);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = max_pair(m, __shfl_xor_sync(0xffffffffu, m, o), dtype);
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
     __syncthreads();
 #pragma unroll
-    for (int j = 0; j < 8; ++j) m = max(m, part[j]);
-    const float s = scale_of(m);
+    for (int j = 0; j < 8; ++j) m = max_pair(m, part[j], dtype);
+    const float s = __fdiv_rn(magnitude(m, dtype), 448.f);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int64_t r = r0 + 16 * j;
-        if (r < rows && c < cols) *reinterpret_cast<uint2 *>(q + r * cols + c) = codes8(v[j], s);
+        if (r < rows && c < cols) {
+            float v[8];
+            values_of(raw[j], dtype, v);
+            *reinterpret_cast<uint2 *>(q + r * cols + c) = codes8(v, s);
+        }
     }
     if (threadIdx.x == 0) scales[blockIdx.x] = s;
 }
@@ -144,11 +205,16 @@ moe_status moe_quantize_fp8(const void *x, int32_t dtype, int64_t rows, int32_t 
     cudaError_t e;
     if (block_rows == 1) {
         const int64_t want = (rows * kb + 15) / 16;
-        e = launch_kernel(quantize_rows_kernel, (unsigned)std::min<int64_t>(want, 16LL * num_sms()), 256, 0, s, x,
-                          (int)dtype, rows, (int)cols, kb, q, scales);
+        auto kern = dtype == MOE_BF16  ? quantize_rows_kernel<MOE_BF16>
+                    : dtype == MOE_F16 ? quantize_rows_kernel<MOE_F16>
+                                       : quantize_rows_kernel<MOE_F32>;
+        e = launch_kernel(kern, (unsigned)std::min<int64_t>(want, 16LL * num_sms()), 256, 0, s, x, rows, (int)cols, kb,
+                          q, scales);
     } else {
-        e = launch_kernel(quantize_square_kernel, (unsigned)blocks, 256, 0, s, x, (int)dtype, rows, (int)cols, kb, q,
-                          scales);
+        auto kern = dtype == MOE_BF16  ? quantize_square_kernel<MOE_BF16>
+                    : dtype == MOE_F16 ? quantize_square_kernel<MOE_F16>
+                                       : quantize_square_kernel<MOE_F32>;
+        e = launch_kernel(kern, (unsigned)blocks, 256, 0, s, x, rows, (int)cols, kb, q, scales);
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -95,6 +95,22 @@ def test_quantiser_is_the_host_s(dtype, rows, cols, br):
 
 
 @pytest.mark.gpu
+def test_quantiser_s_quotients_are_rounded_once():
+    """A million quotients of ordinary and extreme scales, bit for bit: ties of the code, and quotients next to them."""
+    g = torch.Generator().manual_seed(11)
+    rows = 8192
+    x = torch.randn(rows, 128, generator=g) * torch.exp2(torch.randint(-80, 80, (rows, 1), generator=g).float())
+    ties = torch.randint(8, 31, (rows, 40), generator=g).float() + 0.5        # halfway between two codes of a binade
+    x[:, 1:41] = ties * torch.exp2(torch.randint(-6, 4, (rows, 40), generator=g).float()) * (x[:, :1].abs() / 448)
+    x[:, 0] = x.abs().amax(1)
+    x[::7, 0] = x[::7, 0].view(torch.int32).bitwise_or(0x7fffff).view(torch.float32)   # significands of all ones
+    q, s = B.quantize_fp8(x.cuda(), 1)
+    s0 = x.abs().amax(1, keepdim=True) / torch.tensor(448.0)
+    q0 = (x / s0).clamp(-448, 448).to(F8)
+    assert torch.equal(s.cpu(), s0) and same_bits(q, q0)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("br", [1, 128])
 def test_quantiser_at_the_edges_of_the_numbers(br):
     """Zeros, magnitudes whose scale underflows or is subnormal, the type's largest, infinities and NaN: of one block each."""
