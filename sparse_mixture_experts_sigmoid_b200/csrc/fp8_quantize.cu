@@ -112,30 +112,50 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float s) {
     return make_uint2(w[0], w[1]);
 }
 
-// 1 x 128 blocks: sixteen lanes per block, eight elements a lane.
+// 1 x 128 blocks: sixteen lanes per block, eight elements a lane, and kPairs
+// pairs of blocks a warp whose loads are all in flight before the first is
+// reduced.  Rows of whole blocks lie end to end, block b at element 128 b;
+// otherwise a block's place takes a division.
+constexpr int kPairs = 4;
 template <int dtype>
-__global__ void __launch_bounds__(256) quantize_rows_kernel(const void *x, int64_t rows, int cols, int kb,
-                                                            uint8_t *q, float *scales) {
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const void *x, int64_t rows, int cols, int kb, uint8_t *q,
+                                                            float *scales) {
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t total = rows * kb, step = (int64_t)gridDim.x * 16;
+    const int64_t total = rows * kb, step = (int64_t)gridDim.x * 16 * kPairs;
     const int l = threadIdx.x & 15;
-    // whole warps stay in the loop: the two blocks of a warp reduce together
-    for (int64_t b0 = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 5) * 2; b0 < total; b0 += step) {
-        const int64_t b = b0 + ((threadIdx.x >> 4) & 1);
-        const int64_t r = b / kb;
-        const int c = (int)(b - r * kb) * kBlock + l * 8;
-        const bool in = b < total && c < cols;
-        Raw raw{};
-        if (in) raw = load_raw(x, dtype, r * cols + c);
-        uint32_t m = max_bits(raw, dtype, 0);
+    const bool flat = cols % kBlock == 0;
+    // whole warps stay in the loop: the two blocks of a pair reduce together
+    for (int64_t b0 = ((int64_t)blockIdx.x * 8 + (threadIdx.x >> 5)) * 2 * kPairs; b0 < total; b0 += step) {
+        Raw raw[kPairs];
+        int64_t at[kPairs];   // this lane's elements; -1: none
 #pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max_pair(m, __shfl_xor_sync(0xffffffffu, m, o), dtype);
-        const float s = __fdiv_rn(magnitude(m, dtype), 448.f);
-        float v[8];
-        values_of(raw, dtype, v);
-        if (in) *reinterpret_cast<uint2 *>(q + r * cols + c) = codes8(v, s);
-        if (b < total && l == 0) scales[b] = s;
+        for (int j = 0; j < kPairs; ++j) {
+            const int64_t b = b0 + 2 * j + ((threadIdx.x >> 4) & 1);
+            at[j] = b * kBlock + l * 8;
+            bool in = b < total;
+            if (!flat) {
+                const int64_t r = b / kb;
+                const int c = (int)(b - r * kb) * kBlock + l * 8;
+                at[j] = r * cols + c;
+                in = in && c < cols;
+            }
+            raw[j] = Raw{};
+            if (in) raw[j] = load_raw(x, dtype, at[j]);
+            else at[j] = -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kPairs; ++j) {
+            uint32_t m = max_bits(raw[j], dtype, 0);
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) m = max_pair(m, __shfl_xor_sync(0xffffffffu, m, o), dtype);
+            const float s = __fdiv_rn(magnitude(m, dtype), 448.f);
+            float v[8];
+            values_of(raw[j], dtype, v);
+            if (at[j] >= 0) *reinterpret_cast<uint2 *>(q + at[j]) = codes8(v, s);
+            const int64_t b = b0 + 2 * j + ((threadIdx.x >> 4) & 1);
+            if (b < total && l == 0) scales[b] = s;
+        }
     }
 }
 
@@ -204,11 +224,11 @@ moe_status moe_quantize_fp8(const void *x, int32_t dtype, int64_t rows, int32_t 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (block_rows == 1) {
-        const int64_t want = (rows * kb + 15) / 16;
+        const int64_t want = (rows * kb + 16 * kPairs - 1) / (16 * kPairs);
         auto kern = dtype == MOE_BF16  ? quantize_rows_kernel<MOE_BF16>
                     : dtype == MOE_F16 ? quantize_rows_kernel<MOE_F16>
                                        : quantize_rows_kernel<MOE_F32>;
-        e = launch_kernel(kern, (unsigned)std::min<int64_t>(want, 16LL * num_sms()), 256, 0, s, x, rows, (int)cols, kb,
+        e = launch_kernel(kern, (unsigned)std::min<int64_t>(want, 1 << 30), 256, 0, s, x, rows, (int)cols, kb,
                           q, scales);
     } else {
         auto kern = dtype == MOE_BF16  ? quantize_square_kernel<MOE_BF16>
