@@ -222,7 +222,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
             }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0 && lead) {
+        if (lead) {   // the whole warp: one lane's instructions take effect
+            const bool mine = lane == 0;
             const uint32_t idesc = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) | ((uint32_t)A_MN << 15) |
                                    ((uint32_t)B_MN << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
             uint32_t it = 0, tc = 0;
@@ -235,10 +236,8 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
                 for (int kb = 0; kb < nk; ++kb, ++it) {
                     const int s = it % kStages;
                     const uint32_t ph = (it / kStages) & 1;
-                    // the operands of both CTAs have landed (acquire at cluster scope)
-                    bool got = mbar_try_wait_cluster(&ctrl->full[s], ph);
-                    if (!got) got = wait_bar(&ctrl->full[s], ph, abort, p.err) && mbar_try_wait_cluster(&ctrl->full[s], ph);
-                    if (!got) {
+                    // the operands of both CTAs have landed
+                    if (!mbar_try_wait(&ctrl->full[s], ph) && !wait_bar(&ctrl->full[s], ph, abort, p.err)) {
                         ok = false;
                         break;
                     }
@@ -249,13 +248,13 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
                                                  : smem_desc(sA + s * kAStage) + 2 * kk;
                         const uint64_t bd = B_MN ? desc_mn(sB + s * kBStage + kk * 2048)
                                                  : smem_desc(sB + s * kBStage) + 2 * kk;
-                        mma2<__nv_bfloat16>(d, ad, bd, idesc, (kb | kk) != 0);
+                        mma_if<2, kF16>(mine, d, ad, bd, idesc, (kb | kk) != 0);
                     }
-                    mma_commit2(&ctrl->empty[s], 0x3);
+                    mma_commit2_if(mine, &ctrl->empty[s], 0x3);
                 }
-                if (ok) mma_commit2(&ctrl->tfull[acc], 0x3);
+                if (ok) mma_commit2_if(mine, &ctrl->tfull[acc], 0x3);
             }
-            mma_commit2(&ctrl->done, 0x3);
+            mma_commit2_if(mine, &ctrl->done, 0x3);
         }
     } else {
         const uint32_t tempty_lead = mapa_shared(&ctrl->tempty[0], 0);
@@ -458,13 +457,30 @@ cudaError_t launch(const Gemm &g, cudaStream_t s) {
     return launch_kernel_pair(kern, 2 * pairs, kThreads, smem, s, maps, p);
 }
 
+// Whether tiles of 128 columns end sooner than tiles of 256: their rounds over
+// the pairs, at (per K block) 512 and 256 cycles of MMA and a tile's fixed cost.
+// The narrow tiles read half as much again per product, which does not show
+// while few pairs are at work; for full rounds the wide ones win.
+bool narrow_tiles(const Gemm &g) {
+    const int64_t pairs = num_sms() / 2, mt = (g.M + kBM - 1) / kBM * g.halves;
+    const int64_t nk = (int64_t)g.ranges * ((g.K + kBK - 1) / kBK);
+    auto rounds = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
+    return rounds(128) * (nk * 290 + 2000) < rounds(256) * (nk * 512 + 3000);
+}
+
 }  // namespace
 
 cudaError_t launch_pair_gemm(const Gemm &g, cudaStream_t s) {
     switch (g.kind) {
         case GATED: return launch<false, false, GATED, 256>(g, s);
-        case DGATED: return launch<false, true, DGATED, 256>(g, s);
+        case DGATED:
+            return narrow_tiles(g) ? launch<false, true, DGATED, 128>(g, s) : launch<false, true, DGATED, 256>(g, s);
         default:
+            if (narrow_tiles(g)) {
+                if (g.a_mn) return launch<true, true, STORE, 128>(g, s);
+                if (g.b_mn) return launch<false, true, STORE, 128>(g, s);
+                return launch<false, false, STORE, 128>(g, s);
+            }
             if (g.a_mn) return launch<true, true, STORE, 256>(g, s);
             if (g.b_mn) return launch<false, true, STORE, 256>(g, s);
             return launch<false, false, STORE, 256>(g, s);

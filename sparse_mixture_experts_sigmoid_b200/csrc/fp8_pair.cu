@@ -63,14 +63,6 @@ struct Params {
     uint32_t *err;
 };
 
-__device__ __forceinline__ void mma2_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int c0, int c1) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
                  ::"l"(reinterpret_cast<uint64_t>(m)), "r"(c0), "r"(c1), "r"(smem_u32(src))
@@ -220,7 +212,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         } else if (warp == kMmaWarp) {
-            if (lane == 0 && lead) {
+            if (lead) {   // the whole warp: one lane's instructions take effect
+                const bool mine = lane == 0;
                 // e4m3 A and B (format 0), fp32 D, both K-major
                 constexpr uint32_t kIdesc = (1u << 4) | ((uint32_t)(kBN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
                 uint32_t it = 0;
@@ -233,21 +226,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                             ok = false;
                             break;
                         }
-                        bool got = mbar_try_wait_cluster(&ctrl->full[s], ph);
-                        if (!got) got = wait_here(&ctrl->full[s], ph, abort, p.err) && mbar_try_wait_cluster(&ctrl->full[s], ph);
-                        if (!got) {
+                        if (!wait_here(&ctrl->full[s], ph, abort, p.err)) {
                             ok = false;
                             break;
                         }
                         tc_fence_after();
                         const uint64_t ad = smem_desc(sA + s * kStage), bd = smem_desc(sB + s * kStage);
     #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) mma2_fp8(tmem + acc * kBN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk != 0);
-                        mma_commit2(&ctrl->empty[s], 0x3);
-                        mma_commit2(&ctrl->tfull[acc], 0x3);
+                        for (int kk = 0; kk < 4; ++kk) mma_if<2, kF8>(mine, tmem + acc * kBN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk != 0);
+                        mma_commit2_if(mine, &ctrl->empty[s], 0x3);
+                        mma_commit2_if(mine, &ctrl->tfull[acc], 0x3);
                     }
                 }
-                mma_commit2(&ctrl->done, 0x3);
+                mma_commit2_if(mine, &ctrl->done, 0x3);
             }
         }
     } else {

@@ -67,14 +67,6 @@ struct Params {
     uint32_t *err;
 };
 
-__device__ __forceinline__ void mma_fp8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}"
-        ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-}
 // Four floats of the shared memory of CTA `rank` of the cluster, at this CTA's address p.
 __device__ __forceinline__ float4 ld_cluster4(const float *p, uint32_t rank) {
     float4 v;
@@ -215,7 +207,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
         }
     } else if (warp == kMmaWarp) {
-        if (lane == 0) {
+        {   // the whole warp: one lane's instructions take effect
+            const bool mine = lane == 0;
             const uint32_t fmt = FP8 ? 0u : p.fmt;
             const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(NT >> 3) << 17) |
                                    ((uint32_t)(kRows >> 4) << 24);
@@ -235,14 +228,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const uint64_t ad = smem_desc(sW + s * kWStage), bd = smem_desc(sX + s * kXStage);
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk) {
-                    if constexpr (FP8) mma_fp8(d, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0);
-                    else mma<__nv_bfloat16>(d, ad + 2 * kk, bd + 2 * kk, idesc, (kb | kk) != 0);
+                    mma_if<1, FP8 ? kF8 : kF16>(mine, d, ad + 2 * kk, bd + 2 * kk, idesc, (FP8 ? kk : kb | kk) != 0);
                 }
-                mma_commit(&ctrl->empty[s]);
-                if (FP8) mma_commit(&ctrl->tfull[kb & 1]);
+                mma_commit_if(mine, &ctrl->empty[s]);
+                if (FP8) mma_commit_if(mine, &ctrl->tfull[kb & 1]);
             }
             // the sums are complete; aborting: this arrival follows whatever was issued
-            if (!FP8 || !ok) mma_commit(&ctrl->tfull[0]);
+            if (!FP8 || !ok) mma_commit_if(mine, &ctrl->tfull[0]);
         }
     } else {
         const uint32_t tb = tmem + ((uint32_t)(warp * 32) << 16);

@@ -308,6 +308,46 @@ __device__ __forceinline__ void tma_load_3d_pair(const CUtensorMap *m, void *dst
         : "memory");
 }
 
+// ---- issue by a whole warp: every lane runs the issuing loop and `mine` (set
+// in one lane) predicates the instruction itself.  The descriptors then stay in
+// uniform registers; issued from inside a one-lane branch, each MMA first moves
+// its operands there, which measured ~125 cycles an MMA.
+enum MmaKind : int { kF16 = 0, kF8 = 1 };
+template <int GROUP, int KIND>
+__device__ __forceinline__ void mma_if(bool mine, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                       uint32_t acc) {
+#define MOE_MMA_IF(FORM)                                             \
+    asm volatile(                                                    \
+        "{\n\t.reg .pred p, q;\n\t"                                  \
+        "setp.ne.b32 p, %4, 0;\n\t"                                  \
+        "setp.ne.b32 q, %5, 0;\n\t"                                  \
+        "@q tcgen05.mma." FORM " [%0], %1, %2, %3, p;\n\t}"          \
+        ::"r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc), "r"((uint32_t)mine) \
+        : "memory")
+    if constexpr (GROUP == 2 && KIND == kF16) MOE_MMA_IF("cta_group::2.kind::f16");
+    else if constexpr (GROUP == 2) MOE_MMA_IF("cta_group::2.kind::f8f6f4");
+    else if constexpr (KIND == kF16) MOE_MMA_IF("cta_group::1.kind::f16");
+    else MOE_MMA_IF("cta_group::1.kind::f8f6f4");
+#undef MOE_MMA_IF
+}
+__device__ __forceinline__ void mma_commit_if(bool mine, uint64_t *bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"((uint32_t)mine)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit2_if(bool mine, uint64_t *bar, uint16_t mask) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}"
+        ::"r"(smem_u32(bar)),
+        "h"(mask), "r"((uint32_t)mine)
+        : "memory");
+}
+
 // 32 lanes x 16 columns of 32-bit words from TMEM: thread i gets row (lane base + i).
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
     uint32_t r[16];
