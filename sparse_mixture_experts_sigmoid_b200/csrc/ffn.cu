@@ -4,8 +4,8 @@
 //   forward : GATED  (x, W_gate, W_up -> a; u and v kept for training)
 //             STORE  (a, W_down -> y)
 //   backward: DGATED (dy, W_down, u, v -> du, dv)
-//             STORE  (dy^T a -> dW_down), STORE (du W_gate + dv W_up -> dx),
-//             STORE  (du^T x, dv^T x -> dW_gate, dW_up: one launch)
+//             STORE  (du W_gate + dv W_up -> dx; du^T x, dv^T x -> dW_gate, dW_up;
+//             dy^T a -> dW_down: one launch)
 #include "ffn.cuh"
 #include "skinny.cuh"
 
@@ -42,11 +42,8 @@ moe_status check(const moe_ffn_config *c) {
 }
 
 // The fields that every product of a call shares.
-Gemm product(const moe_ffn_config &c, Kind kind, bool a_mn, bool b_mn, int64_t M, int N, int64_t K, uint32_t *err) {
+Gemm product(const moe_ffn_config &c, int64_t M, int N, int64_t K, uint32_t *err) {
     Gemm g{};
-    g.kind = kind;
-    g.a_mn = a_mn;
-    g.b_mn = b_mn;
     g.M = M;
     g.N = N;
     g.K = K;
@@ -101,7 +98,7 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
         }
         return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
     }
-    Gemm g = product(*c, GATED, false, false, T, c->h, d, err);
+    Gemm g = product(*c, T, c->h, d, err);
     g.a0 = {x, T, d, d};
     g.b0 = {wg, h, d, d};
     g.b1 = {wu, h, d, d};
@@ -110,13 +107,13 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
         g.c1 = {pre, T, h, 2 * h};
         g.c2 = {pre + 2 * h, T, h, 2 * h};
     }
-    cudaError_t e = launch_pair_gemm(g, s);
+    cudaError_t e = launch_gated(g, s);
     if (e == cudaSuccess) {
-        g = product(*c, STORE, false, false, T, c->d, h, err);
+        g = product(*c, T, c->d, h, err);
         g.a0 = {act, T, h, h};
         g.b0 = {wd, d, h, h};
         g.c0 = {y, T, d, d};
-        e = launch_pair_gemm(g, s);
+        e = launch_down(g, s);
     }
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
@@ -175,42 +172,45 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
          *grad = static_cast<char *>(ws) + L.grad;
     const Matrix du{grad, T, h, 2 * h}, dv{grad + 2 * h, T, h, 2 * h};
     if (inner) {
-        Gemm g = product(*c, DGATED, false, true, T, c->h, d, err);
+        Gemm g = product(*c, T, c->h, d, err);
         g.a0 = {dy, T, d, d};
         g.b0 = {w_down, d, h, h};
         g.u = {pre, T, h, 2 * h};
         g.v = {pre + 2 * h, T, h, 2 * h};
         g.c0 = du;
         g.c1 = dv;
-        e = launch_pair_gemm(g, s);
+        e = launch_dgated(g, s);
     }
-    if (e == cudaSuccess && dw_down) {
-        Gemm g = product(*c, STORE, true, true, d, c->h, T, err);
-        g.a0 = {dy, T, d, d};
-        g.b0 = {act, T, h, h};
-        g.c0 = {dw_down, d, h, h};
-        e = launch_pair_gemm(g, s);
+    // the rest in one launch: dx, then the weights' gradients (all over the T tokens)
+    Gemm g[3];
+    int n = 0;
+    if (dx) {
+        g[n] = product(*c, T, c->d, h, err);
+        g[n].ranges = 2;
+        g[n].a0 = du;
+        g[n].a1 = dv;
+        g[n].b0 = {w_gate, h, d, d};
+        g[n].b1 = {w_up, h, d, d};
+        g[n++].c0 = {dx, T, d, d};
     }
-    if (e == cudaSuccess && dx) {
-        Gemm g = product(*c, STORE, false, true, T, c->d, h, err);
-        g.ranges = 2;
-        g.a0 = du;
-        g.a1 = dv;
-        g.b0 = {w_gate, h, d, d};
-        g.b1 = {w_up, h, d, d};
-        g.c0 = {dx, T, d, d};
-        e = launch_pair_gemm(g, s);
+    if (gates) {
+        g[n] = product(*c, h, c->d, T, err);
+        g[n].a_mn = true;
+        g[n].halves = dw_gate && dw_up ? 2 : 1;
+        g[n].a0 = dw_gate ? du : dv;
+        g[n].a1 = dv;
+        g[n].b0 = {x, T, d, d};
+        g[n].c0 = {dw_gate ? dw_gate : dw_up, h, d, d};
+        g[n++].c1 = {dw_up, h, d, d};
     }
-    if (e == cudaSuccess && gates) {
-        Gemm g = product(*c, STORE, true, true, h, c->d, T, err);
-        g.halves = dw_gate && dw_up ? 2 : 1;
-        g.a0 = dw_gate ? du : dv;
-        g.a1 = dv;
-        g.b0 = {x, T, d, d};
-        g.c0 = {dw_gate ? dw_gate : dw_up, h, d, d};
-        g.c1 = {dw_up, h, d, d};
-        e = launch_pair_gemm(g, s);
+    if (dw_down) {
+        g[n] = product(*c, d, c->h, T, err);
+        g[n].a_mn = true;
+        g[n].a0 = {dy, T, d, d};
+        g[n].b0 = {act, T, h, h};
+        g[n++].c0 = {dw_down, d, h, h};
     }
+    if (e == cudaSuccess) e = launch_grads(g, n, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

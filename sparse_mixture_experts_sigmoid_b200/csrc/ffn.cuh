@@ -16,12 +16,12 @@ struct Matrix {
     int64_t rows, cols, ld;
 };
 
+// What an epilogue does (see ffn_pair.cu).
 enum Kind : int { GATED = 0, STORE = 1, DGATED = 2 };
 
 // One product C[M, N] = sum over K of A and B (see ffn_pair.cu).
 struct Gemm {
-    Kind kind;
-    bool a_mn, b_mn;     // the reduction runs over the operand's rows
+    bool a_mn;           // the reduction runs over A's rows (launch_grads)
     Matrix a0, a1, b0, b1;
     Matrix c0, c1, c2;   // GATED: act, and u, v (base null: not kept); STORE: C (C1: second half); DGATED: du, dv
     Matrix u, v;         // DGATED: the kept pre-activations
@@ -32,7 +32,13 @@ struct Gemm {
     bool bf16;           // else fp16
     uint32_t *err;
 };
-cudaError_t launch_pair_gemm(const Gemm &g, cudaStream_t s);
+// act = act(A B0^T) * (A B1^T);  C = A B^T;  du, dv from r = A B.
+cudaError_t launch_gated(const Gemm &g, cudaStream_t s);
+cudaError_t launch_down(const Gemm &g, cudaStream_t s);
+cudaError_t launch_dgated(const Gemm &g, cudaStream_t s);
+// C = A B, or A^T B (a_mn), of up to three products in one launch; the second and
+// third have the same K.
+cudaError_t launch_grads(const Gemm *g, int n, cudaStream_t s);
 
 // ------------------------------------------------------------------ elements
 
@@ -63,8 +69,9 @@ __device__ __forceinline__ float gelu_gate(float u) {
 __device__ __forceinline__ float gelu_tanh_f(float u) { return u * gelu_gate(u); }
 
 // a = act(u), da = act'(u).
-__device__ __forceinline__ void act_grad(int act, float u, float &a, float &da) {
-    if (act == MOE_ACT_SILU) {
+template <int ACT>
+__device__ __forceinline__ void act_grad(float u, float &a, float &da) {
+    if constexpr (ACT == MOE_ACT_SILU) {
         const float s = __fdividef(1.f, 1.f + __expf(-u));
         a = u * s;
         da = s * (1.f + u * (1.f - s));

@@ -3,8 +3,9 @@
 // accumulation:
 //
 //   GATED  : u = x Wg^T, v = x Wu^T;  act(u) v is stored (and u, v for training)
-//   STORE  : C = A B, rounded once: the down projection, dx (two K ranges, du Wg
-//            + dv Wu) and the weight gradients
+//   STORE  : C = A B, rounded once: the down projection; and, several products
+//            in one launch, dx (two K ranges, du Wg + dv Wu) and the weight
+//            gradients
 //   DGATED : r = dy Wd;  du = r v act'(u), dv = r act(u), from the kept u, v
 //
 // Bound by the tensor cores for all but short inputs, so the kernel is one
@@ -33,7 +34,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kBM = 256;                   // rows of a pair's tile
+constexpr int kBM = 256, kBN = 256;        // a pair's tile (GATED: 128 columns of each product)
 constexpr int kBK = 64;                    // 16-bit elements of a 128-byte row
 constexpr int kAStage = 128 * 128;         // this CTA's A of one K block
 constexpr int kAtom = 8192;                // an MN-major atom: 64 k-rows x 128 bytes
@@ -60,28 +61,48 @@ template <int EPI>
 constexpr int epi_bytes() {
     return kEpiWarps * kBox * (EPI == DGATED ? 2 : 1);
 }
-template <int EPI, int BN>
+template <int EPI>
 constexpr int stages() {
-    const int s = (kSmemMax - 1024 - (int)sizeof(Ctrl) - epi_bytes<EPI>()) / (kAStage + BN * 64);
+    const int s = (kSmemMax - 1024 - (int)sizeof(Ctrl) - epi_bytes<EPI>()) / (2 * kAStage);
     return s > kMaxStages ? kMaxStages : s;
 }
 
-struct Params {
+// One product of a launch.
+struct Job {
     int M, N, K;       // output rows and columns; K per range
     int ranges;        // K ranges (A0 B0, then A1 B1)
-    int halves;        // STORE: products that share B and the shape (A0 -> C0, A1 -> C1)
     int mt, nt;        // tiles of one half
+    int tiles;         // of both halves (products that share B and the shape: A0 -> C0, A1 -> C1)
+    int a_mn;          // FORM == GRADS: A is MN-major
+};
+constexpr int kMaxJobs = 3;
+struct Params {
+    Job job[kMaxJobs];
+    int njobs;
+    // The order of the tiles: job 0's first, dealt out to the pairs in rounds.
+    // Of the others' the pairs from `behind` on, which had one tile of job 0
+    // less, take `extra` rounds first; then all pairs take rounds.
+    int behind, extra, rest;   // rest: tiles of the jobs after the first
     int act;           // moe_ffn_act
     uint32_t fmt;      // operand format of the instruction descriptor: 0 fp16, 1 bf16
     bool keep;         // GATED: store u and v as well
     uint32_t *err;
 };
 
-struct Maps {
+struct JobMaps {
     CUtensorMap a0, a1, b0, b1;   // operands
-    CUtensorMap c0, c1, c2;       // outputs: C0 (act, du), C1 (u, dv), C2 (v)
+    CUtensorMap c0, c1;           // outputs: C0 (act, du), C1 (u, dv; the second half)
+};
+template <int NJOBS>
+struct Maps {
+    JobMaps job[NJOBS];
+    CUtensorMap c2;               // GATED: v
     CUtensorMap u, v;             // DGATED: the kept pre-activations
 };
+
+// How the operands lie: both K-major; B MN-major; or (several jobs) B MN-major
+// and A either.
+enum { KK = 0, KN = 1, GRADS = 2 };
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *m, const void *src, int c0, int c1) {
     asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];"
@@ -99,22 +120,42 @@ __device__ __forceinline__ uint64_t desc_mn(const void *p) {
            ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
-// Tile id -> (half, m, n).  Row tiles run in groups of eight with the column
-// tiles outside them, so that the pairs at work at one time read about as many
-// rows of A as of B and share them through L2.
+// The k-th tile of a pair: its job, half, row and column tile; false past the
+// last.  Row tiles of a job run in groups of eight with the column tiles outside
+// them, so that the pairs at work at one time read about as many rows of A as of
+// B and share them through L2.
 struct Tile {
-    int half, m, n;
+    int job, half, m, n;
 };
-__device__ __forceinline__ Tile tile_of(int id, const Params &p) {
-    const int per = p.mt * p.nt;
-    Tile t;
+__device__ __forceinline__ bool tile_at(int k, int pair, int npairs, const Params &p, Tile &t) {
+    const int first = p.job[0].tiles;
+    int id = k * npairs + pair;
+    t.job = 0;
+    if (id >= first) {
+        if (p.njobs == 1) return false;
+        k -= pair < first ? (first - pair + npairs - 1) / npairs : 0;
+        const int late = pair - p.behind;   // >= 0: one tile of job 0 less
+        if (late >= 0 && k < p.extra) {
+            id = k * (npairs - p.behind) + late;
+        } else {
+            if (late >= 0) k -= p.extra;
+            id = p.extra * (npairs - p.behind) + k * npairs + pair;
+        }
+        if (id >= p.rest) return false;
+        t.job = 1;
+        if (id >= p.job[1].tiles) {
+            id -= p.job[1].tiles;
+            t.job = 2;
+        }
+    }
+    const int mt = p.job[t.job].mt, nt = p.job[t.job].nt, per = mt * nt;
     t.half = id / per;
     id -= t.half * per;
-    const int g = id / (8 * p.nt), first = 8 * g, size = min(p.mt - first, 8);
-    id -= g * 8 * p.nt;
+    const int g = id / (8 * nt), top = 8 * g, size = min(mt - top, 8);
+    id -= top * nt;
     t.n = id / size;
-    t.m = first + id - t.n * size;
-    return t;
+    t.m = top + id - t.n * size;
+    return true;
 }
 
 // A warp's box of 32 rows x 64 columns in shared memory, 128-byte swizzle: the
@@ -124,9 +165,35 @@ __device__ __forceinline__ uint4 *box_word(uint8_t *box, int j) {
     return reinterpret_cast<uint4 *>(box + i * 128 + ((j ^ (i & 7)) << 4));
 }
 
-template <bool A_MN, bool B_MN, int EPI, int BN>
-__global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_constant__ Maps maps, Params p) {
-    constexpr int kStages = stages<EPI, BN>();
+// DGATED: this lane's row of 64 columns, u and v in its boxes and r in f: du and
+// dv in their place.
+template <int ACT>
+__device__ __forceinline__ void gate_grad(uint8_t *box_u, uint8_t *box_v, const float (&f)[64], uint32_t fmt) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        uint4 wu = *box_word(box_u, j), wv = *box_word(box_v, j);
+        uint32_t *pu = reinterpret_cast<uint32_t *>(&wu), *pv = reinterpret_cast<uint32_t *>(&wv);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const float2 uu = unpack2(pu[z], fmt), vv = unpack2(pv[z], fmt);
+            float a[2], da[2];
+            act_grad<ACT>(uu.x, a[0], da[0]);
+            act_grad<ACT>(uu.y, a[1], da[1]);
+            const float r0 = f[8 * j + 2 * z], r1 = f[8 * j + 2 * z + 1];
+            pu[z] = pack2(r0 * vv.x * da[0], r1 * vv.y * da[1], fmt);
+            pv[z] = pack2(r0 * a[0], r1 * a[1], fmt);
+        }
+        *box_word(box_u, j) = wu;
+        *box_word(box_v, j) = wv;
+    }
+}
+
+template <int FORM, int EPI>
+__global__ void __launch_bounds__(kThreads, 1)
+    ffn_pair_kernel(const __grid_constant__ Maps<FORM == GRADS ? kMaxJobs : 1> maps, const __grid_constant__ Params p) {
+    constexpr bool B_MN = FORM != KK;
+    constexpr int BN = kBN;
+    constexpr int kStages = stages<EPI>();
     constexpr int kBStage = BN * 64;       // this CTA's half of B of one K block
     constexpr int kCols = EPI == GATED ? BN / 2 : BN;   // output columns of a tile
     constexpr int kWarpCols = kCols / 2;   // of one epilogue warp
@@ -157,9 +224,9 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
     }
     if (warp == kMmaWarp) tmem_alloc2(&ctrl->tmem_base, kTmemCols);
     if (warp == kTmaWarp && lane == 0) {
-        prefetch_tmap(&maps.a0);
-        prefetch_tmap(&maps.b0);
-        prefetch_tmap(&maps.c0);
+        prefetch_tmap(&maps.job[0].a0);
+        prefetch_tmap(&maps.job[0].b0);
+        prefetch_tmap(&maps.job[0].c0);
     }
     pdl_wait();
     tc_fence_before();
@@ -169,8 +236,6 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
     pdl_launch_dependents();
 
     const uint32_t tmem = ctrl->tmem_base;
-    const int total = p.halves * p.mt * p.nt;
-    const int kr = (p.K + kBK - 1) / kBK, nk = p.ranges * kr;
     const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
 
     if (warp == kTmaWarp) {
@@ -179,8 +244,12 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
             const uint32_t full_lead = mapa_shared(&ctrl->full[0], 0);
             uint32_t it = 0;
             bool ok = true;
-            for (int id = pair; id < total && ok; id += npairs) {
-                const Tile t = tile_of(id, p);
+            Tile t;
+            for (int k = 0; ok && tile_at(k, pair, npairs, p, t); ++k) {
+                const Job &j = p.job[t.job];
+                const JobMaps &jm = maps.job[FORM == GRADS ? t.job : 0];
+                const int kr = (j.K + kBK - 1) / kBK, nk = j.ranges * kr;
+                const bool a_mn = FORM == GRADS && j.a_mn;
                 const int m0 = t.m * kBM + (int)rank * 128;
                 // GATED: the even CTA holds the gate's rows, the odd one the up projection's
                 const int n0 = EPI == GATED ? t.n * kCols : t.n * BN + (int)rank * (BN / 2);
@@ -194,10 +263,10 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
                     const uint32_t fb = full_lead + s * (uint32_t)sizeof(uint64_t);
                     const bool second = kb >= kr;
                     const int k0 = (second ? kb - kr : kb) * kBK;
-                    const CUtensorMap *ma = second || t.half ? &maps.a1 : &maps.a0;
-                    const CUtensorMap *mb = (EPI == GATED ? !lead : second) ? &maps.b1 : &maps.b0;
+                    const CUtensorMap *ma = second || t.half ? &jm.a1 : &jm.a0;
+                    const CUtensorMap *mb = (EPI == GATED ? !lead : second) ? &jm.b1 : &jm.b0;
                     uint8_t *a = sA + s * kAStage, *b = sB + s * kBStage;
-                    if constexpr (A_MN) {
+                    if (a_mn) {
                         tma_load_2d_pair(ma, a, fb, m0, k0);
                         tma_load_2d_pair(ma, a + kAtom, fb, m0 + 64, k0);
                     } else {
@@ -205,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
                     }
                     if constexpr (B_MN) {
 #pragma unroll
-                        for (int j = 0; j < BN / 128; ++j) tma_load_2d_pair(mb, b + j * kAtom, fb, n0 + 64 * j, k0);
+                        for (int q = 0; q < 2; ++q) tma_load_2d_pair(mb, b + q * kAtom, fb, n0 + 64 * q, k0);
                     } else {
                         tma_load_2d_pair(mb, b, fb, k0, n0);
                     }
@@ -224,14 +293,19 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
     } else if (warp == kMmaWarp) {
         if (lead) {   // the whole warp: one lane's instructions take effect
             const bool mine = lane == 0;
-            const uint32_t idesc = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) | ((uint32_t)A_MN << 15) |
-                                   ((uint32_t)B_MN << 16) | ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
-            uint32_t it = 0, tc = 0;
+            const uint32_t idesc0 = (1u << 4) | (p.fmt << 7) | (p.fmt << 10) | ((uint32_t)B_MN << 16) |
+                                    ((uint32_t)(BN >> 3) << 17) | ((uint32_t)(kBM >> 4) << 24);
+            uint32_t it = 0;
             bool ok = true;
-            for (int id = pair; id < total && ok; id += npairs, ++tc) {
+            Tile t;
+            for (int tc = 0; ok && tile_at(tc, pair, npairs, p, t); ++tc) {
                 const uint32_t acc = tc & 1;
                 if (!wait_bar(&ctrl->tempty[acc], ((tc >> 1) & 1) ^ 1, abort, p.err)) break;
                 tc_fence_after();
+                const Job &j = p.job[t.job];
+                const int nk = j.ranges * ((j.K + kBK - 1) / kBK);
+                const bool a_mn = FORM == GRADS && j.a_mn;
+                const uint32_t idesc = idesc0 | ((uint32_t)a_mn << 15);
                 const uint32_t d = tmem + acc * BN;
                 for (int kb = 0; kb < nk; ++kb, ++it) {
                     const int s = it % kStages;
@@ -242,14 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
                         break;
                     }
                     tc_fence_after();
+                    const uint64_t ad = a_mn ? desc_mn(sA + s * kAStage) : smem_desc(sA + s * kAStage);
+                    const uint64_t bd = B_MN ? desc_mn(sB + s * kBStage) : smem_desc(sB + s * kBStage);
+                    // a K slice of 16: 2 KB on in an MN-major operand, 32 bytes in a K-major one
+                    const uint64_t an = a_mn ? 2048 >> 4 : 32 >> 4, bn = B_MN ? 2048 >> 4 : 32 >> 4;
 #pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t ad = A_MN ? desc_mn(sA + s * kAStage + kk * 2048)
-                                                 : smem_desc(sA + s * kAStage) + 2 * kk;
-                        const uint64_t bd = B_MN ? desc_mn(sB + s * kBStage + kk * 2048)
-                                                 : smem_desc(sB + s * kBStage) + 2 * kk;
-                        mma_if<2, kF16>(mine, d, ad, bd, idesc, (kb | kk) != 0);
-                    }
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_if<2, kF16>(mine, d, ad + kk * an, bd + kk * bn, idesc, (kb | kk) != 0);
                     mma_commit2_if(mine, &ctrl->empty[s], 0x3);
                 }
                 if (ok) mma_commit2_if(mine, &ctrl->tfull[acc], 0x3);
@@ -261,17 +334,16 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int cw = (warp >> 2) * kWarpCols;   // this warp's first output column of the tile
         uint8_t *box = sEpi + warp * (epi_bytes<EPI>() / kEpiWarps), *box2 = box + kBox;
-        uint32_t tc = 0;
         [[maybe_unused]] uint32_t loads = 0;      // DGATED: u, v box loads issued so far
         // stores the packed 64 columns of this warp's 32 rows (8 words a row)
-        auto put = [&](const CUtensorMap *m, const uint4 (&w)[8], int c, int r) {
+        auto put = [&](const CUtensorMap *m, const uint4 (&w)[8], int c, int r, const Job &j) {
             if (lane == 0) bulk_wait_read();   // the previous store has left the box
             __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) *box_word(box, j) = w[j];
+            for (int q = 0; q < 8; ++q) *box_word(box, q) = w[q];
             fence_proxy_async();
             __syncwarp();
-            if (lane == 0 && r < p.M && c < p.N) {
+            if (lane == 0 && r < j.M && c < j.N) {
                 tma_store_2d(m, box, c, r);
                 bulk_commit();
             }
@@ -297,12 +369,14 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
             }
             ++loads;
         };
-        for (int id = pair; id < total; id += npairs, ++tc) {
-            const Tile t = tile_of(id, p);
+        Tile t;
+        for (int tc = 0; tile_at(tc, pair, npairs, p, t); ++tc) {
+            const Job &j = p.job[t.job];
+            const JobMaps &jm = maps.job[FORM == GRADS ? t.job : 0];
             const uint32_t acc = tc & 1;
             const int r = t.m * kBM + (int)rank * 128 + (warp & 3) * 32, c0 = t.n * kCols + cw;
             if constexpr (EPI == DGATED) {
-                if (r < p.M && c0 < p.N) ask(c0, r);
+                if (r < j.M && c0 < j.N) ask(c0, r);
             }
             if (!wait_bar(&ctrl->tfull[acc], (tc >> 1) & 1, abort, p.err)) {
                 if constexpr (EPI == DGATED) {
@@ -316,17 +390,17 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
             }
             tc_fence_after();
             const uint32_t tb = tmem + acc * BN + lane_base;
-            if (r < p.M && c0 < p.N) {
+            if (r < j.M && c0 < j.N) {
                 if constexpr (EPI == STORE) {
-                    const CUtensorMap *mc = t.half ? &maps.c1 : &maps.c0;
+                    const CUtensorMap *mc = t.half ? &jm.c1 : &jm.c0;
 #pragma unroll 1
                     for (int q = 0; q < kWarpCols; q += 64) {
-                        if (c0 + q >= p.N) break;
+                        if (c0 + q >= j.N) break;
                         float f[64];
                         uint4 w[8];
                         read64(tb + cw + q, f);
                         pack(f, w);
-                        put(mc, w, c0 + q, r);
+                        put(mc, w, c0 + q, r, j);
                     }
                 } else if constexpr (EPI == GATED) {
                     float g[64], u[64];
@@ -335,9 +409,9 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
                     read64(tb + BN / 2 + cw, u);
                     if (p.keep) {
                         pack(g, w);
-                        put(&maps.c1, w, c0, r);
+                        put(&jm.c1, w, c0, r, j);
                         pack(u, w);
-                        put(&maps.c2, w, c0, r);
+                        put(&maps.c2, w, c0, r, j);
                     }
                     if (p.act == MOE_ACT_SILU) {
 #pragma unroll
@@ -347,37 +421,24 @@ __global__ void __launch_bounds__(kThreads, 1) ffn_pair_kernel(const __grid_cons
                         for (int i = 0; i < 64; ++i) g[i] = gelu_tanh_f(g[i]) * u[i];
                     }
                     pack(g, w);
-                    put(&maps.c0, w, c0, r);
+                    put(&jm.c0, w, c0, r, j);
                 } else {
 #pragma unroll 1
                     for (int q = 0; q < kWarpCols; q += 64) {
-                        if (c0 + q >= p.N) break;
+                        if (c0 + q >= j.N) break;
                         if (q) ask(c0 + q, r);
                         if (!wait_bar(&ctrl->kept[warp], (loads - 1) & 1, abort, p.err)) break;
                         float f[64];
                         read64(tb + cw + q, f);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            uint4 wu = *box_word(box, j), wv = *box_word(box2, j);
-                            uint32_t *pu = reinterpret_cast<uint32_t *>(&wu), *pv = reinterpret_cast<uint32_t *>(&wv);
-#pragma unroll
-                            for (int z = 0; z < 4; ++z) {
-                                const float2 uu = unpack2(pu[z], p.fmt), vv = unpack2(pv[z], p.fmt);
-                                float a[2], da[2];
-                                act_grad(p.act, uu.x, a[0], da[0]);
-                                act_grad(p.act, uu.y, a[1], da[1]);
-                                const float r0 = f[8 * j + 2 * z], r1 = f[8 * j + 2 * z + 1];
-                                pu[z] = pack2(r0 * vv.x * da[0], r1 * vv.y * da[1], p.fmt);
-                                pv[z] = pack2(r0 * a[0], r1 * a[1], p.fmt);
-                            }
-                            *box_word(box, j) = wu;
-                            *box_word(box2, j) = wv;
-                        }
+                        // one loop per activation: a branch inside would keep the
+                        // elements' chains (exponential, reciprocal) from overlapping
+                        if (p.act == MOE_ACT_SILU) gate_grad<MOE_ACT_SILU>(box, box2, f, p.fmt);
+                        else gate_grad<MOE_ACT_GELU_TANH>(box, box2, f, p.fmt);
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&maps.c0, box, c0 + q, r);
-                            tma_store_2d(&maps.c1, box2, c0 + q, r);
+                            tma_store_2d(&jm.c0, box, c0 + q, r);
+                            tma_store_2d(&jm.c1, box2, c0 + q, r);
                             bulk_commit();
                         }
                     }
@@ -423,69 +484,64 @@ bool make_map16(CUtensorMap *m, const Matrix &x, uint32_t box_rows) {
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool A_MN, bool B_MN, int EPI, int BN>
-cudaError_t launch(const Gemm &g, cudaStream_t s) {
-    constexpr int kCols = EPI == GATED ? BN / 2 : BN;
-    Maps maps{};
-    // operand boxes: K-major 128 (A) or BN / 2 (B) rows of 64 k; MN-major 64 k-rows of 64 columns
-    bool ok = make_map16(&maps.a0, g.a0, A_MN ? 64 : 128) && make_map16(&maps.b0, g.b0, B_MN ? 64 : BN / 2) &&
-              make_map16(&maps.c0, g.c0, 32);
-    if (ok && g.a1.base) ok = make_map16(&maps.a1, g.a1, A_MN ? 64 : 128);
-    if (ok && g.b1.base) ok = make_map16(&maps.b1, g.b1, B_MN ? 64 : BN / 2);
-    if (ok && g.c1.base) ok = make_map16(&maps.c1, g.c1, 32);
-    if (ok && g.c2.base) ok = make_map16(&maps.c2, g.c2, 32);
-    if (ok && EPI == DGATED) ok = make_map16(&maps.u, g.u, 32) && make_map16(&maps.v, g.v, 32);
-    if (!ok) return cudaErrorInvalidValue;
-    Params p{};
-    p.M = (int)g.M;
-    p.N = g.N;
-    p.K = (int)g.K;
-    p.ranges = g.ranges;
-    p.halves = g.halves;
-    p.mt = (int)((g.M + kBM - 1) / kBM);
-    p.nt = (g.N + kCols - 1) / kCols;
-    p.act = g.act;
-    p.fmt = g.bf16 ? 1u : 0u;
-    p.keep = g.c1.base != nullptr;
-    p.err = g.err;
-    const size_t smem = 1024 + (size_t)stages<EPI, BN>() * (kAStage + BN * 64) + epi_bytes<EPI>() + sizeof(Ctrl);
-    auto kern = ffn_pair_kernel<A_MN, B_MN, EPI, BN>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const int64_t tiles = (int64_t)p.halves * p.mt * p.nt;
-    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2, tiles));
-    return launch_kernel_pair(kern, 2 * pairs, kThreads, smem, s, maps, p);
+// Job i of a launch from its product; false when a tensor map cannot be made.
+template <int FORM, int EPI, typename M>
+bool set_job(const Gemm &g, int i, M &maps, Params &p) {
+    constexpr int kCols = EPI == GATED ? kBN / 2 : kBN;
+    JobMaps &m = maps.job[i];
+    // operand boxes: K-major 128 rows of 64 k; MN-major 64 k-rows of 64 columns
+    const uint32_t ab = g.a_mn ? 64 : 128, bb = FORM == KK ? 128 : 64;
+    if (!make_map16(&m.a0, g.a0, ab) || !make_map16(&m.b0, g.b0, bb) || !make_map16(&m.c0, g.c0, 32)) return false;
+    if (g.a1.base && !make_map16(&m.a1, g.a1, ab)) return false;
+    if (g.b1.base && !make_map16(&m.b1, g.b1, bb)) return false;
+    if (g.c1.base && !make_map16(&m.c1, g.c1, 32)) return false;
+    Job &j = p.job[i];
+    j.M = (int)g.M;
+    j.N = g.N;
+    j.K = (int)g.K;
+    j.ranges = g.ranges;
+    j.mt = (int)((g.M + kBM - 1) / kBM);
+    j.nt = (g.N + kCols - 1) / kCols;
+    j.tiles = g.halves * j.mt * j.nt;
+    j.a_mn = g.a_mn;
+    return true;
 }
 
-// Whether tiles of 128 columns end sooner than tiles of 256: their rounds over
-// the pairs, at (per K block) 512 and 256 cycles of MMA and a tile's fixed cost.
-// The narrow tiles read half as much again per product, which does not show
-// while few pairs are at work; for full rounds the wide ones win.
-bool narrow_tiles(const Gemm &g) {
-    const int64_t pairs = num_sms() / 2, mt = (g.M + kBM - 1) / kBM * g.halves;
-    const int64_t nk = (int64_t)g.ranges * ((g.K + kBK - 1) / kBK);
-    auto rounds = [&](int bn) { return (mt * ((g.N + bn - 1) / bn) + pairs - 1) / pairs; };
-    return rounds(128) * (nk * 290 + 2000) < rounds(256) * (nk * 512 + 3000);
+template <int FORM, int EPI>
+cudaError_t launch(const Gemm *g, int n, cudaStream_t s) {
+    Maps<FORM == GRADS ? kMaxJobs : 1> maps{};
+    Params p{};
+    for (int i = 0; i < n; ++i)
+        if (!set_job<FORM, EPI>(g[i], i, maps, p)) return cudaErrorInvalidValue;
+    if (g->c2.base && !make_map16(&maps.c2, g->c2, 32)) return cudaErrorInvalidValue;
+    if (EPI == DGATED && (!make_map16(&maps.u, g->u, 32) || !make_map16(&maps.v, g->v, 32))) return cudaErrorInvalidValue;
+    p.njobs = n;
+    p.act = g->act;
+    p.fmt = g->bf16 ? 1u : 0u;
+    p.keep = g->c1.base != nullptr;
+    p.err = g->err;
+    for (int i = 1; i < n; ++i) p.rest += p.job[i].tiles;
+    const int64_t tiles = (int64_t)p.job[0].tiles + p.rest;
+    const int pairs = (int)std::max<int64_t>(1, std::min<int64_t>(num_sms() / 2, tiles));
+    // the pairs without a last tile of job 0, and how many of the others fit into its time
+    p.behind = p.job[0].tiles % pairs;
+    if (n > 1 && p.behind) {
+        auto blocks = [&](const Job &j) { return j.ranges * ((j.K + kBK - 1) / kBK); };
+        p.extra = blocks(p.job[0]) / blocks(p.job[1]);
+    }
+    const size_t smem = 1024 + (size_t)stages<EPI>() * 2 * kAStage + epi_bytes<EPI>() + sizeof(Ctrl);
+    auto kern = ffn_pair_kernel<FORM, EPI>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    return launch_kernel_pair(kern, 2 * pairs, kThreads, smem, s, maps, p);
 }
 
 }  // namespace
 
-cudaError_t launch_pair_gemm(const Gemm &g, cudaStream_t s) {
-    switch (g.kind) {
-        case GATED: return launch<false, false, GATED, 256>(g, s);
-        case DGATED:
-            return narrow_tiles(g) ? launch<false, true, DGATED, 128>(g, s) : launch<false, true, DGATED, 256>(g, s);
-        default:
-            if (narrow_tiles(g)) {
-                if (g.a_mn) return launch<true, true, STORE, 128>(g, s);
-                if (g.b_mn) return launch<false, true, STORE, 128>(g, s);
-                return launch<false, false, STORE, 128>(g, s);
-            }
-            if (g.a_mn) return launch<true, true, STORE, 256>(g, s);
-            if (g.b_mn) return launch<false, true, STORE, 256>(g, s);
-            return launch<false, false, STORE, 256>(g, s);
-    }
-}
+cudaError_t launch_gated(const Gemm &g, cudaStream_t s) { return launch<KK, GATED>(&g, 1, s); }
+cudaError_t launch_down(const Gemm &g, cudaStream_t s) { return launch<KK, STORE>(&g, 1, s); }
+cudaError_t launch_dgated(const Gemm &g, cudaStream_t s) { return launch<KN, DGATED>(&g, 1, s); }
+cudaError_t launch_grads(const Gemm *g, int n, cudaStream_t s) { return launch<GRADS, STORE>(g, n, s); }
 
 }  // namespace ffn
 }  // namespace moe
