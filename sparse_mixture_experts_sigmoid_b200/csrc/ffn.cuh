@@ -6,6 +6,7 @@
 #include <cuda_fp16.h>
 
 #include "moe_internal.cuh"
+#include "packed.cuh"
 
 namespace moe {
 namespace ffn {
@@ -60,28 +61,39 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, uint32_t fmt) {
 }
 
 // ------------------------------------------------------------------ activations
-// silu: silu_f of moe_internal.cuh.  gelu_tanh(u) = u (1 + tanh z) / 2 with
-// z = sqrt(2 / pi) (u + 0.044715 u^3); (1 + tanh z) / 2 = 1 / (1 + exp(-2 z)).
-__device__ __forceinline__ float gelu_gate(float u) {
-    const float z2 = 1.5957691216057308f * u * fmaf(0.044715f * u, u, 1.f);   // 2 z
-    return __fdividef(1.f, 1.f + __expf(-z2));
-}
-__device__ __forceinline__ float gelu_tanh_f(float u) { return u * gelu_gate(u); }
+// silu(u) = u s, s = 1 / (1 + exp(-u));  gelu_tanh(u) = u (1 + tanh z) / 2 = u s,
+// z = sqrt(2 / pi) (u + 0.044715 u^3), s = 1 / (1 + exp(-2 z)).  Two elements at a
+// time: s takes two operations of the special function unit, the rest is packed.
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGelu = 1.5957691216057308f;   // 2 sqrt(2 / pi)
 
-// a = act(u), da = act'(u).
+// s of a pair; for gelu_tanh u2 = u^2 as well.
 template <int ACT>
-__device__ __forceinline__ void act_grad(float u, float &a, float &da) {
-    if constexpr (ACT == MOE_ACT_SILU) {
-        const float s = __fdividef(1.f, 1.f + __expf(-u));
-        a = u * s;
-        da = s * (1.f + u * (1.f - s));
-    } else {
-        const float s = gelu_gate(u);
-        a = u * s;
+__device__ __forceinline__ float2 act_gate(float2 u, float2 &u2) {
+    if constexpr (ACT == MOE_ACT_SILU) return logistic2(mul2(u, both(-kLog2e)));
+    u2 = mul2(u, u);
+    return logistic2(mul2(u, fma2(u2, both(-kLog2e * kGelu * 0.044715f), both(-kLog2e * kGelu))));
+}
+// act(u) v
+template <int ACT>
+__device__ __forceinline__ float2 gated2(float2 u, float2 v) {
+    float2 u2;
+    return mul2(mul2(u, act_gate<ACT>(u, u2)), v);
+}
+// a = act(u), da = act'(u) = s + u s' with s' = s (1 - s) d(2 z)/du.
+template <int ACT>
+__device__ __forceinline__ void act_grad2(float2 u, float2 &a, float2 &da) {
+    float2 u2;
+    const float2 s = act_gate<ACT>(u, u2);
+    a = mul2(u, s);
+    float2 t = mul2(a, fma2(s, both(-1.f), both(1.f)));
+    if constexpr (ACT == MOE_ACT_GELU_TANH) {
         // d(2 z) / du = 2 sqrt(2 / pi) (1 + 3 * 0.044715 u^2); past |u| = 100, where s is 0 or 1
         // and the term vanishes, u^2 is held so that it cannot become 0 * inf
-        da = s + a * (1.f - s) * 1.5957691216057308f * fmaf(0.134145f, fminf(u * u, 1e4f), 1.f);
+        u2 = make_float2(fminf(u2.x, 1e4f), fminf(u2.y, 1e4f));
+        t = mul2(t, fma2(u2, both(3.f * 0.044715f * kGelu), both(kGelu)));
     }
+    da = add2(t, s);
 }
 
 }  // namespace ffn

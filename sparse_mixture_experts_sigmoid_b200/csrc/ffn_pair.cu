@@ -165,6 +165,16 @@ __device__ __forceinline__ uint4 *box_word(uint8_t *box, int j) {
     return reinterpret_cast<uint4 *>(box + i * 128 + ((j ^ (i & 7)) << 4));
 }
 
+// GATED: g = act(g) u over a lane's 64 columns.
+template <int ACT>
+__device__ __forceinline__ void gate(float (&g)[64], const float (&u)[64]) {
+#pragma unroll
+    for (int i = 0; i < 64; i += 2) {
+        const float2 a = gated2<ACT>(make_float2(g[i], g[i + 1]), make_float2(u[i], u[i + 1]));
+        g[i] = a.x;
+        g[i + 1] = a.y;
+    }
+}
 // DGATED: this lane's row of 64 columns, u and v in its boxes and r in f: du and
 // dv in their place.
 template <int ACT>
@@ -175,13 +185,12 @@ __device__ __forceinline__ void gate_grad(uint8_t *box_u, uint8_t *box_v, const 
         uint32_t *pu = reinterpret_cast<uint32_t *>(&wu), *pv = reinterpret_cast<uint32_t *>(&wv);
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-            const float2 uu = unpack2(pu[z], fmt), vv = unpack2(pv[z], fmt);
-            float a[2], da[2];
-            act_grad<ACT>(uu.x, a[0], da[0]);
-            act_grad<ACT>(uu.y, a[1], da[1]);
-            const float r0 = f[8 * j + 2 * z], r1 = f[8 * j + 2 * z + 1];
-            pu[z] = pack2(r0 * vv.x * da[0], r1 * vv.y * da[1], fmt);
-            pv[z] = pack2(r0 * a[0], r1 * a[1], fmt);
+            const float2 r = make_float2(f[8 * j + 2 * z], f[8 * j + 2 * z + 1]);
+            float2 a, da;
+            act_grad2<ACT>(unpack2(pu[z], fmt), a, da);
+            const float2 du = mul2(mul2(r, unpack2(pv[z], fmt)), da), dv = mul2(r, a);
+            pu[z] = pack2(du.x, du.y, fmt);
+            pv[z] = pack2(dv.x, dv.y, fmt);
         }
         *box_word(box_u, j) = wu;
         *box_word(box_v, j) = wv;
@@ -413,13 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         pack(u, w);
                         put(&maps.c2, w, c0, r, j);
                     }
-                    if (p.act == MOE_ACT_SILU) {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) g[i] = silu_f(g[i]) * u[i];
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 64; ++i) g[i] = gelu_tanh_f(g[i]) * u[i];
-                    }
+                    if (p.act == MOE_ACT_SILU) gate<MOE_ACT_SILU>(g, u);
+                    else gate<MOE_ACT_GELU_TANH>(g, u);
                     pack(g, w);
                     put(&jm.c0, w, c0, r, j);
                 } else {

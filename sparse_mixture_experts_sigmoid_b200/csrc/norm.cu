@@ -29,6 +29,7 @@
 #include <cuda_fp16.h>
 
 #include "moe_internal.cuh"
+#include "packed.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -47,27 +48,6 @@ template <typename T> __device__ __forceinline__ T el_from(float v);
 template <> __device__ __forceinline__ float el_from<float>(float v) { return v; }
 template <> __device__ __forceinline__ __nv_bfloat16 el_from<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 template <> __device__ __forceinline__ __half el_from<__half>(float v) { return __float2half_rn(v); }
-
-// Two fp32 operations an instruction (sm_100's packed fp32), which halves what
-// these kernels issue per element besides the conversions.
-__device__ __forceinline__ unsigned long long bits2(float2 v) { return *reinterpret_cast<unsigned long long *>(&v); }
-__device__ __forceinline__ float2 from2(unsigned long long b) { return *reinterpret_cast<float2 *>(&b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-    unsigned long long r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)), "l"(bits2(c)));
-    return from2(r);
-}
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return from2(r);
-}
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    unsigned long long r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(bits2(a)), "l"(bits2(b)));
-    return from2(r);
-}
-__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
 
 // A word's elements as pairs of fp32, and back (rounded to nearest).
 template <typename T>

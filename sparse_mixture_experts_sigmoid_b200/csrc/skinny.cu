@@ -321,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         float u[4], v[4];
         add_ranges(at, S, u);
         if (GATED) add_ranges(at + kOutRows, S, v);
-        const int64_t o = (int64_t)(t0 + t) * p.N + n;
+        const int64_t at_out = (int64_t)(t0 + t) * p.N + n;
         if constexpr (GATED) {
             if (p.pre) {
                 const int64_t b = (int64_t)(t0 + t) * 2 * p.N + n;
@@ -329,10 +329,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                 store4(p.pre, b + p.N, v, p.out_dtype);
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                u[j] = (p.act == MOE_ACT_SILU ? silu_f(u[j]) : ffn::gelu_tanh_f(u[j])) * v[j];
+            for (int j = 0; j < 4; j += 2) {
+                const float2 a = make_float2(u[j], u[j + 1]), b = make_float2(v[j], v[j + 1]);
+                const float2 o = p.act == MOE_ACT_SILU ? ffn::gated2<MOE_ACT_SILU>(a, b) : ffn::gated2<MOE_ACT_GELU_TANH>(a, b);
+                u[j] = o.x;
+                u[j + 1] = o.y;
+            }
         }
-        store4(p.out, o, u, p.out_dtype);
+        store4(p.out, at_out, u, p.out_dtype);
     }
     if (S > 1) cluster_sync_all();   // the others may still be reading this CTA's sums
 }
