@@ -68,48 +68,49 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t T = c->T, d = c->d, h = c->h;
     char *act = static_cast<char *>(ws) + L.act, *pre = static_cast<char *>(ws) + L.pre;
-    if (skinny::wants(T, c->h, c->d)) {
-        skinny::Product p{};
+    // each product by the kernel that its size wants
+    skinny::Product p{};
+    p.bf16 = c->dtype == MOE_BF16;
+    p.T = T;
+    p.out_dtype = c->dtype;
+    p.err = err;
+    cudaError_t e;
+    if (skinny::wants(skinny::Form::kGated, T, c->h, c->d)) {
         p.gated = true;
-        p.bf16 = c->dtype == MOE_BF16;
-        p.T = T;
         p.N = c->h;
         p.K = c->d;
         p.x = x;
         p.w0 = wg;
         p.w1 = wu;
         p.out = act;
-        p.out_dtype = c->dtype;
         p.pre = train ? pre : nullptr;
         p.act = c->act;
-        p.err = err;
-        cudaError_t e = skinny::launch(p, s);
-        if (e == cudaSuccess) {
-            p.gated = false;
-            p.N = c->d;
-            p.K = c->h;
-            p.x = act;
-            p.w0 = wd;
-            p.w1 = nullptr;
-            p.out = y;
-            p.pre = nullptr;
-            p.early = true;   // the kernel before is the one above
-            e = skinny::launch(p, s);
+        e = skinny::launch(p, s);
+    } else {
+        Gemm g = product(*c, T, c->h, d, err);
+        g.a0 = {x, T, d, d};
+        g.b0 = {wg, h, d, d};
+        g.b1 = {wu, h, d, d};
+        g.c0 = {act, T, h, h};
+        if (train) {
+            g.c1 = {pre, T, h, 2 * h};
+            g.c2 = {pre + 2 * h, T, h, 2 * h};
         }
-        return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+        e = launch_gated(g, s);
     }
-    Gemm g = product(*c, T, c->h, d, err);
-    g.a0 = {x, T, d, d};
-    g.b0 = {wg, h, d, d};
-    g.b1 = {wu, h, d, d};
-    g.c0 = {act, T, h, h};
-    if (train) {
-        g.c1 = {pre, T, h, 2 * h};
-        g.c2 = {pre + 2 * h, T, h, 2 * h};
-    }
-    cudaError_t e = launch_gated(g, s);
-    if (e == cudaSuccess) {
-        g = product(*c, T, c->d, h, err);
+    if (e != cudaSuccess) return MOE_ERR_CUDA;
+    if (skinny::wants(skinny::Form::kStore, T, c->d, c->h)) {
+        p.gated = false;
+        p.N = c->d;
+        p.K = c->h;
+        p.x = act;
+        p.w0 = wd;
+        p.out = y;
+        p.pre = nullptr;
+        p.early = true;   // the kernel before is the one above
+        e = skinny::launch(p, s);
+    } else {
+        Gemm g = product(*c, T, c->d, h, err);
         g.a0 = {act, T, h, h};
         g.b0 = {wd, d, h, h};
         g.c0 = {y, T, d, d};

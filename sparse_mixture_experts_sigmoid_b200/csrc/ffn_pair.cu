@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     tc_fence_before();
     __syncthreads();
-    cluster_sync_all();
+    cluster_sync_all();   // (release: the remote arrivals have landed)
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc2(tmem, kTmemCols);
 }

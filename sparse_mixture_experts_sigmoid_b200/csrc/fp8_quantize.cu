@@ -252,7 +252,7 @@ moe_status moe_gemm_fp8(int64_t M, int32_t N, int32_t K, const uint8_t *a, const
     if (!err) return MOE_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
-    if (skinny::wants(M, N, K)) {
+    if (skinny::wants(skinny::Form::kFp8, M, N, K)) {
         skinny::Product p{};
         p.fp8 = true;
         p.T = M;

@@ -411,13 +411,37 @@ template <bool FP8, bool GATED>
 cudaError_t launch_form(const Product &g, cudaStream_t s) {
     if (g.T <= 16) return launch_nt<FP8, GATED, 16>(g, s);
     if (g.T <= 32) return launch_nt<FP8, GATED, 32>(g, s);
-    if (g.T <= 64) return launch_nt<FP8, GATED, 64>(g, s);
-    return launch_nt<FP8, GATED, 128>(g, s);
+    // 8 bits: the 128 sums of a thread leave no registers for more tokens a tile
+    // (14336 x 4096, T = 128: 66 us with 128, 32 with 64)
+    if constexpr (FP8) {
+        return launch_nt<true, GATED, 64>(g, s);
+    } else {
+        if (g.T <= 64) return launch_nt<false, GATED, 64>(g, s);
+        return launch_nt<false, GATED, 128>(g, s);
+    }
 }
 
 }  // namespace
 
-bool wants(int64_t T, int N, int K) { return T <= 256; }
+// Measured on both sides (us, this kernel / the 256-row tiles; d x h of the block,
+// or N x K of the 8-bit product):
+//   GATED  640 x 2048: T = 64 21/22, 256 23/23, 1024 29/23;  4096 x 14336: T = 64
+//          112/119, 256 159/126;  1024 x 512 (few tiles): T = 512 23/25, 768 28/25
+//   STORE  2048 x 5632: T = 64 26/45, 768 54/58, 2048 116/101;  4096 x 14336: T = 256
+//          97/126, 768 240/208;  512 x 8192: T = 2048 75/111, 4096 126/114;  K = 512:
+//          27/24 at T = 128
+//   8 bits 14336 x 4096: T = 64 20/33, 128 32/34, 256 62/35;  2048 x 2048: T = 512
+//          13/14, 768 18/14;  640 x 8192: T = 1024 31/39, 2048 56/39
+// The 256-row tiles need enough tiles for the pairs of SMs and a long enough K; this
+// kernel reads the weights again for every 128 (8 bits: 64) tokens.
+bool wants(Form form, int64_t T, int N, int K) {
+    const int64_t tiles = (T + 255) / 256 * ((N + 255) / 256);
+    switch (form) {
+        case Form::kGated: return T <= 64 || 2 * tiles <= 8;
+        case Form::kFp8: return T <= 128 || tiles <= 16;
+        default: return T <= 64 || (tiles <= 24 && K >= 1024);
+    }
+}
 
 cudaError_t launch(const Product &g, cudaStream_t s) {
     if (g.fp8) return launch_form<true, false>(g, s);

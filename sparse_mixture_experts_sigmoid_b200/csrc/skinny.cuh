@@ -24,7 +24,8 @@ struct Product {
     uint32_t *err;
 };
 // Whether the product is one for this kernel (else the 256-row tiles).
-bool wants(int64_t T, int N, int K);
+enum class Form { kStore, kGated, kFp8 };
+bool wants(Form form, int64_t T, int N, int K);
 cudaError_t launch(const Product &p, cudaStream_t s);
 
 }  // namespace skinny
