@@ -13,10 +13,12 @@
 // a stage of the ring is 16 KB of weights.  K is cut into S consecutive ranges,
 // one per CTA of a cluster, so that small weights too have enough CTAs to draw on
 // HBM; two CTAs fit on an SM, so one's set-up and ending run under the other's
-// loads.  Each CTA leaves its fp32 sums in its shared memory; after a cluster
-// barrier each adds 1/S of the tile's rows over the S ranges, in their order
-// (repeated calls give the same bits), through distributed shared memory, applies
-// the activation, and stores.
+// loads.  Each CTA adds 1/S of the tile's rows over the S ranges, in their order
+// (repeated calls give the same bits), applies the activation, and stores.  Up to
+// 64 tokens the CTAs push their sums into the adding CTA's shared memory (beside
+// the ring, which may still be in use there), so that after one cluster barrier
+// everything is local; reading the sums from the other CTAs instead, which 128
+// tokens' sums leave the only way, took 1 to 1.5 us more a product.
 //
 // Every mbarrier wait is bounded as in the grouped kernels.
 #include <cuda_fp16.h>
@@ -40,9 +42,16 @@ constexpr int kThreads = 6 * 32;
 constexpr int kMaxStages = 6;
 constexpr int kSmem = 113 * 1024;          // two CTAs per SM
 
+// Whether the sums are pushed, and the bytes that they take beside the ring.
+template <int NT>
+constexpr bool kPush = NT <= 64;
+template <int NT>
+constexpr int recv_bytes() {
+    return kPush<NT> ? kRows * NT * 4 : 0;
+}
 template <int NT>
 constexpr int stages() {
-    const int s = (kSmem - 1024 - 2048 - 4 * 2 * NT * 4) / (kWStage + NT * 128);
+    const int s = (kSmem - 1024 - 2048 - 4 * 2 * NT * 4 - recv_bytes<NT>()) / (kWStage + NT * 128);
     return s > kMaxStages ? kMaxStages : s;
 }
 
@@ -76,12 +85,31 @@ __device__ __forceinline__ float4 ld_cluster4(const float *p, uint32_t rank) {
                  : "memory");
     return v;
 }
-// The sum over the S CTAs of the cluster of the four floats at p.
-__device__ __forceinline__ void add_ranges(const float *p, int S, float (&o)[4]) {
+// The cluster barrier in halves: every thread arrives when it is set up, and
+// waits before it, or its CTA, goes on to another CTA's shared memory: that CTA
+// has started by then.
+__device__ __forceinline__ void cluster_started() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+// Four floats into the shared memory of CTA `rank`, at this CTA's address p.
+__device__ __forceinline__ void push4(float *p, uint32_t rank, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(mapa_shared(p, rank)), "f"(v.x), "f"(v.y),
+                 "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+// The sum over the S ranges of four floats: at p of every CTA of the cluster
+// (REMOTE), or at p, p + step, ... here.  All reads are in flight before the first
+// is added.
+template <bool REMOTE>
+__device__ __forceinline__ void add_ranges(const float *p, int S, int step, float (&o)[4]) {
     float4 f[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q)
-        if (q < S) f[q] = S > 1 ? ld_cluster4(p, q) : *reinterpret_cast<const float4 *>(p);
+        if (q < S)
+            f[q] = REMOTE && S > 1 ? ld_cluster4(p, q) : *reinterpret_cast<const float4 *>(p + (REMOTE ? 0 : q * step));
     o[0] = f[0].x;
     o[1] = f[0].y;
     o[2] = f[0].z;
@@ -95,7 +123,22 @@ __device__ __forceinline__ void add_ranges(const float *p, int S, float (&o)[4])
             o[3] += f[q].w;
         }
 }
+// u = act(u) v
+__device__ __forceinline__ void gate4(int act, float (&u)[4], const float (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        const float2 a = make_float2(u[j], u[j + 1]), b = make_float2(v[j], v[j + 1]);
+        const float2 o = act == MOE_ACT_SILU ? ffn::gated2<MOE_ACT_SILU>(a, b) : ffn::gated2<MOE_ACT_GELU_TANH>(a, b);
+        u[j] = o.x;
+        u[j + 1] = o.y;
+    }
+}
 
+__device__ __forceinline__ void store1(void *out, int64_t i, float v, int dtype) {
+    if (dtype == MOE_F32) static_cast<float *>(out)[i] = v;
+    else if (dtype == MOE_BF16) static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
+    else static_cast<__half *>(out)[i] = __float2half_rn(v);
+}
 // Elements i .. i + 3 (i a multiple of 4) of a row-major tensor.
 __device__ __forceinline__ void store4(void *out, int64_t i, const float (&v)[4], int dtype) {
     if (dtype == MOE_F32) {
@@ -117,14 +160,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr int kTmemCols = FP8 ? 2 * kBuf : kBuf;
     constexpr int kK = FP8 ? 128 : 64;                     // elements of a K block
     constexpr int kOutRows = GATED ? kRows / 2 : kRows;
-    static_assert(kStages * (kWStage + kXStage) >= kRows * NT * 4, "the sums fit over the ring");
+    static_assert(kPush<NT> || kStages * (kWStage + kXStage) >= kRows * NT * 4, "the sums fit over the ring");
 
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sW = smem, *sX = sW + kStages * kWStage;
-    float *scales = reinterpret_cast<float *>(sX + kStages * kXStage);   // fp8: [4 warps][2][NT]
+    float *recv = reinterpret_cast<float *>(sX + kStages * kXStage);     // [S][NT / 4][rows of this CTA][4]
+    float *scales = recv + recv_bytes<NT>() / 4;                          // fp8: [4 warps][2][NT]
     Ctrl *ctrl = reinterpret_cast<Ctrl *>(scales + (FP8 ? 4 * 2 * NT : 0));
-    float *sums = reinterpret_cast<float *>(smem);         // [NT][128], over the ring once it is drained
+    float *sums = reinterpret_cast<float *>(smem);         // (not pushed) [NT][128], over the drained ring
     volatile int *abort = &ctrl->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -156,10 +200,12 @@ __global__ void __launch_bounds__(kThreads, 2)
         pdl_launch_dependents();
     }
 
+    if (kPush<NT> && p.S > 1) cluster_started();
     const uint32_t tmem = ctrl->tmem_base;
     const int S = p.S, rank = S > 1 ? (int)cluster_rank() : 0;
     const int tile = blockIdx.x / S, tt = tile / p.mt, m = tile - tt * p.mt;
-    const int t0 = tt * NT, n0 = m * kOutRows;
+    const int t0 = tt * NT, n0 = m * kOutRows, nt = min(NT, p.T - t0);
+    const int per = kOutRows / S, width = kRows / S;   // output rows, and sums' rows, of this CTA
     const int k0 = (int)((int64_t)p.kb * rank / S), k1 = (int)((int64_t)p.kb * (rank + 1) / S), nk = k1 - k0;
 
     if (warp == kTmaWarp) {
@@ -239,6 +285,10 @@ __global__ void __launch_bounds__(kThreads, 2)
     } else {
         const uint32_t tb = tmem + ((uint32_t)(warp * 32) << 16);
         const int row = warp * 32 + lane;
+        // where this row's sums go: CTA `owner`, behind those of the ranges before this one
+        const int orow = GATED ? row & (kOutRows - 1) : row, owner = orow / per;
+        [[maybe_unused]] float *to =
+            recv + rank * NT * width + 4 * (orow - owner * per + (GATED && row >= kOutRows ? per : 0));
         if constexpr (FP8) {
             float acc[NT];
 #pragma unroll
@@ -286,59 +336,91 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctrl->tempty[kb & 1]);
             }
-            // every block product has been read, so every load of the ring has
-            // been consumed -- by all four warps, once they have met
-            asm volatile("bar.sync 1, 128;" ::: "memory");
+            if constexpr (kPush<NT>) {
+                if (S > 1) cluster_wait_started();
 #pragma unroll
-            for (int t = 0; t < NT; ++t) sums[t * kRows + row] = acc[t];
+                for (int t = 0; t < NT; t += 4)
+                    if (t < nt) push4(to + t * width, owner, make_float4(acc[t], acc[t + 1], acc[t + 2], acc[t + 3]));
+            } else {
+                // every block product has been read, so every load of the ring has
+                // been consumed -- by all four warps, once they have met
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+#pragma unroll
+                for (int t = 0; t < NT; ++t) sums[t * kRows + row] = acc[t];
+            }
         } else {
             wait_bar(&ctrl->tfull[0], 0, abort, p.err);
             tc_fence_after();
+            if (kPush<NT> && S > 1) cluster_wait_started();
 #pragma unroll
             for (int q = 0; q < NT; q += 16) {
                 float v[16];
                 tmem_ld16(tb + q, v);
                 tmem_wait_ld();
 #pragma unroll
-                for (int z = 0; z < 16; ++z) sums[(q + z) * kRows + row] = v[z];
+                for (int z = 0; z < 16; z += 4) {
+                    if constexpr (kPush<NT>) {
+                        if (q + z < nt) push4(to + (q + z) * width, owner, make_float4(v[z], v[z + 1], v[z + 2], v[z + 3]));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sums[(q + z + e) * kRows + row] = v[z + e];
+                    }
+                }
             }
             tc_fence_before();
         }
     }
+    __syncwarp();
+    if (kPush<NT> && S > 1 && warp >= kTmaWarp) cluster_wait_started();
     if (S > 1) cluster_sync_all();
     else __syncthreads();
     tc_fence_after();
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
     if (warp == kTmaWarp) pdl_wait();   // (its other lanes) before anything is written
 
-    // 1 / S of the tile's rows, four of one token a step, over the S ranges in
-    // their order (all S reads are in flight before the first is added)
-    const int per = kOutRows / S, quads = per / 4, r0 = rank * per, nt = min(NT, p.T - t0);
-    for (int i = threadIdx.x; i < quads * nt; i += kThreads) {
-        const int t = i / quads, r = r0 + 4 * (i - t * quads), n = n0 + r;
-        if (n >= p.N) continue;   // N is a multiple of 8: four rows are in or out together
-        const float *at = sums + t * kRows + r;
-        float u[4], v[4];
-        add_ranges(at, S, u);
-        if (GATED) add_ranges(at + kOutRows, S, v);
-        const int64_t at_out = (int64_t)(t0 + t) * p.N + n;
-        if constexpr (GATED) {
-            if (p.pre) {
+    // 1 / S of the tile's rows, over the S ranges in their order
+    if constexpr (kPush<NT>) {
+        // one row of four tokens a step
+        for (int i = threadIdx.x; i < per * ((nt + 3) / 4); i += kThreads) {
+            const int t = i / per * 4, r = i - (i / per) * per, n = n0 + rank * per + r;
+            if (n >= p.N) continue;
+            const float *at = recv + t * width + 4 * r;
+            float u[4], v[4];
+            add_ranges<false>(at, S, NT * width, u);
+            if (GATED) add_ranges<false>(at + 4 * per, S, NT * width, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (GATED && p.pre && t + e < nt) {
+                    const int64_t b = (int64_t)(t0 + t + e) * 2 * p.N + n;
+                    store1(p.pre, b, u[e], p.out_dtype);
+                    store1(p.pre, b + p.N, v[e], p.out_dtype);
+                }
+            if (GATED) gate4(p.act, u, v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (t + e < nt) store1(p.out, (int64_t)(t0 + t + e) * p.N + n, u[e], p.out_dtype);
+        }
+    } else {
+        // four rows of one token a step
+        const int quads = per / 4, r0 = rank * per;
+        for (int i = threadIdx.x; i < quads * nt; i += kThreads) {
+            const int t = i / quads, r = r0 + 4 * (i - t * quads), n = n0 + r;
+            if (n >= p.N) continue;   // N is a multiple of 8: four rows are in or out together
+            const float *at = sums + t * kRows + r;
+            float u[4], v[4];
+            add_ranges<true>(at, S, 0, u);
+            if (GATED) add_ranges<true>(at + kOutRows, S, 0, v);
+            const int64_t o = (int64_t)(t0 + t) * p.N + n;
+            if (GATED && p.pre) {
                 const int64_t b = (int64_t)(t0 + t) * 2 * p.N + n;
                 store4(p.pre, b, u, p.out_dtype);
                 store4(p.pre, b + p.N, v, p.out_dtype);
             }
-#pragma unroll
-            for (int j = 0; j < 4; j += 2) {
-                const float2 a = make_float2(u[j], u[j + 1]), b = make_float2(v[j], v[j + 1]);
-                const float2 o = p.act == MOE_ACT_SILU ? ffn::gated2<MOE_ACT_SILU>(a, b) : ffn::gated2<MOE_ACT_GELU_TANH>(a, b);
-                u[j] = o.x;
-                u[j + 1] = o.y;
-            }
+            if (GATED) gate4(p.act, u, v);
+            store4(p.out, o, u, p.out_dtype);
         }
-        store4(p.out, at_out, u, p.out_dtype);
+        if (S > 1) cluster_sync_all();   // the others may still be reading this CTA's sums
     }
-    if (S > 1) cluster_sync_all();   // the others may still be reading this CTA's sums
 }
 
 // ------------------------------------------------------------------ host side
@@ -384,7 +466,8 @@ cudaError_t launch_nt(const Product &g, cudaStream_t s) {
     // K ranges: as many as fill two CTAs on every SM, with four K blocks each at least
     p.S = 1;
     while (p.S < 8 && tiles * p.S * 2 <= 2 * num_sms() && p.kb >= 8 * p.S) p.S *= 2;
-    const size_t smem = 1024 + (size_t)stages<NT>() * (kWStage + NT * 128) + (FP8 ? 4 * 2 * NT * 4 : 0) + sizeof(Ctrl);
+    const size_t smem = 1024 + (size_t)stages<NT>() * (kWStage + NT * 128) + recv_bytes<NT>() +
+                        (FP8 ? 4 * 2 * NT * 4 : 0) + sizeof(Ctrl);
     auto kern = skinny_kernel<FP8, GATED, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
