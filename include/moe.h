@@ -485,8 +485,9 @@ moe_status moe_norm_backward(const moe_norm_config *cfg, const void *h, const vo
  *   dx = du W_gate + dv W_up,  dW_gate = du^T x,  dW_up = dv^T x,
  *   dW_down = dy^T a.
  *
- * Accumulation is fp32.  a, and for training u, v, du and dv, are rounded to
- * dtype once each between the products; every output is rounded once. */
+ * Accumulation is fp32.  a, and in the backward pass du and dv, are operands of
+ * the next product and rounded to dtype once each; u and v are kept for the
+ * backward pass in fp32; every output is rounded once. */
 typedef enum { MOE_ACT_SILU = 0, MOE_ACT_GELU_TANH = 1 } moe_ffn_act;
 typedef struct {
     int64_t T;      /* tokens; 0 is allowed */

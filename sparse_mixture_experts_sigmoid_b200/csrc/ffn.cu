@@ -17,14 +17,14 @@ size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 struct Layout {
-    size_t act, pre, grad, total;   // offsets: a [T, h]; u | v [T, 2h]; du | dv [T, 2h]
+    size_t act, pre, grad, total;   // offsets: a [T, h]; u | v [T, 2h] fp32; du | dv [T, 2h]
 };
 Layout layout(const moe_ffn_config &c, bool train) {
     const size_t rows = (size_t)c.T * (size_t)c.h * 2;
     Layout L{};
     L.act = 0;
     L.pre = align256(rows);
-    L.grad = L.pre + (train ? align256(2 * rows) : 0);
+    L.grad = L.pre + (train ? align256(4 * rows) : 0);
     L.total = L.grad + (train ? align256(2 * rows) : 0);
     return L;
 }
@@ -83,7 +83,7 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
         p.w0 = wg;
         p.w1 = wu;
         p.out = act;
-        p.pre = train ? pre : nullptr;
+        p.pre = train ? reinterpret_cast<float *>(pre) : nullptr;
         p.act = c->act;
         e = skinny::launch(p, s);
     } else {
@@ -94,7 +94,7 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
         g.c0 = {act, T, h, h};
         if (train) {
             g.c1 = {pre, T, h, 2 * h};
-            g.c2 = {pre + 2 * h, T, h, 2 * h};
+            g.c2 = {pre + 4 * h, T, h, 2 * h};
         }
         e = launch_gated(g, s);
     }
@@ -176,8 +176,7 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
         Gemm g = product(*c, T, c->h, d, err);
         g.a0 = {dy, T, d, d};
         g.b0 = {w_down, d, h, h};
-        g.u = {pre, T, h, 2 * h};
-        g.v = {pre + 2 * h, T, h, 2 * h};
+        g.pre = reinterpret_cast<const float *>(pre);
         g.c0 = du;
         g.c1 = dv;
         e = launch_dgated(g, s);

@@ -11,7 +11,7 @@
 namespace moe {
 namespace ffn {
 
-// A row-major matrix of 16-bit elements, row stride ld elements.
+// A row-major matrix of 16-bit elements (u and v: fp32), row stride ld elements.
 struct Matrix {
     const void *base;
     int64_t rows, cols, ld;
@@ -25,7 +25,7 @@ struct Gemm {
     bool a_mn;           // the reduction runs over A's rows (launch_grads)
     Matrix a0, a1, b0, b1;
     Matrix c0, c1, c2;   // GATED: act, and u, v (base null: not kept); STORE: C (C1: second half); DGATED: du, dv
-    Matrix u, v;         // DGATED: the kept pre-activations
+    const float *pre;    // DGATED: the kept u | v, rows of 2 N
     int64_t M, K;        // K per range
     int N;
     int ranges, halves;

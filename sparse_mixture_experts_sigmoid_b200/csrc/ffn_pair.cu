@@ -52,7 +52,6 @@ struct Ctrl {
     uint64_t tfull[2];            // both: accumulator ready
     uint64_t tempty[2];           // even CTA: accumulator released by both epilogues
     uint64_t done;                // both: all MMAs of the pair completed
-    uint64_t kept[kEpiWarps];     // DGATED: an epilogue warp's u and v landed
     uint32_t tmem_base;
     int abort;
 };
@@ -86,6 +85,7 @@ struct Params {
     int act;           // moe_ffn_act
     uint32_t fmt;      // operand format of the instruction descriptor: 0 fp16, 1 bf16
     bool keep;         // GATED: store u and v as well
+    const float *pre;  // DGATED: the kept u | v, rows of 2 N
     uint32_t *err;
 };
 
@@ -97,7 +97,6 @@ template <int NJOBS>
 struct Maps {
     JobMaps job[NJOBS];
     CUtensorMap c2;               // GATED: v
-    CUtensorMap u, v;             // DGATED: the kept pre-activations
 };
 
 // How the operands lie: both K-major; B MN-major; or (several jobs) B MN-major
@@ -175,25 +174,45 @@ __device__ __forceinline__ void gate(float (&g)[64], const float (&u)[64]) {
         g[i + 1] = a.y;
     }
 }
-// DGATED: this lane's row of 64 columns, u and v in its boxes and r in f: du and
-// dv in their place.
-template <int ACT>
-__device__ __forceinline__ void gate_grad(uint8_t *box_u, uint8_t *box_v, const float (&f)[64], uint32_t fmt) {
+// DGATED: the kept u and v of 16 columns of a lane's row, by 32-byte loads (whole
+// sectors: the lanes' rows lie apart).  Columns past N are not read.
+struct Kept {
+    float u[16], v[16];
+    __device__ __forceinline__ static void load8f(const float *p, float *o) {
+        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
+                     : "l"(p));
+    }
+    __device__ __forceinline__ void load(const float *pre, int r, int c, const Job &j) {
+        const float *at = pre + (int64_t)r * 2 * j.N + c;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        uint4 wu = *box_word(box_u, j), wv = *box_word(box_v, j);
-        uint32_t *pu = reinterpret_cast<uint32_t *>(&wu), *pv = reinterpret_cast<uint32_t *>(&wv);
+        for (int k = 0; k < 16; k += 8) {
+            if (r < j.M && c + k < j.N) {
+                load8f(at + k, u + k);
+                load8f(at + j.N + k, v + k);
+            }
+        }
+    }
+};
+// du and dv of those columns into words k and k + 1 of the lane's rows of two boxes.
+template <int ACT>
+__device__ __forceinline__ void gate_grad(const Kept &x, const float (&f)[16], uint32_t fmt, uint8_t *box_u,
+                                          uint8_t *box_v, int k) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        uint32_t wu[4], wv[4];
 #pragma unroll
         for (int z = 0; z < 4; ++z) {
-            const float2 r = make_float2(f[8 * j + 2 * z], f[8 * j + 2 * z + 1]);
+            const int i = 8 * h + 2 * z;
+            const float2 r = make_float2(f[i], f[i + 1]);
             float2 a, da;
-            act_grad2<ACT>(unpack2(pu[z], fmt), a, da);
-            const float2 du = mul2(mul2(r, unpack2(pv[z], fmt)), da), dv = mul2(r, a);
-            pu[z] = pack2(du.x, du.y, fmt);
-            pv[z] = pack2(dv.x, dv.y, fmt);
+            act_grad2<ACT>(make_float2(x.u[i], x.u[i + 1]), a, da);
+            const float2 du = mul2(mul2(r, make_float2(x.v[i], x.v[i + 1])), da), dv = mul2(r, a);
+            wu[z] = pack2(du.x, du.y, fmt);
+            wv[z] = pack2(dv.x, dv.y, fmt);
         }
-        *box_word(box_u, j) = wu;
-        *box_word(box_v, j) = wv;
+        *box_word(box_u, k + h) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
+        *box_word(box_v, k + h) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
     }
 }
 
@@ -226,7 +245,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctrl->tfull[a], 1);
             mbar_init(&ctrl->tempty[a], 2 * kEpiWarps);
         }
-        for (int w = 0; w < kEpiWarps; ++w) mbar_init(&ctrl->kept[w], 1);
         mbar_init(&ctrl->done, 1);
         ctrl->abort = 0;
         fence_barrier_init();
@@ -343,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int cw = (warp >> 2) * kWarpCols;   // this warp's first output column of the tile
         uint8_t *box = sEpi + warp * (epi_bytes<EPI>() / kEpiWarps), *box2 = box + kBox;
-        [[maybe_unused]] uint32_t loads = 0;      // DGATED: u, v box loads issued so far
         // stores the packed 64 columns of this warp's 32 rows (8 words a row)
         auto put = [&](const CUtensorMap *m, const uint4 (&w)[8], int c, int r, const Job &j) {
             if (lane == 0) bulk_wait_read();   // the previous store has left the box
@@ -363,20 +380,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 w[j] = make_uint4(pack2(f[8 * j], f[8 * j + 1], p.fmt), pack2(f[8 * j + 2], f[8 * j + 3], p.fmt),
                                   pack2(f[8 * j + 4], f[8 * j + 5], p.fmt), pack2(f[8 * j + 6], f[8 * j + 7], p.fmt));
         };
+        auto words = [&](const float *f, uint4 (&w)[8]) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                w[j] = make_uint4(__float_as_uint(f[4 * j]), __float_as_uint(f[4 * j + 1]), __float_as_uint(f[4 * j + 2]),
+                                  __float_as_uint(f[4 * j + 3]));
+        };
         auto read64 = [&](uint32_t at, float (&f)[64]) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld16(at + 16 * q, *reinterpret_cast<float(*)[16]>(&f[16 * q]));
             tmem_wait_ld();
-        };
-        // DGATED: the kept u and v of 64 columns from c into the warp's two boxes
-        auto ask = [&](int c, int r) {
-            if (lane == 0) {
-                bulk_wait_read();
-                mbar_expect_tx(&ctrl->kept[warp], 2 * kBox);
-                tma_load_2d(&maps.u, box, &ctrl->kept[warp], c, r);
-                tma_load_2d(&maps.v, box2, &ctrl->kept[warp], c, r);
-            }
-            ++loads;
         };
         Tile t;
         for (int tc = 0; tile_at(tc, pair, npairs, p, t); ++tc) {
@@ -384,19 +397,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const JobMaps &jm = maps.job[FORM == GRADS ? t.job : 0];
             const uint32_t acc = tc & 1;
             const int r = t.m * kBM + (int)rank * 128 + (warp & 3) * 32, c0 = t.n * kCols + cw;
-            if constexpr (EPI == DGATED) {
-                if (r < j.M && c0 < j.N) ask(c0, r);
-            }
-            if (!wait_bar(&ctrl->tfull[acc], (tc >> 1) & 1, abort, p.err)) {
-                if constexpr (EPI == DGATED) {
-                    // the copies into this warp's boxes land before the CTA leaves
-                    const uint64_t t0 = globaltimer();
-                    while (loads && !mbar_try_wait(&ctrl->kept[warp], (loads - 1) & 1) &&
-                           globaltimer() - t0 < 100000000ull) {
-                    }
-                }
-                break;
-            }
+            [[maybe_unused]] Kept kept;   // DGATED: the first columns' u and v, asked for before r is ready
+            if constexpr (EPI == DGATED) kept.load(p.pre, r + lane, c0, j);
+            if (!wait_bar(&ctrl->tfull[acc], (tc >> 1) & 1, abort, p.err)) break;
             tc_fence_after();
             const uint32_t tb = tmem + acc * BN + lane_base;
             if (r < j.M && c0 < j.N) {
@@ -417,10 +420,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                     read64(tb + cw, g);
                     read64(tb + BN / 2 + cw, u);
                     if (p.keep) {
-                        pack(g, w);
-                        put(&jm.c1, w, c0, r, j);
-                        pack(u, w);
-                        put(&maps.c2, w, c0, r, j);
+                        // fp32, 32 columns a box
+#pragma unroll
+                        for (int q = 0; q < 64; q += 32) {
+                            words(&g[q], w);
+                            put(&jm.c1, w, c0 + q, r, j);
+                            words(&u[q], w);
+                            put(&maps.c2, w, c0 + q, r, j);
+                        }
                     }
                     if (p.act == MOE_ACT_SILU) gate<MOE_ACT_SILU>(g, u);
                     else gate<MOE_ACT_GELU_TANH>(g, u);
@@ -430,14 +437,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
                     for (int q = 0; q < kWarpCols; q += 64) {
                         if (c0 + q >= j.N) break;
-                        if (q) ask(c0 + q, r);
-                        if (!wait_bar(&ctrl->kept[warp], (loads - 1) & 1, abort, p.err)) break;
-                        float f[64];
-                        read64(tb + cw + q, f);
-                        // one loop per activation: a branch inside would keep the
-                        // elements' chains (exponential, reciprocal) from overlapping
-                        if (p.act == MOE_ACT_SILU) gate_grad<MOE_ACT_SILU>(box, box2, f, p.fmt);
-                        else gate_grad<MOE_ACT_GELU_TANH>(box, box2, f, p.fmt);
+                        if (lane == 0) bulk_wait_read();   // the previous stores have left the boxes
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 64; k += 16) {
+                            const Kept now = kept;
+                            if (q + k + 16 < kWarpCols) kept.load(p.pre, r + lane, c0 + q + k + 16, j);
+                            float f[16];
+                            tmem_ld16(tb + cw + q + k, f);
+                            tmem_wait_ld();
+                            // one loop per activation: a branch inside would keep the
+                            // elements' chains (exponential, reciprocal) from overlapping
+                            if (p.act == MOE_ACT_SILU) gate_grad<MOE_ACT_SILU>(now, f, p.fmt, box, box2, k / 8);
+                            else gate_grad<MOE_ACT_GELU_TANH>(now, f, p.fmt, box, box2, k / 8);
+                        }
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) {
@@ -474,16 +487,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host side
 
-// A row-major matrix of 16-bit elements, boxes of 64 columns (128 bytes, 128-byte
-// swizzle) by box_rows; what lies outside reads as zero and is not written.
-bool make_map16(CUtensorMap *m, const Matrix &x, uint32_t box_rows) {
+// A row-major matrix of 16-bit (or fp32) elements, boxes of 128 bytes of columns
+// (128-byte swizzle) by box_rows; what lies outside reads as zero and is not
+// written.
+bool make_map16(CUtensorMap *m, const Matrix &x, uint32_t box_rows, bool f32 = false) {
     auto fn = encode_fn();
     if (!fn || !x.base) return false;
+    const uint32_t size = f32 ? 4 : 2;
     cuuint64_t dims[2] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows};
-    cuuint64_t strides[1] = {(cuuint64_t)x.ld * 2};
-    cuuint32_t box[2] = {64, box_rows};
+    cuuint64_t strides[1] = {(cuuint64_t)x.ld * size};
+    cuuint32_t box[2] = {128 / size, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(x.base), dims, strides, box, estr,
+    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(x.base), dims, strides, box, estr,
               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -498,7 +513,7 @@ bool set_job(const Gemm &g, int i, M &maps, Params &p) {
     if (!make_map16(&m.a0, g.a0, ab) || !make_map16(&m.b0, g.b0, bb) || !make_map16(&m.c0, g.c0, 32)) return false;
     if (g.a1.base && !make_map16(&m.a1, g.a1, ab)) return false;
     if (g.b1.base && !make_map16(&m.b1, g.b1, bb)) return false;
-    if (g.c1.base && !make_map16(&m.c1, g.c1, 32)) return false;
+    if (g.c1.base && !make_map16(&m.c1, g.c1, 32, EPI == GATED)) return false;   // GATED: u, fp32
     Job &j = p.job[i];
     j.M = (int)g.M;
     j.N = g.N;
@@ -517,12 +532,12 @@ cudaError_t launch(const Gemm *g, int n, cudaStream_t s) {
     Params p{};
     for (int i = 0; i < n; ++i)
         if (!set_job<FORM, EPI>(g[i], i, maps, p)) return cudaErrorInvalidValue;
-    if (g->c2.base && !make_map16(&maps.c2, g->c2, 32)) return cudaErrorInvalidValue;
-    if (EPI == DGATED && (!make_map16(&maps.u, g->u, 32) || !make_map16(&maps.v, g->v, 32))) return cudaErrorInvalidValue;
+    if (g->c2.base && !make_map16(&maps.c2, g->c2, 32, true)) return cudaErrorInvalidValue;
     p.njobs = n;
     p.act = g->act;
     p.fmt = g->bf16 ? 1u : 0u;
     p.keep = g->c1.base != nullptr;
+    p.pre = g->pre;
     p.err = g->err;
     for (int i = 1; i < n; ++i) p.rest += p.job[i].tiles;
     const int64_t tiles = (int64_t)p.job[0].tiles + p.rest;

@@ -69,7 +69,7 @@ struct Params {
     const float *sx, *sw;
     void *out;
     int out_dtype;
-    void *pre;
+    float *pre;
     int act;
     uint32_t fmt;         // 16-bit operand format of the instruction descriptor: 0 fp16, 1 bf16
     bool early;
@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < 4; ++e)
                 if (GATED && p.pre && t + e < nt) {
                     const int64_t b = (int64_t)(t0 + t + e) * 2 * p.N + n;
-                    store1(p.pre, b, u[e], p.out_dtype);
-                    store1(p.pre, b + p.N, v[e], p.out_dtype);
+                    p.pre[b] = u[e];
+                    p.pre[b + p.N] = v[e];
                 }
             if (GATED) gate4(p.act, u, v);
 #pragma unroll
@@ -413,8 +413,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const int64_t o = (int64_t)(t0 + t) * p.N + n;
             if (GATED && p.pre) {
                 const int64_t b = (int64_t)(t0 + t) * 2 * p.N + n;
-                store4(p.pre, b, u, p.out_dtype);
-                store4(p.pre, b + p.N, v, p.out_dtype);
+                store4(p.pre, b, u, MOE_F32);
+                store4(p.pre, b + p.N, v, MOE_F32);
             }
             if (GATED) gate4(p.act, u, v);
             store4(p.out, o, u, p.out_dtype);

@@ -17,7 +17,7 @@ struct Product {
     const float *sx, *sw;
     void *out;                 // [T, N]
     int out_dtype;
-    void *pre;                 // GATED, optional: [T, 2N] u | v in the operands' type
+    float *pre;                // GATED, optional: [T, 2N] u | v
     int act;                   // moe_ffn_act
     bool early;                // the kernel before this one in the stream does not write the weights:
                                // they are requested before it has completed
