@@ -166,6 +166,9 @@ def _elem_dtype(cfg: MoEConfig):
 def _ptr(t: torch.Tensor | None, name: str, shape=None, dtype=None, dev=None):
     if t is None:
         return None
+    # what a small call pays for each of its tensors: the checks in one expression, the message apart
+    if t.get_device() == dev and t.dtype is dtype and (shape is None or t.shape == shape) and t.is_contiguous():
+        return t.data_ptr()
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if dev is not None and t.get_device() != dev:
@@ -650,11 +653,11 @@ def norm_forward(cfg: NormConfig, x, weight, bias=None, residual=None, y=None, h
     if h is None and residual is not None:
         h = torch.empty_like(x)
     mean = x.new_empty(cfg.T, dtype=torch.float32) if want_stats and cfg.kind == 0 else None
-    rstd = x.new_empty(cfg.T, dtype=torch.float32) if want_stats else None
+    rstd = None if not want_stats else x.new_empty(cfg.T, dtype=torch.float32) if mean is None else torch.empty_like(mean)
     _check(lib().moe_norm_forward(ctypes.byref(cfg), px, _ptr(residual, "residual", rows, dt, dev),
                                   _ptr(weight, "weight", (cfg.d,), wt, dev), _ptr(bias, "bias", (cfg.d,), wt, dev),
-                                  _ptr(h, "h", rows, dt, dev), _ptr(y, "y", rows, dt, dev), _ptr(mean, "mean"),
-                                  _ptr(rstd, "rstd"), _stream(stream)), "moe_norm_forward")
+                                  _ptr(h, "h", rows, dt, dev), _ptr(y, "y", rows, dt, dev), None if mean is None else mean.data_ptr(),
+                                  None if rstd is None else rstd.data_ptr(), _stream(stream)), "moe_norm_forward")
     return y, h, mean, rstd
 
 
@@ -668,17 +671,17 @@ def norm_backward(cfg: NormConfig, h, weight, mean, rstd, dy, dh=None, dx=None, 
     ph = _ptr(h, "h", rows, dt, dev)
     if dx is None:
         dx = torch.empty_like(h)
-    dweight = h.new_empty(cfg.d, dtype=torch.float32) if want_weight else None
-    dbias = h.new_empty(cfg.d, dtype=torch.float32) if want_bias else None
+    dweight = torch.empty_like(weight, dtype=torch.float32) if want_weight else None
+    dbias = torch.empty_like(weight, dtype=torch.float32) if want_bias else None
     if ws is None and (want_weight or want_bias):
         ws = h.new_empty(max(norm_workspace_size(cfg), 1), dtype=torch.uint8)
     f32 = torch.float32
     _check(lib().moe_norm_backward(ctypes.byref(cfg), ph, _ptr(weight, "weight", (cfg.d,), wt, dev),
                                    _ptr(mean, "mean", (cfg.T,), f32, dev), _ptr(rstd, "rstd", (cfg.T,), f32, dev),
                                    _ptr(dy, "dy", rows, dt, dev), _ptr(dh, "dh", rows, dt, dev),
-                                   _ptr(dx, "dx", rows, dt, dev), _ptr(dweight, "dweight"), _ptr(dbias, "dbias"),
-                                   _ptr(ws, "ws", dtype=torch.uint8, dev=dev), 0 if ws is None else ws.numel(),
-                                   _stream(stream)), "moe_norm_backward")
+                                   _ptr(dx, "dx", rows, dt, dev), None if dweight is None else dweight.data_ptr(),
+                                   None if dbias is None else dbias.data_ptr(), _ptr(ws, "ws", None, torch.uint8, dev),
+                                   0 if ws is None else ws.numel(), _stream(stream)), "moe_norm_backward")
     return dx, dweight, dbias
 
 
