@@ -507,7 +507,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
 constexpr int kRing = 4;
 
 template <typename T, int VPT, bool DB>
-__global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(NormBwd a) {
+__global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_bwd_ring_kernel(NormBwd a) {
+    // three words a thread leave no registers for the weights: they stay in
+    // shared memory, as fp32
+    constexpr bool W_SHARED = VPT == 3;
     constexpr int E = kElems<T>, P = kPairs<T>;
     __shared__ float2 red[8 * 32];
     __shared__ uint64_t landed[8][kRing];
@@ -551,9 +554,15 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(NormBwd a) {
     if (i == 0)
         for (int k = 0; k < kRing - 1; ++k)
             if (r + k * step < a.T) request(r + k * step, k);
-    float2 w[VPT][P];          // this thread's weights, for all its rows
+    float2 w[W_SHARED ? 1 : VPT][P];   // this thread's weights, for all its rows
+    float *shared_w = reinterpret_cast<float *>(ring + (size_t)a.groups * kRing * stage);
+    if constexpr (W_SHARED) {
+        for (int c = threadIdx.x; c < d; c += blockDim.x) shared_w[c] = param<T>(a.weight, wf32, c);
+        __syncthreads();
+    } else {
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) load_param<T, false>(a.weight, wf32, c0 + j * cj, d, w[j]);
+        for (int j = 0; j < VPT; ++j) load_param<T, false>(a.weight, wf32, c0 + j * cj, d, w[j]);
+    }
     float nm[2] = {0.f, 0.f}, ns[2] = {0.f, 0.f};   // the statistics of the next two rows
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -580,13 +589,22 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_ring_kernel(NormBwd a) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const bool in = c0 + j * cj < d;
+            if constexpr (W_SHARED) {
+#pragma unroll
+                for (int q = 0; q < P; q += 2) {
+                    const float4 f = in ? *reinterpret_cast<const float4 *>(shared_w + c0 + j * cj + 2 * q)
+                                        : make_float4(0.f, 0.f, 0.f, 0.f);
+                    w[0][q] = make_float2(f.x, f.y);
+                    w[0][q + 1] = make_float2(f.z, f.w);
+                }
+            }
             float2 y[P];
             unpack<T>(in ? h[j * G] : make_uint4(0, 0, 0, 0), z[j]);
             unpack<T>(in ? dy[j * G] : make_uint4(0, 0, 0, 0), y);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
                 z[j][q] = add2(z[j][q], both(-mean));
-                g[j][q] = mul2(y[q], w[j][q]);
+                g[j][q] = mul2(y[q], w[W_SHARED ? 0 : j][q]);
                 sg = add2(sg, g[j][q]);
                 sz = fma2(g[j][q], z[j][q], sz);
                 dw[j][q] = fma2(mul2(y[q], both(rstd)), z[j][q], dw[j][q]);
@@ -863,11 +881,13 @@ auto bwd_kernel(const Spread &s, bool db) -> void (*)(NormBwd) {
     return db ? bwd_words<T, true>(s) : bwd_words<T, false>(s);
 }
 // Dynamic shared memory of that kernel: the columns' sums of a block's groups,
-// or the ring, whose memory the sums take when it is drained.
+// or the ring (and the weights after it), whose memory the sums take when it is
+// drained.
 size_t bwd_smem(const Spread &s, int d, int elem, bool more) {
     const size_t sums = s.groups > 1 || s.vpt == 0 ? 2 * sizeof(float) * (size_t)d : 0;
     if (s.vpt == 0 || s.shift || s.vpt > 3) return sums;
-    return std::max(sums, (size_t)s.groups * kRing * (more ? 3 : 2) * (size_t)d * elem);
+    const size_t weights = s.vpt == 3 ? sizeof(float) * (size_t)d : 0;
+    return std::max(sums, (size_t)s.groups * kRing * (more ? 3 : 2) * (size_t)d * elem + weights);
 }
 
 moe_status check(const moe_norm_config *c) {
