@@ -637,8 +637,36 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
         }
     }
     if (!a.part) return;
-    __syncthreads();           // the ring is drained: its memory holds the columns' sums
-    write_part<T, VPT, false, DB>(a, reinterpret_cast<float *>(ring), group, c0, cj, dw, db);
+    // the ring is drained: each group's sums go there, [groups][dw, db][d], and
+    // every column is added over the groups in their order
+    constexpr int H = DB ? 2 : 1;
+    float *cols = reinterpret_cast<float *>(ring), *out = a.part + (int64_t)blockIdx.x * 2 * d;
+    float *to = a.groups > 1 ? cols + (size_t)group * H * d : out;
+    if (a.groups > 1) __syncthreads();
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = c0 + j * cj;
+        if (c >= d) continue;
+#pragma unroll
+        for (int q = 0; q < P; q += 2) {
+            const float2 u = dw[j][q], v = dw[j][q + 1];
+            *reinterpret_cast<float4 *>(to + c + 2 * q) = make_float4(u.x, u.y, v.x, v.y);
+            if constexpr (DB) {
+                const float2 x = db[j][q], y = db[j][q + 1];
+                *reinterpret_cast<float4 *>(to + d + c + 2 * q) = make_float4(x.x, x.y, y.x, y.y);
+            }
+        }
+    }
+    if (a.groups == 1) return;
+    __syncthreads();
+    for (int c = threadIdx.x * 4; c < H * d; c += blockDim.x * 4) {
+        float4 f = *reinterpret_cast<const float4 *>(cols + c);
+        for (int k = 1; k < a.groups; ++k) {
+            const float4 b = *reinterpret_cast<const float4 *>(cols + (size_t)k * H * d + c);
+            f = make_float4(f.x + b.x, f.y + b.y, f.z + b.z, f.w + b.w);
+        }
+        *reinterpret_cast<float4 *>(out + c) = f;
+    }
 }
 
 // Any width and alignment: one block per row at a time, its columns strided
@@ -881,8 +909,8 @@ auto bwd_kernel(const Spread &s, bool db) -> void (*)(NormBwd) {
     return db ? bwd_words<T, true>(s) : bwd_words<T, false>(s);
 }
 // Dynamic shared memory of that kernel: the columns' sums of a block's groups,
-// or the ring (and the weights after it), whose memory the sums take when it is
-// drained.
+// or the ring (and the weights after it), whose memory the groups' sums take when
+// it is drained (4 * 2 * 16 bits a column and group at least, the sums 2 * 32).
 size_t bwd_smem(const Spread &s, int d, int elem, bool more) {
     const size_t sums = s.groups > 1 || s.vpt == 0 ? 2 * sizeof(float) * (size_t)d : 0;
     if (s.vpt == 0 || s.shift || s.vpt > 3) return sums;
