@@ -76,7 +76,7 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
     p.err = err;
     cudaError_t e;
     if (skinny::wants(skinny::Form::kGated, T, c->h, c->d)) {
-        p.gated = true;
+        p.form = skinny::Form::kGated;
         p.N = c->h;
         p.K = c->d;
         p.x = x;
@@ -100,7 +100,7 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
     }
     if (e != cudaSuccess) return MOE_ERR_CUDA;
     if (skinny::wants(skinny::Form::kStore, T, c->d, c->h)) {
-        p.gated = false;
+        p.form = skinny::Form::kStore;
         p.N = c->d;
         p.K = c->h;
         p.x = act;
@@ -172,7 +172,22 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
     char *act = static_cast<char *>(ws) + L.act, *pre = static_cast<char *>(ws) + L.pre,
          *grad = static_cast<char *>(ws) + L.grad;
     const Matrix du{grad, T, h, 2 * h}, dv{grad + 2 * h, T, h, 2 * h};
-    if (inner) {
+    skinny::Product p{};
+    p.bf16 = c->dtype == MOE_BF16;
+    p.T = T;
+    p.out_dtype = c->dtype;
+    p.act = c->act;
+    p.err = err;
+    if (inner && skinny::wants(skinny::Form::kDGated, T, c->h, c->d)) {
+        p.form = skinny::Form::kDGated;
+        p.N = c->h;
+        p.K = c->d;
+        p.x = dy;
+        p.w0 = w_down;
+        p.pre = reinterpret_cast<float *>(pre);
+        p.out = grad;
+        e = skinny::launch(p, s);
+    } else if (inner) {
         Gemm g = product(*c, T, c->h, d, err);
         g.a0 = {dy, T, d, d};
         g.b0 = {w_down, d, h, h};
@@ -181,10 +196,23 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
         g.c1 = dv;
         e = launch_dgated(g, s);
     }
-    // the rest in one launch: dx, then the weights' gradients (all over the T tokens)
+    // the rest in one launch: dx, then the weights' gradients (all over the T
+    // tokens); dx of few tokens by itself
     Gemm g[3];
     int n = 0;
-    if (dx) {
+    if (e == cudaSuccess && dx && skinny::wants(skinny::Form::kDx, T, c->d, c->h)) {
+        p.form = skinny::Form::kDx;
+        p.N = c->d;
+        p.K = c->h;
+        p.ldx = 2 * h;
+        p.x = du.base;
+        p.x1 = dv.base;
+        p.w0 = w_gate;
+        p.w1 = w_up;
+        p.out = dx;
+        p.early = true;   // the kernel before is the one above
+        e = skinny::launch(p, s);
+    } else if (dx) {
         g[n] = product(*c, T, c->d, h, err);
         g[n].ranges = 2;
         g[n].a0 = du;
@@ -210,7 +238,7 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
         g[n].b0 = {act, T, h, h};
         g[n++].c0 = {dw_down, d, h, h};
     }
-    if (e == cudaSuccess) e = launch_grads(g, n, s);
+    if (e == cudaSuccess && n) e = launch_grads(g, n, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -7,6 +7,7 @@
 
 #include "moe_internal.cuh"
 #include "packed.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace ffn {
@@ -40,6 +41,16 @@ cudaError_t launch_dgated(const Gemm &g, cudaStream_t s);
 // C = A B, or A^T B (a_mn), of up to three products in one launch; the second and
 // third have the same K.
 cudaError_t launch_grads(const Gemm *g, int n, cudaStream_t s);
+
+// Shared-memory descriptor of an MN-major operand of 64 k-rows (128-byte swizzle):
+// atoms of 64 columns, kAtom bytes apart; 8-row groups 1 KB apart; a K slice of 16
+// rows is 2 KB on.
+constexpr int kAtom = 8192;   // 64 k-rows x 128 bytes
+__device__ __forceinline__ uint64_t desc_mn(const void *p) {
+    const uint32_t a = tc::smem_u32(p);
+    return (uint64_t)((a & 0x3FFFF) >> 4) | ((uint64_t)(kAtom >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
 
 // ------------------------------------------------------------------ elements
 

@@ -113,12 +113,6 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
-__device__ __forceinline__ uint64_t desc_mn(const void *p) {
-    const uint32_t a = smem_u32(p);
-    return (uint64_t)((a & 0x3FFFF) >> 4) | ((uint64_t)(kAtom >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-
 // The k-th tile of a pair: its job, half, row and column tile; false past the
 // last.  Row tiles of a job run in groups of eight with the column tiles outside
 // them, so that the pairs at work at one time read about as many rows of A as of

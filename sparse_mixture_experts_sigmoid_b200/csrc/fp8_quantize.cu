@@ -254,7 +254,7 @@ moe_status moe_gemm_fp8(int64_t M, int32_t N, int32_t K, const uint8_t *a, const
     cudaError_t e;
     if (skinny::wants(skinny::Form::kFp8, M, N, K)) {
         skinny::Product p{};
-        p.fp8 = true;
+        p.form = skinny::Form::kFp8;
         p.T = M;
         p.N = N;
         p.K = K;

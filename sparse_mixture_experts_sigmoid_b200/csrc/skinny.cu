@@ -2,9 +2,12 @@
 //
 //   STORE : out[t, n] = sum_k x[t, k] w[n, k]
 //   GATED : out[t, n] = act(u) v,  u = x w0^T, v = x w1^T  (u, v kept for training)
+//   DX    : out[t, n] = sum_k x0[t, k] w0[k, n] + x1[t, k] w1[k, n]
+//   DGATED: r = x w (w [K, N]);  du = r v act'(u), dv = r act(u) from the kept u, v
 //
-// for bf16 / fp16 operands, and (STORE) e4m3 operands with a scale per row and
-// 128 columns of x and per 128 x 128 block of w.
+// for bf16 / fp16 operands, and (FP8, as STORE) e4m3 operands with a scale per row
+// and 128 columns of x and per 128 x 128 block of w.  The backward pass's weights
+// are read as they lie, with the reduction over their rows (MN-major).
 //
 // Such a product reads each weight once and is bound by that: the kernel keeps
 // weight bytes in flight and does little else.  The weight rows are the M of the
@@ -65,6 +68,7 @@ struct Ctrl {
 
 struct Params {
     int T, N, kb;         // kb: K blocks of 128 bytes
+    int kr;               // DX: those of the first of the two K ranges
     int S, mt;            // cluster size; weight tiles
     const float *sx, *sw;
     void *out;
@@ -134,6 +138,22 @@ __device__ __forceinline__ void gate4(int act, float (&u)[4], const float (&v)[4
     }
 }
 
+// From the kept u, v and r: u = du = r v act'(u), v = dv = r act(u).
+__device__ __forceinline__ void grad4(int act, const float (&r)[4], float (&u)[4], float (&v)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; j += 2) {
+        const float2 rr = make_float2(r[j], r[j + 1]), vv = make_float2(v[j], v[j + 1]);
+        float2 a, da;
+        if (act == MOE_ACT_SILU) ffn::act_grad2<MOE_ACT_SILU>(make_float2(u[j], u[j + 1]), a, da);
+        else ffn::act_grad2<MOE_ACT_GELU_TANH>(make_float2(u[j], u[j + 1]), a, da);
+        const float2 du = mul2(mul2(rr, vv), da), dv = mul2(rr, a);
+        u[j] = du.x;
+        u[j + 1] = du.y;
+        v[j] = dv.x;
+        v[j + 1] = dv.y;
+    }
+}
+
 __device__ __forceinline__ void store1(void *out, int64_t i, float v, int dtype) {
     if (dtype == MOE_F32) static_cast<float *>(out)[i] = v;
     else if (dtype == MOE_BF16) static_cast<__nv_bfloat16 *>(out)[i] = __float2bfloat16_rn(v);
@@ -150,10 +170,12 @@ __device__ __forceinline__ void store4(void *out, int64_t i, const float (&v)[4]
     }
 }
 
-template <bool FP8, bool GATED, int NT>
+template <Form F, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
-    skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW0,
-                  const __grid_constant__ CUtensorMap tmW1, Params p) {
+    skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX1,
+                  const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1, Params p) {
+    constexpr bool FP8 = F == Form::kFp8, GATED = F == Form::kGated, DX = F == Form::kDx, DGATED = F == Form::kDGated;
+    constexpr bool MN = DX || DGATED;                      // the weights' rows are the reduction
     constexpr int kStages = stages<NT>();
     constexpr int kXStage = NT * 128;
     constexpr int kBuf = NT < 32 ? 32 : NT;                // TMEM columns of one accumulator
@@ -188,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kTmaWarp && lane == 0) {
         prefetch_tmap(&tmX);
         prefetch_tmap(&tmW0);
-        if (GATED) prefetch_tmap(&tmW1);
+        if (GATED || DX) prefetch_tmap(&tmW1);
     }
     if (!p.early) pdl_wait();
     tc_fence_before();
@@ -211,10 +233,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kTmaWarp) {
         if (lane == 0) {
             const uint64_t policy = l2_evict_first_policy();   // a weight is read by this CTA only, or soon by few
+            // K block kb of this CTA's range: its range of K (DX) and column in it
             auto weights = [&](int s, int kb) {
                 uint8_t *w = sW + s * kWStage;
-                const int k = (k0 + kb) * kK;
-                if constexpr (GATED) {
+                const bool second = DX && k0 + kb >= p.kr;
+                const int k = (k0 + kb - (second ? p.kr : 0)) * kK;
+                if constexpr (MN) {
+                    const CUtensorMap *m = second ? &tmW1 : &tmW0;
+                    tma_load_2d_hint(m, w, &ctrl->full[s], n0, k, policy);
+                    tma_load_2d_hint(m, w + kWStage / 2, &ctrl->full[s], n0 + 64, k, policy);
+                } else if constexpr (GATED) {
                     tma_load_2d_hint(&tmW0, w, &ctrl->full[s], k, n0, policy);
                     tma_load_2d_hint(&tmW1, w + kWStage / 2, &ctrl->full[s], k, n0, policy);
                 } else {
@@ -222,7 +250,9 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
             };
             auto tokens = [&](int s, int kb) {
-                tma_load_2d(&tmX, sX + s * kXStage, &ctrl->full[s], (k0 + kb) * kK, t0);
+                const bool second = DX && k0 + kb >= p.kr;
+                tma_load_2d(second ? &tmX1 : &tmX, sX + s * kXStage, &ctrl->full[s], (k0 + kb - (second ? p.kr : 0)) * kK,
+                            t0);
             };
             const int head = min(nk, kStages);
             for (int kb = 0; kb < head; ++kb) {
@@ -256,8 +286,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         {   // the whole warp: one lane's instructions take effect
             const bool mine = lane == 0;
             const uint32_t fmt = FP8 ? 0u : p.fmt;
-            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)(NT >> 3) << 17) |
-                                   ((uint32_t)(kRows >> 4) << 24);
+            const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)MN << 15) |
+                                   ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
             bool ok = true;
             for (int kb = 0; kb < nk; ++kb) {
                 const int s = kb % kStages;
@@ -271,11 +301,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                     break;
                 }
                 tc_fence_after();
-                const uint64_t ad = smem_desc(sW + s * kWStage), bd = smem_desc(sX + s * kXStage);
+                const uint64_t ad = MN ? ffn::desc_mn(sW + s * kWStage) : smem_desc(sW + s * kWStage);
+                const uint64_t bd = smem_desc(sX + s * kXStage);
+                // a K slice of 32 bytes; of an MN-major operand, 16 rows of it
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk) {
-                    mma_if<1, FP8 ? kF8 : kF16>(mine, d, ad + 2 * kk, bd + 2 * kk, idesc, (FP8 ? kk : kb | kk) != 0);
-                }
+                for (int kk = 0; kk < 4; ++kk)
+                    mma_if<1, FP8 ? kF8 : kF16>(mine, d, ad + (MN ? 128 : 2) * kk, bd + 2 * kk, idesc,
+                                                (FP8 ? kk : kb | kk) != 0);
                 mma_commit_if(mine, &ctrl->empty[s]);
                 if (FP8) mma_commit_if(mine, &ctrl->tfull[kb & 1]);
             }
@@ -395,6 +427,26 @@ __global__ void __launch_bounds__(kThreads, 2)
                     p.pre[b] = u[e];
                     p.pre[b + p.N] = v[e];
                 }
+            if constexpr (DGATED) {
+                // u, v: the kept pre-activations; then u = du, v = dv
+                float r4[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int64_t b = (int64_t)(t0 + min(t + e, nt - 1)) * 2 * p.N + n;
+                    r4[e] = u[e];
+                    u[e] = p.pre[b];
+                    v[e] = p.pre[b + p.N];
+                }
+                grad4(p.act, r4, u, v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t + e < nt) {
+                        const int64_t b = (int64_t)(t0 + t + e) * 2 * p.N + n;
+                        store1(p.out, b, u[e], p.out_dtype);
+                        store1(p.out, b + p.N, v[e], p.out_dtype);
+                    }
+                continue;
+            }
             if (GATED) gate4(p.act, u, v);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -416,6 +468,16 @@ __global__ void __launch_bounds__(kThreads, 2)
                 store4(p.pre, b, u, MOE_F32);
                 store4(p.pre, b + p.N, v, MOE_F32);
             }
+            if constexpr (DGATED) {
+                const int64_t b = (int64_t)(t0 + t) * 2 * p.N + n;
+                const float4 pu = *reinterpret_cast<const float4 *>(p.pre + b);
+                const float4 pv = *reinterpret_cast<const float4 *>(p.pre + b + p.N);
+                float gu[4] = {pu.x, pu.y, pu.z, pu.w}, gv[4] = {pv.x, pv.y, pv.z, pv.w};
+                grad4(p.act, u, gu, gv);
+                store4(p.out, b, gu, p.out_dtype);
+                store4(p.out, b + p.N, gv, p.out_dtype);
+                continue;
+            }
             if (GATED) gate4(p.act, u, v);
             store4(p.out, o, u, p.out_dtype);
         }
@@ -425,12 +487,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // ------------------------------------------------------------------ host side
 
-// Rows of 128-byte K blocks (128-byte swizzle), box_rows of them a box.
-bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_t cols, uint32_t box_rows) {
+// A row-major matrix of row stride ld elements, boxes of 128 bytes of columns
+// (128-byte swizzle) by box_rows.
+bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_t cols, int64_t ld, uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
     cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-    cuuint64_t strides[1] = {(cuuint64_t)cols * esize};
+    cuuint64_t strides[1] = {(cuuint64_t)ld * esize};
     cuuint32_t box[2] = {(cuuint32_t)(128 / esize), box_rows};
     cuuint32_t estr[2] = {1, 1};
     return fn(m, esize == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
@@ -439,19 +502,27 @@ bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool FP8, bool GATED, int NT>
+template <Form F, int NT>
 cudaError_t launch_nt(const Product &g, cudaStream_t s) {
+    constexpr bool FP8 = F == Form::kFp8, GATED = F == Form::kGated, DX = F == Form::kDx, MN = DX || F == Form::kDGated;
     constexpr int kOutRows = GATED ? kRows / 2 : kRows;
     const int esize = FP8 ? 1 : 2;
-    CUtensorMap mX, mW0, mW1;
-    if (!make_rows(&mX, g.x, esize, g.T, g.K, NT) || !make_rows(&mW0, g.w0, esize, g.N, g.K, kOutRows))
-        return cudaErrorInvalidValue;
+    CUtensorMap mX, mX1, mW0, mW1;
+    // weights: [N, K], boxes of kOutRows rows; the backward pass's [K, N], of 64 k-rows
+    auto weight = [&](CUtensorMap *m, const void *w) {
+        return MN ? make_rows(m, w, esize, g.K, g.N, g.N, 64) : make_rows(m, w, esize, g.N, g.K, g.K, kOutRows);
+    };
+    const int64_t ldx = g.ldx ? g.ldx : g.K;
+    if (!make_rows(&mX, g.x, esize, g.T, g.K, ldx, NT) || !weight(&mW0, g.w0)) return cudaErrorInvalidValue;
+    mX1 = mX;
     mW1 = mW0;
-    if (GATED && !make_rows(&mW1, g.w1, esize, g.N, g.K, kOutRows)) return cudaErrorInvalidValue;
+    if (DX && !make_rows(&mX1, g.x1, esize, g.T, g.K, ldx, NT)) return cudaErrorInvalidValue;
+    if ((GATED || DX) && !weight(&mW1, g.w1)) return cudaErrorInvalidValue;
     Params p{};
     p.T = (int)g.T;
     p.N = g.N;
-    p.kb = (int)(((int64_t)g.K * esize + 127) / 128);
+    p.kr = (int)(((int64_t)g.K * esize + 127) / 128);
+    p.kb = DX ? 2 * p.kr : p.kr;
     p.mt = (g.N + kOutRows - 1) / kOutRows;
     p.sx = g.sx;
     p.sw = g.sw;
@@ -464,11 +535,12 @@ cudaError_t launch_nt(const Product &g, cudaStream_t s) {
     p.err = g.err;
     const int tiles = p.mt * (int)((g.T + NT - 1) / NT);
     // K ranges: as many as fill two CTAs on every SM, with four K blocks each at least
+    // (half as many, or half as many again: 5 to 20 % slower on the listed sizes of wants())
     p.S = 1;
     while (p.S < 8 && tiles * p.S * 2 <= 2 * num_sms() && p.kb >= 8 * p.S) p.S *= 2;
     const size_t smem = 1024 + (size_t)stages<NT>() * (kWStage + NT * 128) + recv_bytes<NT>() +
                         (FP8 ? 4 * 2 * NT * 4 : 0) + sizeof(Ctrl);
-    auto kern = skinny_kernel<FP8, GATED, NT>;
+    auto kern = skinny_kernel<F, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -485,22 +557,22 @@ cudaError_t launch_nt(const Product &g, cudaStream_t s) {
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = pdl_enabled() ? 2 : 1;
-    e = cudaLaunchKernelEx(&cfg, kern, mX, mW0, mW1, p);
+    e = cudaLaunchKernelEx(&cfg, kern, mX, mX1, mW0, mW1, p);
     note_launch();
     return e;
 }
 
-template <bool FP8, bool GATED>
+template <Form F>
 cudaError_t launch_form(const Product &g, cudaStream_t s) {
-    if (g.T <= 16) return launch_nt<FP8, GATED, 16>(g, s);
-    if (g.T <= 32) return launch_nt<FP8, GATED, 32>(g, s);
+    if (g.T <= 16) return launch_nt<F, 16>(g, s);
+    if (g.T <= 32) return launch_nt<F, 32>(g, s);
     // 8 bits: the 128 sums of a thread leave no registers for more tokens a tile
     // (14336 x 4096, T = 128: 66 us with 128, 32 with 64)
-    if constexpr (FP8) {
-        return launch_nt<true, GATED, 64>(g, s);
+    if constexpr (F == Form::kFp8) {
+        return launch_nt<F, 64>(g, s);
     } else {
-        if (g.T <= 64) return launch_nt<false, GATED, 64>(g, s);
-        return launch_nt<false, GATED, 128>(g, s);
+        if (g.T <= 64) return launch_nt<F, 64>(g, s);
+        return launch_nt<F, 128>(g, s);
     }
 }
 
@@ -515,20 +587,32 @@ cudaError_t launch_form(const Product &g, cudaStream_t s) {
 //          27/24 at T = 128
 //   8 bits 14336 x 4096: T = 64 20/33, 128 32/34, 256 62/35;  2048 x 2048: T = 512
 //          13/14, 768 18/14;  640 x 8192: T = 1024 31/39, 2048 56/39
+//   and of the whole backward pass with this kernel in the place of one product:
+//   DGATED 3672 x 384: T = 64 22/46, 2048 81/103;  2048 x 5632: T = 128 93/106, 512
+//          115/109;  208 x 2944 (short K): T = 32 61/64, 128 70/61
+//   DX     640 x 2048: T = 9 23/41, 1024 43/47, 2048 61/54;  4096 x 14336: T = 64
+//          154/234, 512 364/347;  3672 x 384 (short K): T = 64 51/46
 // The 256-row tiles need enough tiles for the pairs of SMs and a long enough K; this
 // kernel reads the weights again for every 128 (8 bits: 64) tokens.
 bool wants(Form form, int64_t T, int N, int K) {
     const int64_t tiles = (T + 255) / 256 * ((N + 255) / 256);
     switch (form) {
         case Form::kGated: return T <= 64 || 2 * tiles <= 8;
+        case Form::kDGated: return T <= 32 || (K >= 512 && (T <= 128 || tiles <= 24));
+        case Form::kDx: return tiles <= 16 && K >= 1024;
         case Form::kFp8: return T <= 128 || tiles <= 16;
         default: return T <= 64 || (tiles <= 24 && K >= 1024);
     }
 }
 
 cudaError_t launch(const Product &g, cudaStream_t s) {
-    if (g.fp8) return launch_form<true, false>(g, s);
-    return g.gated ? launch_form<false, true>(g, s) : launch_form<false, false>(g, s);
+    switch (g.form) {
+        case Form::kGated: return launch_form<Form::kGated>(g, s);
+        case Form::kFp8: return launch_form<Form::kFp8>(g, s);
+        case Form::kDx: return launch_form<Form::kDx>(g, s);
+        case Form::kDGated: return launch_form<Form::kDGated>(g, s);
+        default: return launch_form<Form::kStore>(g, s);
+    }
 }
 
 }  // namespace skinny
