@@ -54,6 +54,28 @@ Gemm product(const moe_ffn_config &c, int64_t M, int N, int64_t K, uint32_t *err
     return g;
 }
 
+// out[n, t] = sum over the tokens of w[., n] x[., t] (and out1 from w1), few tiles
+// over many tokens: the few-row kernel splits the tokens.
+cudaError_t weight_grad(const moe_ffn_config &c, const void *x, int cols, int64_t ldx, const void *w, const void *w1,
+                        int rows, int64_t ldw, void *out, void *out1, uint32_t *err, cudaStream_t s) {
+    skinny::Product p{};
+    p.form = skinny::Form::kWeight;
+    p.bf16 = c.dtype == MOE_BF16;
+    p.T = cols;
+    p.N = rows;
+    p.K = (int)c.T;
+    p.ldx = ldx;
+    p.ldw = ldw;
+    p.x = x;
+    p.w0 = w;
+    p.w1 = w1;
+    p.out = out;
+    p.out1 = out1;
+    p.out_dtype = c.dtype;
+    p.err = err;
+    return skinny::launch(p, s);
+}
+
 moe_status forward(const moe_ffn_config *c, bool train, const void *x, const void *wg, const void *wu, const void *wd,
                    void *y, void *ws, size_t ws_bytes, void *stream) {
     const moe_status st = check(c);
@@ -197,7 +219,7 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
         e = launch_dgated(g, s);
     }
     // the rest in one launch: dx, then the weights' gradients (all over the T
-    // tokens); dx of few tokens by itself
+    // tokens); dx of few tokens, and gradients of few tiles, by themselves
     Gemm g[3];
     int n = 0;
     if (e == cudaSuccess && dx && skinny::wants(skinny::Form::kDx, T, c->d, c->h)) {
@@ -222,21 +244,33 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
         g[n++].c0 = {dx, T, d, d};
     }
     if (gates) {
-        g[n] = product(*c, h, c->d, T, err);
-        g[n].a_mn = true;
-        g[n].halves = dw_gate && dw_up ? 2 : 1;
-        g[n].a0 = dw_gate ? du : dv;
-        g[n].a1 = dv;
-        g[n].b0 = {x, T, d, d};
-        g[n].c0 = {dw_gate ? dw_gate : dw_up, h, d, d};
-        g[n++].c1 = {dw_up, h, d, d};
+        const Matrix &a0 = dw_gate ? du : dv;
+        void *c0 = dw_gate ? dw_gate : dw_up;
+        const bool both = dw_gate && dw_up;
+        if (e == cudaSuccess && skinny::wants(skinny::Form::kWeight, c->d, (both ? 2 : 1) * c->h, (int)T)) {
+            e = weight_grad(*c, x, c->d, d, a0.base, both ? dv.base : nullptr, c->h, 2 * h, c0, both ? dw_up : nullptr,
+                            err, s);
+        } else {
+            g[n] = product(*c, h, c->d, T, err);
+            g[n].a_mn = true;
+            g[n].halves = both ? 2 : 1;
+            g[n].a0 = a0;
+            g[n].a1 = dv;
+            g[n].b0 = {x, T, d, d};
+            g[n].c0 = {c0, h, d, d};
+            g[n++].c1 = {dw_up, h, d, d};
+        }
     }
     if (dw_down) {
-        g[n] = product(*c, d, c->h, T, err);
-        g[n].a_mn = true;
-        g[n].a0 = {dy, T, d, d};
-        g[n].b0 = {act, T, h, h};
-        g[n++].c0 = {dw_down, d, h, h};
+        if (e == cudaSuccess && skinny::wants(skinny::Form::kWeight, c->h, c->d, (int)T)) {
+            e = weight_grad(*c, act, c->h, h, dy, nullptr, c->d, d, dw_down, nullptr, err, s);
+        } else {
+            g[n] = product(*c, d, c->h, T, err);
+            g[n].a_mn = true;
+            g[n].a0 = {dy, T, d, d};
+            g[n].b0 = {act, T, h, h};
+            g[n++].c0 = {dw_down, d, h, h};
+        }
     }
     if (e == cudaSuccess && n) e = launch_grads(g, n, s);
     return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;

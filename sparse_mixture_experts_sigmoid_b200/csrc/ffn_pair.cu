@@ -385,8 +385,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 4; ++q) tmem_ld16(at + 16 * q, *reinterpret_cast<float(*)[16]>(&f[16 * q]));
             tmem_wait_ld();
         };
+        // DGATED: this warp's u and v of a pair's k-th tile into L2, a tile ahead (from
+        // HBM they would be waited for 16 columns at a time)
+        [[maybe_unused]] auto fetch = [&](int k) {
+            Tile t;
+            if (!tile_at(k, pair, npairs, p, t)) return;
+            const Job &j = p.job[0];
+            const int r = t.m * kBM + (int)rank * 128 + (warp & 3) * 32 + lane, c0 = t.n * kCols + cw;
+            if (r >= j.M) return;
+            const float *at = p.pre + (int64_t)r * 2 * j.N + c0;
+#pragma unroll
+            for (int c = 0; c < kWarpCols; c += 32) {
+                if (c0 + c >= j.N) break;
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c));
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + j.N + c));
+            }
+        };
+        if constexpr (EPI == DGATED) fetch(0);
         Tile t;
         for (int tc = 0; tile_at(tc, pair, npairs, p, t); ++tc) {
+            if constexpr (EPI == DGATED) fetch(tc + 1);
             const Job &j = p.job[t.job];
             const JobMaps &jm = maps.job[FORM == GRADS ? t.job : 0];
             const uint32_t acc = tc & 1;

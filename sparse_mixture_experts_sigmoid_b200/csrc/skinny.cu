@@ -4,6 +4,8 @@
 //   GATED : out[t, n] = act(u) v,  u = x w0^T, v = x w1^T  (u, v kept for training)
 //   DX    : out[t, n] = sum_k x0[t, k] w0[k, n] + x1[t, k] w1[k, n]
 //   DGATED: r = x w (w [K, N]);  du = r v act'(u), dv = r act(u) from the kept u, v
+//   WEIGHT: out[n, t] = sum_k w[k, n] x[k, t], a weight's gradient (w and x hold one
+//           row per token k) that has few tiles and many tokens
 //
 // for bf16 / fp16 operands, and (FP8, as STORE) e4m3 operands with a scale per row
 // and 128 columns of x and per 128 x 128 block of w.  The backward pass's weights
@@ -69,7 +71,8 @@ struct Ctrl {
 struct Params {
     int T, N, kb;         // kb: K blocks of 128 bytes
     int kr;               // DX: those of the first of the two K ranges
-    int S, mt;            // cluster size; weight tiles
+    int S, mt;            // cluster size; weight tiles (of one half)
+    void *out1;           // WEIGHT: the second half's output (from the second weights), or null
     const float *sx, *sw;
     void *out;
     int out_dtype;
@@ -175,7 +178,9 @@ __global__ void __launch_bounds__(kThreads, 2)
     skinny_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmX1,
                   const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1, Params p) {
     constexpr bool FP8 = F == Form::kFp8, GATED = F == Form::kGated, DX = F == Form::kDx, DGATED = F == Form::kDGated;
-    constexpr bool MN = DX || DGATED;                      // the weights' rows are the reduction
+    constexpr bool WEIGHT = F == Form::kWeight;
+    constexpr bool MN = DX || DGATED || WEIGHT;            // the weights' rows are the reduction
+    static_assert(!WEIGHT || NT == 64, "one atom of x");
     constexpr int kStages = stages<NT>();
     constexpr int kXStage = NT * 128;
     constexpr int kBuf = NT < 32 ? 32 : NT;                // TMEM columns of one accumulator
@@ -225,7 +230,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (kPush<NT> && p.S > 1) cluster_started();
     const uint32_t tmem = ctrl->tmem_base;
     const int S = p.S, rank = S > 1 ? (int)cluster_rank() : 0;
-    const int tile = blockIdx.x / S, tt = tile / p.mt, m = tile - tt * p.mt;
+    int tile = blockIdx.x / S;
+    const int half_tiles = p.mt * ((p.T + NT - 1) / NT);
+    const bool half = WEIGHT && tile >= half_tiles;   // WEIGHT: of the second weights
+    if (half) tile -= half_tiles;
+    const int tt = tile / p.mt, m = tile - tt * p.mt;
     const int t0 = tt * NT, n0 = m * kOutRows, nt = min(NT, p.T - t0);
     const int per = kOutRows / S, width = kRows / S;   // output rows, and sums' rows, of this CTA
     const int k0 = (int)((int64_t)p.kb * rank / S), k1 = (int)((int64_t)p.kb * (rank + 1) / S), nk = k1 - k0;
@@ -239,7 +248,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 const bool second = DX && k0 + kb >= p.kr;
                 const int k = (k0 + kb - (second ? p.kr : 0)) * kK;
                 if constexpr (MN) {
-                    const CUtensorMap *m = second ? &tmW1 : &tmW0;
+                    const CUtensorMap *m = second || half ? &tmW1 : &tmW0;
                     tma_load_2d_hint(m, w, &ctrl->full[s], n0, k, policy);
                     tma_load_2d_hint(m, w + kWStage / 2, &ctrl->full[s], n0 + 64, k, policy);
                 } else if constexpr (GATED) {
@@ -251,8 +260,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             };
             auto tokens = [&](int s, int kb) {
                 const bool second = DX && k0 + kb >= p.kr;
-                tma_load_2d(second ? &tmX1 : &tmX, sX + s * kXStage, &ctrl->full[s], (k0 + kb - (second ? p.kr : 0)) * kK,
-                            t0);
+                const int k = (k0 + kb - (second ? p.kr : 0)) * kK;
+                if constexpr (WEIGHT) tma_load_2d(&tmX, sX + s * kXStage, &ctrl->full[s], t0, k);
+                else tma_load_2d(second ? &tmX1 : &tmX, sX + s * kXStage, &ctrl->full[s], k, t0);
             };
             const int head = min(nk, kStages);
             for (int kb = 0; kb < head; ++kb) {
@@ -287,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             const bool mine = lane == 0;
             const uint32_t fmt = FP8 ? 0u : p.fmt;
             const uint32_t idesc = (1u << 4) | (fmt << 7) | (fmt << 10) | ((uint32_t)MN << 15) |
-                                   ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
+                                   ((uint32_t)WEIGHT << 16) | ((uint32_t)(NT >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
             bool ok = true;
             for (int kb = 0; kb < nk; ++kb) {
                 const int s = kb % kStages;
@@ -302,11 +312,11 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 tc_fence_after();
                 const uint64_t ad = MN ? ffn::desc_mn(sW + s * kWStage) : smem_desc(sW + s * kWStage);
-                const uint64_t bd = smem_desc(sX + s * kXStage);
+                const uint64_t bd = WEIGHT ? ffn::desc_mn(sX + s * kXStage) : smem_desc(sX + s * kXStage);
                 // a K slice of 32 bytes; of an MN-major operand, 16 rows of it
 #pragma unroll
                 for (int kk = 0; kk < 4; ++kk)
-                    mma_if<1, FP8 ? kF8 : kF16>(mine, d, ad + (MN ? 128 : 2) * kk, bd + 2 * kk, idesc,
+                    mma_if<1, FP8 ? kF8 : kF16>(mine, d, ad + (MN ? 128 : 2) * kk, bd + (WEIGHT ? 128 : 2) * kk, idesc,
                                                 (FP8 ? kk : kb | kk) != 0);
                 mma_commit_if(mine, &ctrl->empty[s]);
                 if (FP8) mma_commit_if(mine, &ctrl->tfull[kb & 1]);
@@ -411,7 +421,18 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kTmaWarp) pdl_wait();   // (its other lanes) before anything is written
 
     // 1 / S of the tile's rows, over the S ranges in their order
-    if constexpr (kPush<NT>) {
+    if constexpr (WEIGHT) {
+        // four columns of a row a step (T is a multiple of 8: in or out together)
+        const int quads = nt / 4;
+        void *out = half ? p.out1 : p.out;
+        for (int i = threadIdx.x; i < per * quads; i += kThreads) {
+            const int r = i / quads, t = 4 * (i - r * quads), n = n0 + rank * per + r;
+            if (n >= p.N) continue;
+            float u[4];
+            add_ranges<false>(recv + t * width + 4 * r, S, NT * width, u);
+            store4(out, (int64_t)n * p.T + t0 + t, u, p.out_dtype);
+        }
+    } else if constexpr (kPush<NT>) {
         // one row of four tokens a step
         for (int i = threadIdx.x; i < per * ((nt + 3) / 4); i += kThreads) {
             const int t = i / per * 4, r = i - (i / per) * per, n = n0 + rank * per + r;
@@ -504,20 +525,22 @@ bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_
 
 template <Form F, int NT>
 cudaError_t launch_nt(const Product &g, cudaStream_t s) {
-    constexpr bool FP8 = F == Form::kFp8, GATED = F == Form::kGated, DX = F == Form::kDx, MN = DX || F == Form::kDGated;
+    constexpr bool FP8 = F == Form::kFp8, GATED = F == Form::kGated, DX = F == Form::kDx;
+    constexpr bool WEIGHT = F == Form::kWeight, MN = DX || F == Form::kDGated || WEIGHT;
     constexpr int kOutRows = GATED ? kRows / 2 : kRows;
     const int esize = FP8 ? 1 : 2;
     CUtensorMap mX, mX1, mW0, mW1;
     // weights: [N, K], boxes of kOutRows rows; the backward pass's [K, N], of 64 k-rows
     auto weight = [&](CUtensorMap *m, const void *w) {
-        return MN ? make_rows(m, w, esize, g.K, g.N, g.N, 64) : make_rows(m, w, esize, g.N, g.K, g.K, kOutRows);
+        return MN ? make_rows(m, w, esize, g.K, g.N, g.ldw ? g.ldw : g.N, 64) : make_rows(m, w, esize, g.N, g.K, g.K, kOutRows);
     };
-    const int64_t ldx = g.ldx ? g.ldx : g.K;
-    if (!make_rows(&mX, g.x, esize, g.T, g.K, ldx, NT) || !weight(&mW0, g.w0)) return cudaErrorInvalidValue;
+    const int64_t ldx = g.ldx ? g.ldx : (WEIGHT ? g.T : g.K);
+    const bool x_ok = WEIGHT ? make_rows(&mX, g.x, esize, g.K, g.T, ldx, 64) : make_rows(&mX, g.x, esize, g.T, g.K, ldx, NT);
+    if (!x_ok || !weight(&mW0, g.w0)) return cudaErrorInvalidValue;
     mX1 = mX;
     mW1 = mW0;
     if (DX && !make_rows(&mX1, g.x1, esize, g.T, g.K, ldx, NT)) return cudaErrorInvalidValue;
-    if ((GATED || DX) && !weight(&mW1, g.w1)) return cudaErrorInvalidValue;
+    if ((GATED || DX || (WEIGHT && g.w1)) && !weight(&mW1, g.w1)) return cudaErrorInvalidValue;
     Params p{};
     p.T = (int)g.T;
     p.N = g.N;
@@ -527,13 +550,14 @@ cudaError_t launch_nt(const Product &g, cudaStream_t s) {
     p.sx = g.sx;
     p.sw = g.sw;
     p.out = g.out;
+    p.out1 = g.out1;
     p.out_dtype = g.out_dtype;
     p.pre = g.pre;
     p.act = g.act;
     p.fmt = g.bf16 ? 1u : 0u;
     p.early = g.early;
     p.err = g.err;
-    const int tiles = p.mt * (int)((g.T + NT - 1) / NT);
+    const int tiles = p.mt * (int)((g.T + NT - 1) / NT) * (WEIGHT && g.w1 ? 2 : 1);
     // K ranges: as many as fill two CTAs on every SM, with four K blocks each at least
     // (half as many, or half as many again: 5 to 20 % slower on the listed sizes of wants())
     p.S = 1;
@@ -592,6 +616,8 @@ cudaError_t launch_form(const Product &g, cudaStream_t s) {
 //          115/109;  208 x 2944 (short K): T = 32 61/64, 128 70/61
 //   DX     640 x 2048: T = 9 23/41, 1024 43/47, 2048 61/54;  4096 x 14336: T = 64
 //          154/234, 512 364/347;  3672 x 384 (short K): T = 64 51/46
+//   WEIGHT 80 x 168: T = 1024 30/25, 8192 40/69;  512 x 512: T = 2048 44/38, 8192
+//          65/84;  640 x 2048 (more tiles): T = 8192 299/189
 // The 256-row tiles need enough tiles for the pairs of SMs and a long enough K; this
 // kernel reads the weights again for every 128 (8 bits: 64) tokens.
 bool wants(Form form, int64_t T, int N, int K) {
@@ -600,6 +626,7 @@ bool wants(Form form, int64_t T, int N, int K) {
         case Form::kGated: return T <= 64 || 2 * tiles <= 8;
         case Form::kDGated: return T <= 32 || (K >= 512 && (T <= 128 || tiles <= 24));
         case Form::kDx: return tiles <= 16 && K >= 1024;
+        case Form::kWeight: return tiles <= 8 && K >= 4096;
         case Form::kFp8: return T <= 128 || tiles <= 16;
         default: return T <= 64 || (tiles <= 24 && K >= 1024);
     }
@@ -611,6 +638,7 @@ cudaError_t launch(const Product &g, cudaStream_t s) {
         case Form::kFp8: return launch_form<Form::kFp8>(g, s);
         case Form::kDx: return launch_form<Form::kDx>(g, s);
         case Form::kDGated: return launch_form<Form::kDGated>(g, s);
+        case Form::kWeight: return launch_nt<Form::kWeight, 64>(g, s);
         default: return launch_form<Form::kStore>(g, s);
     }
 }

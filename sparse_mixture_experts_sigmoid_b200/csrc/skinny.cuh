@@ -12,16 +12,18 @@ namespace skinny {
 //            KB = ceil(K / 128)
 //   kDx    : out[t, n] = sum_k x[t, k] w0[k, n] + x1[t, k] w1[k, n]
 //   kDGated: r[t, n] = sum_k x[t, k] w0[k, n]; out [T, 2N]: du | dv from r and pre
-enum class Form { kStore, kGated, kFp8, kDx, kDGated };
+//   kWeight: out[n, t] = sum_k w0[k, n] x[k, t] over K tokens; w1, out1: a second such
+//            product with the same x, or null
+enum class Form { kStore, kGated, kFp8, kDx, kDGated, kWeight };
 struct Product {
     Form form;
     bool bf16;                 // 16-bit operands are bf16, else fp16
     int64_t T;
     int N, K;
-    int64_t ldx;               // row stride of x (and x1); 0: K
+    int64_t ldx, ldw;          // row strides of x (and x1), and of kWeight's w; 0: their columns
     const void *x, *x1, *w0, *w1;
     const float *sx, *sw;
-    void *out;                 // [T, N]
+    void *out, *out1;          // [T, N]; kWeight: [N, T]
     int out_dtype;
     float *pre;                // [T, 2N] u | v; kGated: optional
     int act;                   // moe_ffn_act

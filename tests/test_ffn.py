@@ -167,6 +167,8 @@ CASES = [
     (256, 256, 256, "silu", "f16"), (300, 512, 384, "silu", "bf16"), (513, 576, 648, "gelu_tanh", "f16"),
     (1000, 1000, 2728, "silu", "bf16"), (2049, 264, 136, "silu", "f16"), (5000, 96, 200, "gelu_tanh", "bf16"),
     (600, 2048, 1408, "silu", "bf16"), (1, 4096, 1032, "silu", "bf16"), (9, 1032, 4096, "gelu_tanh", "f16"),
+    # few columns under many tokens: the weights' gradients split over the tokens
+    (4099, 64, 80, "silu", "bf16"), (4096, 136, 72, "gelu_tanh", "f16"), (5000, 520, 328, "silu", "bf16"), (8191, 8, 1000, "silu", "f16"),
 ]
 
 
