@@ -184,14 +184,14 @@ def _ptr(t: torch.Tensor | None, name: str, shape=None, dtype=None, dev=None):
 
 def _here(t: torch.Tensor):
     """The current device, for _ptr to hold the tensors of a call to (a host tensor is refused there)."""
-    return torch.cuda.current_device() if t.is_cuda else None
+    return torch._C._cuda_getDevice() if t.is_cuda else None
 
 
-def _stream(stream=None):
+def _stream(stream=None, dev=None):
     if stream is not None:
         return stream.cuda_stream
     # torch.cuda.current_stream().cuda_stream without the Stream object (3 us of a small call's 17)
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev is None else dev)
 
 
 def validate(cfg: MoEConfig) -> int:
@@ -645,19 +645,29 @@ def norm_workspace_size(cfg: NormConfig) -> int:
 def norm_forward(cfg: NormConfig, x, weight, bias=None, residual=None, y=None, h=None, want_stats=False, stream=None):
     """moe_norm_forward: (y[T,d], h[T,d] | None, mean[T] | None, rstd[T] | None).  h = x + residual with a
     residual (allocated unless given); mean (layer norm) and rstd with want_stats."""
-    dt, wt = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype]
-    rows, dev = (cfg.T, cfg.d), _here(x)
+    dt, wt, T, d = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype], cfg.T, cfg.d
+    rows, cols, dev = (T, d), (d,), _here(x)
     px = _ptr(x, "x", rows, dt, dev)
     if y is None:
         y = torch.empty_like(x)
+        py = y.data_ptr()
+    else:
+        py = _ptr(y, "y", rows, dt, dev)
     if h is None and residual is not None:
         h = torch.empty_like(x)
-    mean = x.new_empty(cfg.T, dtype=torch.float32) if want_stats and cfg.kind == 0 else None
-    rstd = None if not want_stats else x.new_empty(cfg.T, dtype=torch.float32) if mean is None else torch.empty_like(mean)
+        ph = h.data_ptr()
+    else:
+        ph = _ptr(h, "h", rows, dt, dev)
+    mean = rstd = pm = pr = None
+    if want_stats:
+        rstd = x.new_empty(T, dtype=torch.float32)
+        pr = rstd.data_ptr()
+        if cfg.kind == 0:
+            mean = torch.empty_like(rstd)
+            pm = mean.data_ptr()
     _check(lib().moe_norm_forward(ctypes.byref(cfg), px, _ptr(residual, "residual", rows, dt, dev),
-                                  _ptr(weight, "weight", (cfg.d,), wt, dev), _ptr(bias, "bias", (cfg.d,), wt, dev),
-                                  _ptr(h, "h", rows, dt, dev), _ptr(y, "y", rows, dt, dev), None if mean is None else mean.data_ptr(),
-                                  None if rstd is None else rstd.data_ptr(), _stream(stream)), "moe_norm_forward")
+                                  _ptr(weight, "weight", cols, wt, dev), _ptr(bias, "bias", cols, wt, dev), ph, py, pm,
+                                  pr, _stream(stream, dev)), "moe_norm_forward")
     return y, h, mean, rstd
 
 
@@ -666,22 +676,32 @@ def norm_backward(cfg: NormConfig, h, weight, mean, rstd, dy, dh=None, dx=None, 
     """moe_norm_backward: (dx[T,d], dweight[d] float32 | None, dbias[d] float32 | None).  h: the rows that were
     normalised; mean (None for an RMS norm) and rstd from norm_forward; dh: the gradient that reaches h by other
     paths, added to dx."""
-    dt, wt = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype]
-    rows, dev = (cfg.T, cfg.d), _here(h)
-    ph = _ptr(h, "h", rows, dt, dev)
+    dt, wt, T, d, f32 = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype], cfg.T, cfg.d, torch.float32
+    rows, cols, dev = (T, d), (d,), _here(h)
+    ph, pw = _ptr(h, "h", rows, dt, dev), _ptr(weight, "weight", cols, wt, dev)
     if dx is None:
         dx = torch.empty_like(h)
-    dweight = torch.empty_like(weight, dtype=torch.float32) if want_weight else None
-    dbias = torch.empty_like(weight, dtype=torch.float32) if want_bias else None
-    if ws is None and (want_weight or want_bias):
-        ws = h.new_empty(max(norm_workspace_size(cfg), 1), dtype=torch.uint8)
-    f32 = torch.float32
-    _check(lib().moe_norm_backward(ctypes.byref(cfg), ph, _ptr(weight, "weight", (cfg.d,), wt, dev),
-                                   _ptr(mean, "mean", (cfg.T,), f32, dev), _ptr(rstd, "rstd", (cfg.T,), f32, dev),
-                                   _ptr(dy, "dy", rows, dt, dev), _ptr(dh, "dh", rows, dt, dev),
-                                   _ptr(dx, "dx", rows, dt, dev), None if dweight is None else dweight.data_ptr(),
-                                   None if dbias is None else dbias.data_ptr(), _ptr(ws, "ws", None, torch.uint8, dev),
-                                   0 if ws is None else ws.numel(), _stream(stream)), "moe_norm_backward")
+        pdx = dx.data_ptr()
+    else:
+        pdx = _ptr(dx, "dx", rows, dt, dev)
+    dweight = dbias = pdw = pdb = pws = None
+    n = 0
+    if want_weight:
+        dweight = torch.empty_like(weight, dtype=f32)
+        pdw = dweight.data_ptr()
+    if want_bias:
+        dbias = torch.empty_like(weight, dtype=f32)
+        pdb = dbias.data_ptr()
+    if ws is not None:
+        pws, n = _ptr(ws, "ws", None, torch.uint8, dev), ws.numel()
+    elif want_weight or want_bias:
+        n = norm_workspace_size(cfg)
+        ws = h.new_empty(n, dtype=torch.uint8)
+        pws = ws.data_ptr()
+    _check(lib().moe_norm_backward(ctypes.byref(cfg), ph, pw, _ptr(mean, "mean", (T,), f32, dev),
+                                   _ptr(rstd, "rstd", (T,), f32, dev), _ptr(dy, "dy", rows, dt, dev),
+                                   _ptr(dh, "dh", rows, dt, dev), pdx, pdw, pdb, pws, n, _stream(stream, dev)),
+           "moe_norm_backward")
     return dx, dweight, dbias
 
 
@@ -712,12 +732,14 @@ def _ffn_forward(name, cfg, x, w_gate, w_up, w_down, y, ws, stream):
     px = _ptr(x, "x", (T, d), dt, dev)
     if y is None:
         y = torch.empty_like(x)
+        py = y.data_ptr()
+    else:
+        py = _ptr(y, "y", (T, d), dt, dev)
     if ws is None:
         ws = alloc_ffn_workspace(cfg, device=x.device)
     _check(getattr(lib(), name)(ctypes.byref(cfg), px, _ptr(w_gate, "w_gate", (h, d), dt, dev),
-                                _ptr(w_up, "w_up", (h, d), dt, dev), _ptr(w_down, "w_down", (d, h), dt, dev),
-                                _ptr(y, "y", (T, d), dt, dev), _ptr(ws, "ws", dtype=torch.uint8, dev=dev), ws.numel(),
-                                _stream(stream)), name)
+                                _ptr(w_up, "w_up", (h, d), dt, dev), _ptr(w_down, "w_down", (d, h), dt, dev), py,
+                                _ptr(ws, "ws", None, torch.uint8, dev), ws.numel(), _stream(stream, dev)), name)
     return y
 
 
@@ -742,12 +764,12 @@ def ffn_backward(cfg: FfnConfig, x, w_gate, w_up, w_down, dy, ws, grads=None, st
     if grads is None:
         grads = {"dx": torch.empty_like(x), "dw_gate": torch.empty_like(w_gate), "dw_up": torch.empty_like(w_up),
                  "dw_down": torch.empty_like(w_down)}
-    _check(lib().moe_ffn_backward(ctypes.byref(cfg), px, pg, pu, pd, pdy, _ptr(ws, "ws", dtype=torch.uint8, dev=dev),
-                                  ws.numel(), _ptr(grads.get("dx"), "dx", rows, dt, dev),
-                                  _ptr(grads.get("dw_gate"), "dw_gate", up, dt, dev),
-                                  _ptr(grads.get("dw_up"), "dw_up", up, dt, dev),
-                                  _ptr(grads.get("dw_down"), "dw_down", down, dt, dev), _stream(stream)),
-           "moe_ffn_backward")
+        out = [g.data_ptr() for g in grads.values()]
+    else:
+        out = [_ptr(grads.get(n), n, s, dt, dev) for n, s in (("dx", rows), ("dw_gate", up), ("dw_up", up),
+                                                               ("dw_down", down))]
+    _check(lib().moe_ffn_backward(ctypes.byref(cfg), px, pg, pu, pd, pdy, _ptr(ws, "ws", None, torch.uint8, dev),
+                                  ws.numel(), *out, _stream(stream, dev)), "moe_ffn_backward")
     return grads
 
 
@@ -769,11 +791,12 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, stream=None):
         raise ValueError(f"x must have two dimensions, got {x.dim()}")
     if block_rows not in (1, 128):
         raise ValueError(f"block_rows must be 1 or 128, got {block_rows}")
-    code, px = _dtype_code(x, "x"), _ptr(x, "x", dev=_here(x))
+    dev = _here(x)
+    code, px = _dtype_code(x, "x"), _ptr(x, "x", None, x.dtype, dev)
     rows, cols = x.shape
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     sc = x.new_empty((-(-rows // block_rows), -(-cols // 128)), dtype=torch.float32)
-    _check(lib().moe_quantize_fp8(px, code, rows, cols, block_rows, q.data_ptr(), sc.data_ptr(), _stream(stream)),
+    _check(lib().moe_quantize_fp8(px, code, rows, cols, block_rows, q.data_ptr(), sc.data_ptr(), _stream(stream, dev)),
            "moe_quantize_fp8")
     return q, sc
 
@@ -784,11 +807,14 @@ def gemm_fp8(a, a_scales, b, b_scales, out_dtype="bf16", out=None, stream=None):
         raise ValueError("a and b must have two dimensions")
     (M, K), N = a.shape, b.shape[0]
     kb, f8, f32 = -(-K // 128), torch.float8_e4m3fn, torch.float32
+    dev, code = _here(a), _choice(DTYPES, out_dtype, "out_dtype")
+    pa = _ptr(a, "a", (M, K), f8, dev)
     if out is None:
-        out = a.new_empty((M, N), dtype=_TORCH_DTYPES[_choice(DTYPES, out_dtype, "out_dtype")])
-    dev = _here(a)
-    _check(lib().moe_gemm_fp8(M, N, K, _ptr(a, "a", (M, K), f8, dev), _ptr(a_scales, "a_scales", (M, kb), f32, dev),
-                              _ptr(b, "b", (N, K), f8, dev), _ptr(b_scales, "b_scales", (-(-N // 128), kb), f32, dev),
-                              _ptr(out, "out", (M, N), None, dev), _dtype_code(out, "out"), _stream(stream)),
-           "moe_gemm_fp8")
+        out = a.new_empty((M, N), dtype=_TORCH_DTYPES[code])
+        po = out.data_ptr()
+    else:
+        code, po = _dtype_code(out, "out"), _ptr(out, "out", (M, N), out.dtype, dev)
+    _check(lib().moe_gemm_fp8(M, N, K, pa, _ptr(a_scales, "a_scales", (M, kb), f32, dev), _ptr(b, "b", (N, K), f8, dev),
+                              _ptr(b_scales, "b_scales", (-(-N // 128), kb), f32, dev), po, code,
+                              _stream(stream, dev)), "moe_gemm_fp8")
     return out
