@@ -617,6 +617,10 @@ def profile_nvtx(on: bool = True) -> None:
 
 
 # ----------------------------------------------------------------------------- norms
+#
+# The functions from here on run a call that is given a stream with that stream as the current one: what they
+# allocate, a workspace that they drop again among it, belongs to that stream.  The caller orders the stream against
+# those that write the inputs or read the outputs.
 
 DTYPES = {"bf16": 0, "f32": 1, "f16": 2}
 _TORCH_DTYPES = {0: torch.bfloat16, 1: torch.float32, 2: torch.float16}
@@ -645,6 +649,9 @@ def norm_workspace_size(cfg: NormConfig) -> int:
 def norm_forward(cfg: NormConfig, x, weight, bias=None, residual=None, y=None, h=None, want_stats=False, stream=None):
     """moe_norm_forward: (y[T,d], h[T,d] | None, mean[T] | None, rstd[T] | None).  h = x + residual with a
     residual (allocated unless given); mean (layer norm) and rstd with want_stats."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_forward(cfg, x, weight, bias, residual, y, h, want_stats)
     dt, wt, T, d = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype], cfg.T, cfg.d
     rows, cols, dev = (T, d), (d,), _here(x)
     px = _ptr(x, "x", rows, dt, dev)
@@ -667,7 +674,7 @@ def norm_forward(cfg: NormConfig, x, weight, bias=None, residual=None, y=None, h
             pm = mean.data_ptr()
     _check(lib().moe_norm_forward(ctypes.byref(cfg), px, _ptr(residual, "residual", rows, dt, dev),
                                   _ptr(weight, "weight", cols, wt, dev), _ptr(bias, "bias", cols, wt, dev), ph, py, pm,
-                                  pr, _stream(stream, dev)), "moe_norm_forward")
+                                  pr, _stream(dev=dev)), "moe_norm_forward")
     return y, h, mean, rstd
 
 
@@ -676,6 +683,9 @@ def norm_backward(cfg: NormConfig, h, weight, mean, rstd, dy, dh=None, dx=None, 
     """moe_norm_backward: (dx[T,d], dweight[d] float32 | None, dbias[d] float32 | None).  h: the rows that were
     normalised; mean (None for an RMS norm) and rstd from norm_forward; dh: the gradient that reaches h by other
     paths, added to dx."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return norm_backward(cfg, h, weight, mean, rstd, dy, dh, dx, want_weight, want_bias, ws)
     dt, wt, T, d, f32 = _TORCH_DTYPES[cfg.dtype], _TORCH_DTYPES[cfg.w_dtype], cfg.T, cfg.d, torch.float32
     rows, cols, dev = (T, d), (d,), _here(h)
     ph, pw = _ptr(h, "h", rows, dt, dev), _ptr(weight, "weight", cols, wt, dev)
@@ -700,7 +710,7 @@ def norm_backward(cfg: NormConfig, h, weight, mean, rstd, dy, dh=None, dx=None, 
         pws = ws.data_ptr()
     _check(lib().moe_norm_backward(ctypes.byref(cfg), ph, pw, _ptr(mean, "mean", (T,), f32, dev),
                                    _ptr(rstd, "rstd", (T,), f32, dev), _ptr(dy, "dy", rows, dt, dev),
-                                   _ptr(dh, "dh", rows, dt, dev), pdx, pdw, pdb, pws, n, _stream(stream, dev)),
+                                   _ptr(dh, "dh", rows, dt, dev), pdx, pdw, pdb, pws, n, _stream(dev=dev)),
            "moe_norm_backward")
     return dx, dweight, dbias
 
@@ -727,6 +737,9 @@ def alloc_ffn_workspace(cfg: FfnConfig, train: bool = False, device=None) -> tor
 
 
 def _ffn_forward(name, cfg, x, w_gate, w_up, w_down, y, ws, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _ffn_forward(name, cfg, x, w_gate, w_up, w_down, y, ws, None)
     dt, T, d, h = _TORCH_DTYPES[cfg.dtype], cfg.T, cfg.d, cfg.h
     dev = _here(x)
     px = _ptr(x, "x", (T, d), dt, dev)
@@ -739,7 +752,7 @@ def _ffn_forward(name, cfg, x, w_gate, w_up, w_down, y, ws, stream):
         ws = alloc_ffn_workspace(cfg, device=x.device)
     _check(getattr(lib(), name)(ctypes.byref(cfg), px, _ptr(w_gate, "w_gate", (h, d), dt, dev),
                                 _ptr(w_up, "w_up", (h, d), dt, dev), _ptr(w_down, "w_down", (d, h), dt, dev), py,
-                                _ptr(ws, "ws", None, torch.uint8, dev), ws.numel(), _stream(stream, dev)), name)
+                                _ptr(ws, "ws", None, torch.uint8, dev), ws.numel(), _stream(dev=dev)), name)
     return y
 
 
@@ -756,6 +769,9 @@ def ffn_forward_train(cfg: FfnConfig, x, w_gate, w_up, w_down, ws, y=None, strea
 def ffn_backward(cfg: FfnConfig, x, w_gate, w_up, w_down, dy, ws, grads=None, stream=None) -> dict:
     """moe_ffn_backward after ffn_forward_train(cfg, x, ..., ws): the gradients dx, dw_gate, dw_up and dw_down, all
     allocated, or those that ``grads`` holds (one that is absent or None there is not computed)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return ffn_backward(cfg, x, w_gate, w_up, w_down, dy, ws, grads)
     dt, T, d, h = _TORCH_DTYPES[cfg.dtype], cfg.T, cfg.d, cfg.h
     dev, rows, up, down = _here(x), (T, d), (h, d), (d, h)
     px, pdy = _ptr(x, "x", rows, dt, dev), _ptr(dy, "dy", rows, dt, dev)
@@ -769,7 +785,7 @@ def ffn_backward(cfg: FfnConfig, x, w_gate, w_up, w_down, dy, ws, grads=None, st
         out = [_ptr(grads.get(n), n, s, dt, dev) for n, s in (("dx", rows), ("dw_gate", up), ("dw_up", up),
                                                                ("dw_down", down))]
     _check(lib().moe_ffn_backward(ctypes.byref(cfg), px, pg, pu, pd, pdy, _ptr(ws, "ws", None, torch.uint8, dev),
-                                  ws.numel(), *out, _stream(stream, dev)), "moe_ffn_backward")
+                                  ws.numel(), *out, _stream(dev=dev)), "moe_ffn_backward")
     return grads
 
 
@@ -787,6 +803,9 @@ def _dtype_code(t: torch.Tensor, name: str) -> int:
 def quantize_fp8(x: torch.Tensor, block_rows: int = 1, stream=None):
     """moe_quantize_fp8 of a [rows, cols] CUDA tensor: (codes float8_e4m3fn [rows, cols], scales float32
     [ceil(rows / block_rows), ceil(cols / 128)]).  block_rows: 1 (activations) or 128 (weights)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_fp8(x, block_rows)
     if x.dim() != 2:
         raise ValueError(f"x must have two dimensions, got {x.dim()}")
     if block_rows not in (1, 128):
@@ -796,13 +815,16 @@ def quantize_fp8(x: torch.Tensor, block_rows: int = 1, stream=None):
     rows, cols = x.shape
     q = torch.empty_like(x, dtype=torch.float8_e4m3fn)
     sc = x.new_empty((-(-rows // block_rows), -(-cols // 128)), dtype=torch.float32)
-    _check(lib().moe_quantize_fp8(px, code, rows, cols, block_rows, q.data_ptr(), sc.data_ptr(), _stream(stream, dev)),
+    _check(lib().moe_quantize_fp8(px, code, rows, cols, block_rows, q.data_ptr(), sc.data_ptr(), _stream(dev=dev)),
            "moe_quantize_fp8")
     return q, sc
 
 
 def gemm_fp8(a, a_scales, b, b_scales, out_dtype="bf16", out=None, stream=None):
     """moe_gemm_fp8: [M, N] = a b^T of quantised a [M, K] (1 x 128 blocks) and b [N, K] (128 x 128 blocks)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return gemm_fp8(a, a_scales, b, b_scales, out_dtype, out)
     if a.dim() != 2 or b.dim() != 2:
         raise ValueError("a and b must have two dimensions")
     (M, K), N = a.shape, b.shape[0]
@@ -816,5 +838,5 @@ def gemm_fp8(a, a_scales, b, b_scales, out_dtype="bf16", out=None, stream=None):
         code, po = _dtype_code(out, "out"), _ptr(out, "out", (M, N), out.dtype, dev)
     _check(lib().moe_gemm_fp8(M, N, K, pa, _ptr(a_scales, "a_scales", (M, kb), f32, dev), _ptr(b, "b", (N, K), f8, dev),
                               _ptr(b_scales, "b_scales", (-(-N // 128), kb), f32, dev), po, code,
-                              _stream(stream, dev)), "moe_gemm_fp8")
+                              _stream(dev=dev)), "moe_gemm_fp8")
     return out

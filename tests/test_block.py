@@ -131,3 +131,38 @@ def test_serving_norm_quantiser_product(T):
     graph.replay()
     torch.cuda.synchronize()
     holds(*out)
+
+
+def test_a_call_given_a_stream_allocates_on_it():
+    """Outputs and a workspace of the call's own belong to the given stream: the current stream's next allocation of
+    the same size is not handed memory that the call, still running there, had dropped."""
+    T, d, h = 300, 512, 640
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, w, wg, wd = (torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16) for s in ((T, d), (d,), (h, d), (d, h)))
+    ncfg, fcfg = B.norm_config(T, d), B.ffn_config(T, d, h)
+    side = torch.cuda.Stream()
+
+    def calls(**kw):
+        y, _, mean, rstd = B.norm_forward(ncfg, x, w, want_stats=True, **kw)
+        ws = B.alloc_ffn_workspace(fcfg, train=True)
+        side.wait_stream(torch.cuda.current_stream())
+        f = B.ffn_forward_train(fcfg, x, wg, wg, wd, ws, **kw)
+        q, s = B.quantize_fp8(x, **kw)
+        p, t = B.quantize_fp8(wg, 128, **kw)
+        grads = B.ffn_backward(fcfg, x, wg, wg, wd, f, ws, **kw)
+        out = [y, f, B.ffn_forward(fcfg, x, wg, wg, wd, **kw), q, B.gemm_fp8(q, s, p, t, **kw),
+               *B.norm_backward(ncfg, x, w, mean, rstd, y, want_bias=True, **kw), *grads.values()]
+        torch.cuda.synchronize()
+        return out
+
+    want = calls()
+    side.wait_stream(torch.cuda.current_stream())
+    got = calls(stream=side)
+    for a, b in zip(got, want):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    del a, b
+    while got:
+        t = got.pop()
+        at, shape, dtype = t.data_ptr(), t.shape, t.dtype
+        del t
+        assert torch.empty(shape, dtype=dtype, device="cuda").data_ptr() != at
