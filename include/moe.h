@@ -449,7 +449,7 @@ typedef struct {
  *     MOE_ERR_INVALID_ARG); y [T, d] out;
  *   mean, rstd [T] fp32 out, each optional: what moe_norm_backward takes.
  * h may be x or residual, and y may be x or residual, but not both the same
- * tensor.  Statistics are fp32, the variance summed about the mean. */
+ * tensor (h == y: MOE_ERR_INVALID_ARG).  Statistics are fp32, the variance summed about the mean. */
 moe_status moe_norm_forward(const moe_norm_config *cfg, const void *x, const void *residual,
                             const void *weight, const void *bias, void *h, void *y, float *mean,
                             float *rstd, void *stream);

@@ -968,7 +968,7 @@ moe_status moe_norm_forward(const moe_norm_config *c, const void *x, const void 
     if (st != MOE_OK) return st;
     if ((residual == nullptr) != (h == nullptr)) return MOE_ERR_INVALID_ARG;
     if (c->T == 0) return MOE_OK;
-    if (!x || !weight || !y) return MOE_ERR_INVALID_ARG;
+    if (!x || !weight || !y || h == y) return MOE_ERR_INVALID_ARG;
     if (!device_error_word()) return MOE_ERR_CUDA;
     const int E = 16 / elem_size(c->dtype);
     const bool aligned = aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(bias) && aligned16(h) &&

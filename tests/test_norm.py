@@ -66,6 +66,12 @@ def test_norm_pointers_are_checked():
     assert B.lib().moe_norm_workspace_size(ctypes.byref(cfg), None) == 1
 
 
+def test_norm_of_two_outputs_in_one_tensor_is_refused():
+    other = ctypes.c_void_p(0x20000)
+    cfg = B.norm_config(16, 64)
+    assert _fwd(cfg, x=other, residual=other, h=FAKE, y=FAKE) == 1
+
+
 def test_norm_binding_names_what_it_refuses():
     with pytest.raises(ValueError, match="kind"):
         B.norm_config(4, 8, kind="batch")
