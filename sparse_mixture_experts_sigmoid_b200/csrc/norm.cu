@@ -631,6 +631,8 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
         }
         const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), slot, turn, wi, W, 1 + group);
         // every thread of the group is past the row before this one: its place is free
+        // (one warp has met in shuffles only, which order no memory)
+        if (W == 1) __syncwarp();
         if (i == 0 && r + (kRing - 1) * step < a.T) request(r + (kRing - 1) * step, k == 0 ? kRing - 1 : k - 1);
         // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
         const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
