@@ -66,10 +66,6 @@ __device__ __forceinline__ uint32_t pack2(float a, float b, uint32_t fmt) {
     }
     return r;
 }
-__device__ __forceinline__ float2 unpack2(uint32_t w, uint32_t fmt) {
-    if (fmt) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-    return __half22float2(*reinterpret_cast<const __half2 *>(&w));
-}
 
 // ------------------------------------------------------------------ activations
 // silu(u) = u s, s = 1 / (1 + exp(-u));  gelu_tanh(u) = u (1 + tanh z) / 2 = u s,

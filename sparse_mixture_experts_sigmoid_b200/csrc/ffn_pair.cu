@@ -37,7 +37,6 @@ using namespace tc;
 constexpr int kBM = 256, kBN = 256;        // a pair's tile (GATED: 128 columns of each product)
 constexpr int kBK = 64;                    // 16-bit elements of a 128-byte row
 constexpr int kAStage = 128 * 128;         // this CTA's A of one K block
-constexpr int kAtom = 8192;                // an MN-major atom: 64 k-rows x 128 bytes
 constexpr int kEpiWarps = 8;               // two per TMEM lane quarter
 constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kThreads = (kEpiWarps + 2) * 32;

@@ -181,6 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     constexpr bool WEIGHT = F == Form::kWeight;
     constexpr bool MN = DX || DGATED || WEIGHT;            // the weights' rows are the reduction
     static_assert(!WEIGHT || NT == 64, "one atom of x");
+    static_assert(!FP8 || kPush<NT>, "a thread's sums go from registers");
     constexpr int kStages = stages<NT>();
     constexpr int kXStage = NT * 128;
     constexpr int kBuf = NT < 32 ? 32 : NT;                // TMEM columns of one accumulator
@@ -378,18 +379,10 @@ __global__ void __launch_bounds__(kThreads, 2)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&ctrl->tempty[kb & 1]);
             }
-            if constexpr (kPush<NT>) {
-                if (S > 1) cluster_wait_started();
+            if (S > 1) cluster_wait_started();
 #pragma unroll
-                for (int t = 0; t < NT; t += 4)
-                    if (t < nt) push4(to + t * width, owner, make_float4(acc[t], acc[t + 1], acc[t + 2], acc[t + 3]));
-            } else {
-                // every block product has been read, so every load of the ring has
-                // been consumed -- by all four warps, once they have met
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-#pragma unroll
-                for (int t = 0; t < NT; ++t) sums[t * kRows + row] = acc[t];
-            }
+            for (int t = 0; t < NT; t += 4)
+                if (t < nt) push4(to + t * width, owner, make_float4(acc[t], acc[t + 1], acc[t + 2], acc[t + 3]));
         } else {
             wait_bar(&ctrl->tfull[0], 0, abort, p.err);
             tc_fence_after();
