@@ -115,8 +115,8 @@ moe_status forward(const moe_ffn_config *c, bool train, const void *x, const voi
         g.b1 = {wu, h, d, d};
         g.c0 = {act, T, h, h};
         if (train) {
-            g.c1 = {pre, T, h, 2 * h};
-            g.c2 = {pre + 4 * h, T, h, 2 * h};
+            g.u = {pre, T, h, 2 * h};
+            g.v = {pre + 4 * h, T, h, 2 * h};
         }
         e = launch_gated(g, s);
     }
@@ -213,7 +213,8 @@ moe_status moe_ffn_backward(const moe_ffn_config *c, const void *x, const void *
         Gemm g = product(*c, T, c->h, d, err);
         g.a0 = {dy, T, d, d};
         g.b0 = {w_down, d, h, h};
-        g.pre = reinterpret_cast<const float *>(pre);
+        g.u = {pre, T, h, 2 * h};
+        g.v = {pre + 4 * h, T, h, 2 * h};
         g.c0 = du;
         g.c1 = dv;
         e = launch_dgated(g, s);

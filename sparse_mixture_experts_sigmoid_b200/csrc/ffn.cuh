@@ -12,7 +12,7 @@
 namespace moe {
 namespace ffn {
 
-// A row-major matrix of 16-bit elements (u and v: fp32), row stride ld elements.
+// A row-major matrix of 16-bit elements (the kept u and v: fp32), row stride ld elements.
 struct Matrix {
     const void *base;
     int64_t rows, cols, ld;
@@ -25,8 +25,8 @@ enum Kind : int { GATED = 0, STORE = 1, DGATED = 2 };
 struct Gemm {
     bool a_mn;           // the reduction runs over A's rows (launch_grads)
     Matrix a0, a1, b0, b1;
-    Matrix c0, c1, c2;   // GATED: act, and u, v (base null: not kept); STORE: C (C1: second half); DGATED: du, dv
-    const float *pre;    // DGATED: the kept u | v, rows of 2 N
+    Matrix c0, c1;       // GATED: act; STORE: C (C1: second half); DGATED: du, dv
+    Matrix u, v;         // the kept pre-activations, fp32: GATED stores them (base null: not), DGATED reads them
     int64_t M, K;        // K per range
     int N;
     int ranges, halves;

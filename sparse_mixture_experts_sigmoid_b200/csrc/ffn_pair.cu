@@ -41,7 +41,7 @@ constexpr int kEpiWarps = 8;               // two per TMEM lane quarter
 constexpr int kTmaWarp = kEpiWarps, kMmaWarp = kEpiWarps + 1;
 constexpr int kThreads = (kEpiWarps + 2) * 32;
 constexpr int kTmemCols = 512;
-constexpr int kBox = 32 * 128;             // a store's box: 32 rows x 64 columns
+constexpr int kBox = 32 * 128;             // a store's box: 32 rows x 64 columns (fp32: 32)
 constexpr int kMaxStages = 8;
 constexpr int kSmemMax = 232448;
 
@@ -50,14 +50,16 @@ struct Ctrl {
     uint64_t empty[kMaxStages];   // both: the MMAs of a K block are done
     uint64_t tfull[2];            // both: accumulator ready
     uint64_t tempty[2];           // even CTA: accumulator released by both epilogues
+    uint64_t kept[kEpiWarps];     // DGATED: 32 columns of u and v of a warp have landed
     uint64_t done;                // both: all MMAs of the pair completed
     uint32_t tmem_base;
     int abort;
 };
 
+// A warp's boxes: DGATED u, v, and half a one each for du and dv.
 template <int EPI>
 constexpr int epi_bytes() {
-    return kEpiWarps * kBox * (EPI == DGATED ? 2 : 1);
+    return kEpiWarps * kBox * (EPI == DGATED ? 3 : 1);
 }
 template <int EPI>
 constexpr int stages() {
@@ -84,18 +86,17 @@ struct Params {
     int act;           // moe_ffn_act
     uint32_t fmt;      // operand format of the instruction descriptor: 0 fp16, 1 bf16
     bool keep;         // GATED: store u and v as well
-    const float *pre;  // DGATED: the kept u | v, rows of 2 N
     uint32_t *err;
 };
 
 struct JobMaps {
     CUtensorMap a0, a1, b0, b1;   // operands
-    CUtensorMap c0, c1;           // outputs: C0 (act, du), C1 (u, dv; the second half)
+    CUtensorMap c0, c1;           // outputs: C0 (act, du), C1 (dv; the second half)
 };
 template <int NJOBS>
 struct Maps {
     JobMaps job[NJOBS];
-    CUtensorMap c2;               // GATED: v
+    CUtensorMap u, v;             // the kept pre-activations: GATED stores, DGATED loads them
 };
 
 // How the operands lie: both K-major; B MN-major; or (several jobs) B MN-major
@@ -157,6 +158,12 @@ __device__ __forceinline__ uint4 *box_word(uint8_t *box, int j) {
     return reinterpret_cast<uint4 *>(box + i * 128 + ((j ^ (i & 7)) << 4));
 }
 
+// The same of a box of 64-byte rows (64-byte swizzle): word j at i * 64 + 16 * (j ^ (i / 2 mod 4)).
+__device__ __forceinline__ uint4 *half_box_word(uint8_t *box, int j) {
+    const int i = threadIdx.x & 31;
+    return reinterpret_cast<uint4 *>(box + i * 64 + ((j ^ ((i >> 1) & 3)) << 4));
+}
+
 // GATED: g = act(g) u over a lane's 64 columns.
 template <int ACT>
 __device__ __forceinline__ void gate(float (&g)[64], const float (&u)[64]) {
@@ -167,46 +174,36 @@ __device__ __forceinline__ void gate(float (&g)[64], const float (&u)[64]) {
         g[i + 1] = a.y;
     }
 }
-// DGATED: the kept u and v of 16 columns of a lane's row, by 32-byte loads (whole
-// sectors: the lanes' rows lie apart).  Columns past N are not read.
+// DGATED: 32 columns of a lane's row of the kept u and v, from the warp's boxes.
 struct Kept {
-    float u[16], v[16];
-    __device__ __forceinline__ static void load8f(const float *p, float *o) {
-        asm volatile("ld.global.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=f"(o[0]), "=f"(o[1]), "=f"(o[2]), "=f"(o[3]), "=f"(o[4]), "=f"(o[5]), "=f"(o[6]), "=f"(o[7])
-                     : "l"(p));
-    }
-    __device__ __forceinline__ void load(const float *pre, int r, int c, const Job &j) {
-        const float *at = pre + (int64_t)r * 2 * j.N + c;
+    float u[32], v[32];
+    __device__ __forceinline__ void read(uint8_t *box_u, uint8_t *box_v) {
 #pragma unroll
-        for (int k = 0; k < 16; k += 8) {
-            if (r < j.M && c + k < j.N) {
-                load8f(at + k, u + k);
-                load8f(at + j.N + k, v + k);
-            }
+        for (int j = 0; j < 8; ++j) {
+            *reinterpret_cast<float4 *>(&u[4 * j]) = *reinterpret_cast<const float4 *>(box_word(box_u, j));
+            *reinterpret_cast<float4 *>(&v[4 * j]) = *reinterpret_cast<const float4 *>(box_word(box_v, j));
         }
     }
 };
-// du and dv of those columns into words k and k + 1 of the lane's rows of two boxes.
+// du and dv of 16 of those columns, from r in f.
 template <int ACT>
-__device__ __forceinline__ void gate_grad(const Kept &x, const float (&f)[16], uint32_t fmt, uint8_t *box_u,
-                                          uint8_t *box_v, int k) {
+__device__ __forceinline__ void gate_grad(const float *u, const float *v, const float (&f)[16], uint32_t fmt,
+                                          uint4 *wu, uint4 *wv) {
+    uint32_t a[8], b[8];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        uint32_t wu[4], wv[4];
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-            const int i = 8 * h + 2 * z;
-            const float2 r = make_float2(f[i], f[i + 1]);
-            float2 a, da;
-            act_grad2<ACT>(make_float2(x.u[i], x.u[i + 1]), a, da);
-            const float2 du = mul2(mul2(r, make_float2(x.v[i], x.v[i + 1])), da), dv = mul2(r, a);
-            wu[z] = pack2(du.x, du.y, fmt);
-            wv[z] = pack2(dv.x, dv.y, fmt);
-        }
-        *box_word(box_u, k + h) = make_uint4(wu[0], wu[1], wu[2], wu[3]);
-        *box_word(box_v, k + h) = make_uint4(wv[0], wv[1], wv[2], wv[3]);
+    for (int z = 0; z < 8; ++z) {
+        const int i = 2 * z;
+        const float2 r = make_float2(f[i], f[i + 1]);
+        float2 g, dg;
+        act_grad2<ACT>(make_float2(u[i], u[i + 1]), g, dg);
+        const float2 du = mul2(mul2(r, make_float2(v[i], v[i + 1])), dg), dv = mul2(r, g);
+        a[z] = pack2(du.x, du.y, fmt);
+        b[z] = pack2(dv.x, dv.y, fmt);
     }
+    wu[0] = make_uint4(a[0], a[1], a[2], a[3]);
+    wu[1] = make_uint4(a[4], a[5], a[6], a[7]);
+    wv[0] = make_uint4(b[0], b[1], b[2], b[3]);
+    wv[1] = make_uint4(b[4], b[5], b[6], b[7]);
 }
 
 template <int FORM, int EPI>
@@ -238,6 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&ctrl->tfull[a], 1);
             mbar_init(&ctrl->tempty[a], 2 * kEpiWarps);
         }
+        for (int w = 0; w < kEpiWarps; ++w) mbar_init(&ctrl->kept[w], 1);
         mbar_init(&ctrl->done, 1);
         ctrl->abort = 0;
         fence_barrier_init();
@@ -353,7 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t tempty_lead = mapa_shared(&ctrl->tempty[0], 0);
         const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
         const int cw = (warp >> 2) * kWarpCols;   // this warp's first output column of the tile
-        uint8_t *box = sEpi + warp * (epi_bytes<EPI>() / kEpiWarps), *box2 = box + kBox;
+        uint8_t *box = sEpi + warp * (epi_bytes<EPI>() / kEpiWarps);
         // stores the packed 64 columns of this warp's 32 rows (8 words a row)
         auto put = [&](const CUtensorMap *m, const uint4 (&w)[8], int c, int r, const Job &j) {
             if (lane == 0) bulk_wait_read();   // the previous store has left the box
@@ -384,32 +382,48 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int q = 0; q < 4; ++q) tmem_ld16(at + 16 * q, *reinterpret_cast<float(*)[16]>(&f[16 * q]));
             tmem_wait_ld();
         };
-        // DGATED: this warp's u and v of a pair's k-th tile into L2, a tile ahead (from
-        // HBM they would be waited for 16 columns at a time)
-        [[maybe_unused]] auto fetch = [&](int k) {
-            Tile t;
-            if (!tile_at(k, pair, npairs, p, t)) return;
+        // DGATED: 32 columns of the kept u and v at a time, requested while the 32 before
+        // them are worked on (the first of a tile under its MMAs).  They go through
+        // shared memory by TMA: read from each lane's own row they took 32 lines an
+        // instruction and too few bytes were in flight (T = 4096, d = 640, h = 8192:
+        // 153 us).
+        uint8_t *box_u = box, *box_v = box + kBox, *box_o = box + 2 * kBox;   // (DGATED)
+        [[maybe_unused]] struct {
+            int k, q, r, c;   // the next 32 columns: tile, column in it, row and column of the matrix
+            bool pending;     // requested, not yet waited for
+        } ask = {-1, 0, 0, 0, false};
+        [[maybe_unused]] uint32_t kept_phase = 0;
+        [[maybe_unused]] uint64_t policy = 0;
+        [[maybe_unused]] auto request = [&] {
             const Job &j = p.job[0];
-            const int r = t.m * kBM + (int)rank * 128 + (warp & 3) * 32 + lane, c0 = t.n * kCols + cw;
-            if (r >= j.M) return;
-            const float *at = p.pre + (int64_t)r * 2 * j.N + c0;
-#pragma unroll
-            for (int c = 0; c < kWarpCols; c += 32) {
-                if (c0 + c >= j.N) break;
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + c));
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(at + j.N + c));
+            if (ask.k >= 0) ask.q += 32;
+            if (ask.k < 0 || ask.q >= kWarpCols || ask.c + ask.q >= j.N) {   // on to the next tile with rows and columns of this warp
+                ask.q = 0;
+                Tile next;
+                do {
+                    if (!tile_at(++ask.k, pair, npairs, p, next)) return;
+                    ask.r = next.m * kBM + (int)rank * 128 + (warp & 3) * 32;
+                    ask.c = next.n * kCols + cw;
+                } while (ask.r >= j.M || ask.c >= j.N);
+            }
+            ask.pending = true;
+            if (lane == 0) {
+                mbar_expect_tx(&ctrl->kept[warp], 2 * kBox);
+                tma_load_2d_hint(&maps.u, box_u, &ctrl->kept[warp], ask.c + ask.q, ask.r, policy);
+                tma_load_2d_hint(&maps.v, box_v, &ctrl->kept[warp], ask.c + ask.q, ask.r, policy);
             }
         };
-        if constexpr (EPI == DGATED) fetch(0);
+        if constexpr (EPI == DGATED) {
+            policy = l2_evict_first_policy();
+            request();
+        }
+        bool ok = true;
         Tile t;
         for (int tc = 0; tile_at(tc, pair, npairs, p, t); ++tc) {
-            if constexpr (EPI == DGATED) fetch(tc + 1);
             const Job &j = p.job[t.job];
             const JobMaps &jm = maps.job[FORM == GRADS ? t.job : 0];
             const uint32_t acc = tc & 1;
             const int r = t.m * kBM + (int)rank * 128 + (warp & 3) * 32, c0 = t.n * kCols + cw;
-            [[maybe_unused]] Kept kept;   // DGATED: the first columns' u and v, asked for before r is ready
-            if constexpr (EPI == DGATED) kept.load(p.pre, r + lane, c0, j);
             if (!wait_bar(&ctrl->tfull[acc], (tc >> 1) & 1, abort, p.err)) break;
             tc_fence_after();
             const uint32_t tb = tmem + acc * BN + lane_base;
@@ -435,9 +449,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int q = 0; q < 64; q += 32) {
                             words(&g[q], w);
-                            put(&jm.c1, w, c0 + q, r, j);
+                            put(&maps.u, w, c0 + q, r, j);
                             words(&u[q], w);
-                            put(&maps.c2, w, c0 + q, r, j);
+                            put(&maps.v, w, c0 + q, r, j);
                         }
                     }
                     if (p.act == MOE_ACT_SILU) gate<MOE_ACT_SILU>(g, u);
@@ -446,32 +460,47 @@ __global__ void __launch_bounds__(kThreads, 1)
                     put(&jm.c0, w, c0, r, j);
                 } else {
 #pragma unroll 1
-                    for (int q = 0; q < kWarpCols; q += 64) {
+                    for (int q = 0; q < kWarpCols && ok; q += 32) {
                         if (c0 + q >= j.N) break;
-                        if (lane == 0) bulk_wait_read();   // the previous stores have left the boxes
-                        __syncwarp();
+                        ok = __all_sync(0xffffffffu, wait_bar(&ctrl->kept[warp], kept_phase, abort, p.err));
+                        if (!ok) break;
+                        kept_phase ^= 1;
+                        ask.pending = false;
+                        Kept kept;
+                        kept.read(box_u, box_v);
+                        __syncwarp();   // all lanes have read: the boxes are free
+                        request();
+                        uint4 wu[4], wv[4];
 #pragma unroll
-                        for (int k = 0; k < 64; k += 16) {
-                            const Kept now = kept;
-                            if (q + k + 16 < kWarpCols) kept.load(p.pre, r + lane, c0 + q + k + 16, j);
+                        for (int k = 0; k < 32; k += 16) {
                             float f[16];
                             tmem_ld16(tb + cw + q + k, f);
                             tmem_wait_ld();
                             // one loop per activation: a branch inside would keep the
                             // elements' chains (exponential, reciprocal) from overlapping
-                            if (p.act == MOE_ACT_SILU) gate_grad<MOE_ACT_SILU>(now, f, p.fmt, box, box2, k / 8);
-                            else gate_grad<MOE_ACT_GELU_TANH>(now, f, p.fmt, box, box2, k / 8);
+                            if (p.act == MOE_ACT_SILU)
+                                gate_grad<MOE_ACT_SILU>(&kept.u[k], &kept.v[k], f, p.fmt, wu + k / 8, wv + k / 8);
+                            else
+                                gate_grad<MOE_ACT_GELU_TANH>(&kept.u[k], &kept.v[k], f, p.fmt, wu + k / 8, wv + k / 8);
+                        }
+                        if (lane == 0) bulk_wait_read();   // the previous stores have left the box
+                        __syncwarp();
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            *half_box_word(box_o, k) = wu[k];
+                            *half_box_word(box_o + kBox / 2, k) = wv[k];
                         }
                         fence_proxy_async();
                         __syncwarp();
                         if (lane == 0) {
-                            tma_store_2d(&jm.c0, box, c0 + q, r);
-                            tma_store_2d(&jm.c1, box2, c0 + q, r);
+                            tma_store_2d(&jm.c0, box_o, c0 + q, r);
+                            tma_store_2d(&jm.c1, box_o + kBox / 2, c0 + q, r);
                             bulk_commit();
                         }
                     }
                 }
             }
+            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
@@ -480,6 +509,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
         if (lane == 0) bulk_wait_all();
+        if (EPI == DGATED && ask.pending) {   // aborting: let the copies land before the CTA leaves
+            const uint64_t t0 = globaltimer();
+            while (!mbar_try_wait(&ctrl->kept[warp], kept_phase) && globaltimer() - t0 < 100000000ull) {
+            }
+        }
     }
 
     // every MMA of the pair has completed (its arrivals on this CTA's barriers
@@ -498,20 +532,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------ host side
 
-// A row-major matrix of 16-bit (or fp32) elements, boxes of 128 bytes of columns
-// (128-byte swizzle) by box_rows; what lies outside reads as zero and is not
-// written.
-bool make_map16(CUtensorMap *m, const Matrix &x, uint32_t box_rows, bool f32 = false) {
+// A row-major matrix of elements of `size` bytes (2, or 4: fp32), boxes of
+// box_cols bytes of columns (128, or 64; swizzled over as many) by box_rows; what
+// lies outside reads as zero and is not written.
+bool make_map(CUtensorMap *m, const Matrix &x, uint32_t box_rows, uint32_t size = 2, uint32_t box_cols = 128) {
     auto fn = encode_fn();
     if (!fn || !x.base) return false;
-    const uint32_t size = f32 ? 4 : 2;
     cuuint64_t dims[2] = {(cuuint64_t)x.cols, (cuuint64_t)x.rows};
     cuuint64_t strides[1] = {(cuuint64_t)x.ld * size};
-    cuuint32_t box[2] = {128 / size, box_rows};
+    cuuint32_t box[2] = {box_cols / size, box_rows};
     cuuint32_t estr[2] = {1, 1};
-    return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(x.base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    return fn(m, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(x.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Job i of a launch from its product; false when a tensor map cannot be made.
@@ -521,10 +555,11 @@ bool set_job(const Gemm &g, int i, M &maps, Params &p) {
     JobMaps &m = maps.job[i];
     // operand boxes: K-major 128 rows of 64 k; MN-major 64 k-rows of 64 columns
     const uint32_t ab = g.a_mn ? 64 : 128, bb = FORM == KK ? 128 : 64;
-    if (!make_map16(&m.a0, g.a0, ab) || !make_map16(&m.b0, g.b0, bb) || !make_map16(&m.c0, g.c0, 32)) return false;
-    if (g.a1.base && !make_map16(&m.a1, g.a1, ab)) return false;
-    if (g.b1.base && !make_map16(&m.b1, g.b1, bb)) return false;
-    if (g.c1.base && !make_map16(&m.c1, g.c1, 32, EPI == GATED)) return false;   // GATED: u, fp32
+    const uint32_t cols = EPI == DGATED ? 64 : 128;   // of an output's box, in bytes
+    if (!make_map(&m.a0, g.a0, ab) || !make_map(&m.b0, g.b0, bb) || !make_map(&m.c0, g.c0, 32, 2, cols)) return false;
+    if (g.a1.base && !make_map(&m.a1, g.a1, ab)) return false;
+    if (g.b1.base && !make_map(&m.b1, g.b1, bb)) return false;
+    if (g.c1.base && !make_map(&m.c1, g.c1, 32, 2, cols)) return false;
     Job &j = p.job[i];
     j.M = (int)g.M;
     j.N = g.N;
@@ -543,12 +578,11 @@ cudaError_t launch(const Gemm *g, int n, cudaStream_t s) {
     Params p{};
     for (int i = 0; i < n; ++i)
         if (!set_job<FORM, EPI>(g[i], i, maps, p)) return cudaErrorInvalidValue;
-    if (g->c2.base && !make_map16(&maps.c2, g->c2, 32, true)) return cudaErrorInvalidValue;
+    p.keep = EPI == GATED && g->u.base != nullptr;
+    if (g->u.base && (!make_map(&maps.u, g->u, 32, 4) || !make_map(&maps.v, g->v, 32, 4))) return cudaErrorInvalidValue;
     p.njobs = n;
     p.act = g->act;
     p.fmt = g->bf16 ? 1u : 0u;
-    p.keep = g->c1.base != nullptr;
-    p.pre = g->pre;
     p.err = g->err;
     for (int i = 1; i < n; ++i) p.rest += p.job[i].tiles;
     const int64_t tiles = (int64_t)p.job[0].tiles + p.rest;
