@@ -534,7 +534,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // A row-major matrix of elements of `size` bytes (2, or 4: fp32), boxes of
 // box_cols bytes of columns (128, or 64; swizzled over as many) by box_rows; what
-// lies outside reads as zero and is not written.
+// lies outside reads as zero and is not written.  fp32, the kept pre-activations:
+// a warp reads its row's next 128 bytes later, under evict-first, and a promotion
+// to 256 bytes fetched them twice (du, dv of T = 4096, d = 2048, h = 5632: 100 us,
+// 88 with 128 bytes; 93 without evict-first).
 bool make_map(CUtensorMap *m, const Matrix &x, uint32_t box_rows, uint32_t size = 2, uint32_t box_cols = 128) {
     auto fn = encode_fn();
     if (!fn || !x.base) return false;
@@ -545,7 +548,7 @@ bool make_map(CUtensorMap *m, const Matrix &x, uint32_t box_rows, uint32_t size 
     return fn(m, size == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
               const_cast<void *>(x.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
               box_cols == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+              size == 4 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Job i of a launch from its product; false when a tensor map cannot be made.
