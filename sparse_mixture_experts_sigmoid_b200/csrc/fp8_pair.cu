@@ -9,10 +9,15 @@
 // each is read back from TMEM and added to fp32 registers under its scale.  TMEM
 // holds two block products (2 x 256 columns): while the epilogue warps add one,
 // the MMAs write the other.  Per K block of a CTA the MMAs take 512 cycles at the
-// full rate, and the eight epilogue warps 128 x 256 multiply-adds (256 cycles of
-// the four schedulers) and as many TMEM words, so the tensor cores stay the
-// bound.  A warp owns 32 rows x 128 columns of the tile, one scale of B: a
-// thread's 128 sums have one scale per block, sa sb.
+// full rate, and the eight epilogue warps 128 x 256 multiply-adds (two an
+// instruction: 128 cycles of the four schedulers) and as many TMEM words.  A warp
+// owns 32 rows x 128 columns of the tile, one scale of B: a thread's 128 sums have
+// one scale per block, sa sb.
+//
+// M = K = 4096, N = 14336: 227 us, 2.1 PFLOP/s (246 with one multiply-add an
+// instruction).  A K block takes 0.54 us: its 64 KB come from L2 in 0.43 with all
+// pairs at work, its MMAs take 0.27, and 13 rounds of tiles are begun where 12.1
+// are full.
 //
 // Every mbarrier wait is bounded as in the grouped kernels.
 #include <cuda_fp16.h>
@@ -20,6 +25,7 @@
 #include <algorithm>
 
 #include "fp8.cuh"
+#include "packed.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
@@ -232,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         tc_fence_after();
                         const uint64_t ad = smem_desc(sA + s * kStage), bd = smem_desc(sB + s * kStage);
-    #pragma unroll
+#pragma unroll
                         for (int kk = 0; kk < 4; ++kk) mma_if<2, kF8>(mine, tmem + acc * kBN, ad + 2 * kk, bd + 2 * kk, kIdesc, kk != 0);
                         mma_commit2_if(mine, &ctrl->empty[s], 0x3);
                         mma_commit2_if(mine, &ctrl->tfull[acc], 0x3);
@@ -310,7 +316,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                         }
 #pragma unroll
-                        for (int z = 0; z < 16; ++z) acc[16 * q + z] = fmaf(v[q & 1][z], scale[i], acc[16 * q + z]);
+                        for (int z = 0; z < 16; z += 2) {
+                            const float *f = &v[q & 1][z];
+                            float *o = &acc[16 * q + z];
+                            const float2 sum = fma2(make_float2(f[0], f[1]), both(scale[i]), make_float2(o[0], o[1]));
+                            o[0] = sum.x;
+                            o[1] = sum.y;
+                        }
                     }
                     ++it;
                 }
