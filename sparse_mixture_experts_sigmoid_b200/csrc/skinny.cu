@@ -516,6 +516,15 @@ bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// K ranges of a product of `tiles` tiles and kb K blocks: as many as fill two CTAs on
+// every SM, with four K blocks each at least (half as many, or half as many again: 5
+// to 20 % slower on the sizes that wants() lists).
+int ranges(int64_t tiles, int kb) {
+    int S = 1;
+    while (S < 8 && tiles * S * 2 <= 2 * num_sms() && kb >= 8 * S) S *= 2;
+    return S;
+}
+
 template <Form F, int NT>
 cudaError_t launch_nt(const Product &g, cudaStream_t s) {
     constexpr bool FP8 = F == Form::kFp8, GATED = F == Form::kGated, DX = F == Form::kDx;
@@ -551,10 +560,7 @@ cudaError_t launch_nt(const Product &g, cudaStream_t s) {
     p.early = g.early;
     p.err = g.err;
     const int tiles = p.mt * (int)((g.T + NT - 1) / NT) * (WEIGHT && g.w1 ? 2 : 1);
-    // K ranges: as many as fill two CTAs on every SM, with four K blocks each at least
-    // (half as many, or half as many again: 5 to 20 % slower on the listed sizes of wants())
-    p.S = 1;
-    while (p.S < 8 && tiles * p.S * 2 <= 2 * num_sms() && p.kb >= 8 * p.S) p.S *= 2;
+    p.S = ranges(tiles, p.kb);
     const size_t smem = 1024 + (size_t)stages<NT>() * (kWStage + NT * 128) + recv_bytes<NT>() +
                         (FP8 ? 4 * 2 * NT * 4 : 0) + sizeof(Ctrl);
     auto kern = skinny_kernel<F, NT>;
@@ -602,17 +608,21 @@ cudaError_t launch_form(const Product &g, cudaStream_t s) {
 //   STORE  2048 x 5632: T = 64 26/45, 768 54/58, 2048 116/101;  4096 x 14336: T = 256
 //          97/126, 768 240/208;  512 x 8192: T = 2048 75/111, 4096 126/114;  K = 512:
 //          27/24 at T = 128
-//   8 bits 14336 x 4096: T = 64 20/33, 128 32/34, 256 62/35;  2048 x 2048: T = 512
-//          13/14, 768 18/14;  640 x 8192: T = 1024 31/39, 2048 56/39
+//   8 bits 14336 x 4096: T = 32 15/19, 64 21/20, 128 35/20;  2048 x 2048: T = 256 9/12,
+//          512 12/12;  640 x 8192: T = 768 19/34, 1024 33/33;  5632 x 2048: T = 64
+//          9/12, 128 12/12, 256 19/12
 //   and of the whole backward pass with this kernel in the place of one product:
-//   DGATED 3672 x 384: T = 64 22/46, 2048 81/103;  2048 x 5632: T = 128 93/106, 512
-//          115/109;  208 x 2944 (short K): T = 32 61/64, 128 70/61
+//   DGATED (with one weight's gradient) 3672 x 384: T = 64 13/32, 2048 36/45, 4096
+//          62/61;  2048 x 5632: T = 128 23/28, 256 31/32, 512 48/38;  640 x 2048: T =
+//          256 18/19, 512 22/21;  208 x 2944 (short K): T = 32 13/15, 64 16/15
 //   DX     640 x 2048: T = 9 23/41, 1024 43/47, 2048 61/54;  4096 x 14336: T = 64
 //          154/234, 512 364/347;  3672 x 384 (short K): T = 64 51/46
 //   WEIGHT 80 x 168: T = 1024 30/25, 8192 40/69;  512 x 512: T = 2048 44/38, 8192
 //          65/84;  640 x 2048 (more tiles): T = 8192 299/189
 // The 256-row tiles need enough tiles for the pairs of SMs and a long enough K; this
-// kernel reads the weights again for every 128 (8 bits: 64) tokens.
+// kernel reads the weights again for every 128 (8 bits: 64) tokens.  In 8 bits, past
+// 32 tokens, it also adds each K block's product under its scales, 1 us a block
+// where the 256-row tiles take 0.45: it needs K in four ranges.
 bool wants(Form form, int64_t T, int N, int K) {
     const int64_t tiles = (T + 255) / 256 * ((N + 255) / 256);
     switch (form) {
@@ -620,7 +630,7 @@ bool wants(Form form, int64_t T, int N, int K) {
         case Form::kDGated: return T <= 32 || (K >= 512 && (T <= 128 || tiles <= 24));
         case Form::kDx: return tiles <= 16 && K >= 1024;
         case Form::kWeight: return tiles <= 8 && K >= 4096;
-        case Form::kFp8: return T <= 128 || tiles <= 16;
+        case Form::kFp8: return T <= 32 || ranges((T + 63) / 64 * ((N + kRows - 1) / kRows), (K + 127) / 128) >= 4;
         default: return T <= 64 || (tiles <= 24 && K >= 1024);
     }
 }
