@@ -200,36 +200,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     volatile int *abort = &ctrl->abort;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(&ctrl->full[s], 1);
-            mbar_init(&ctrl->empty[s], 1);
-        }
-        for (int a = 0; a < 2; ++a) {
-            mbar_init(&ctrl->tfull[a], 1);
-            mbar_init(&ctrl->tempty[a], 4);
-        }
-        ctrl->abort = 0;
-        fence_barrier_init();
-    }
-    if (warp == kMmaWarp) tmem_alloc(&ctrl->tmem_base, kTmemCols);
-    if (warp == kTmaWarp && lane == 0) {
-        prefetch_tmap(&tmX);
-        prefetch_tmap(&tmW0);
-        if (GATED || DX) prefetch_tmap(&tmW1);
-    }
-    if (!p.early) pdl_wait();
-    tc_fence_before();
-    __syncthreads();
-    tc_fence_after();
-    // early: only the producer goes ahead of the previous kernel's completion
-    if (warp != kTmaWarp) {
-        if (p.early) pdl_wait();
-        pdl_launch_dependents();
-    }
-
-    if (kPush<NT> && p.S > 1) cluster_started();
-    const uint32_t tmem = ctrl->tmem_base;
     const int S = p.S, rank = S > 1 ? (int)cluster_rank() : 0;
     int tile = blockIdx.x / S;
     const int half_tiles = p.mt * ((p.T + NT - 1) / NT);
@@ -240,38 +210,67 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int per = kOutRows / S, width = kRows / S;   // output rows, and sums' rows, of this CTA
     const int k0 = (int)((int64_t)p.kb * rank / S), k1 = (int)((int64_t)p.kb * (rank + 1) / S), nk = k1 - k0;
 
+    // the producer sets its barriers up and requests the first stages; meanwhile the
+    // others allocate TMEM
+    const int head = min(nk, kStages);
+    const uint64_t policy = l2_evict_first_policy();   // a weight is read by this CTA only, or soon by few
+    // K block kb of this CTA's range: its range of K (DX) and column in it
+    auto weights = [&](int s, int kb) {
+        uint8_t *w = sW + s * kWStage;
+        const bool second = DX && k0 + kb >= p.kr;
+        const int k = (k0 + kb - (second ? p.kr : 0)) * kK;
+        if constexpr (MN) {
+            const CUtensorMap *m = second || half ? &tmW1 : &tmW0;
+            tma_load_2d_hint(m, w, &ctrl->full[s], n0, k, policy);
+            tma_load_2d_hint(m, w + kWStage / 2, &ctrl->full[s], n0 + 64, k, policy);
+        } else if constexpr (GATED) {
+            tma_load_2d_hint(&tmW0, w, &ctrl->full[s], k, n0, policy);
+            tma_load_2d_hint(&tmW1, w + kWStage / 2, &ctrl->full[s], k, n0, policy);
+        } else {
+            tma_load_2d_hint(&tmW0, w, &ctrl->full[s], k, n0, policy);
+        }
+    };
+    auto tokens = [&](int s, int kb) {
+        const bool second = DX && k0 + kb >= p.kr;
+        const int k = (k0 + kb - (second ? p.kr : 0)) * kK;
+        if constexpr (WEIGHT) tma_load_2d(&tmX, sX + s * kXStage, &ctrl->full[s], t0, k);
+        else tma_load_2d(second ? &tmX1 : &tmX, sX + s * kXStage, &ctrl->full[s], k, t0);
+    };
+    if (warp == kTmaWarp && lane == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&ctrl->full[s], 1);
+            mbar_init(&ctrl->empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&ctrl->tfull[a], 1);
+            mbar_init(&ctrl->tempty[a], 4);
+        }
+        ctrl->abort = 0;
+        fence_barrier_init();
+        fence_proxy_async();   // (this thread's copies arrive on them next)
+        // early: the weights are not the previous kernel's, they go ahead of its completion
+        if (!p.early) pdl_wait();
+        for (int kb = 0; kb < head; ++kb) {
+            mbar_expect_tx(&ctrl->full[kb], kWStage + kXStage);
+            weights(kb, kb);
+        }
+        if (p.early) pdl_wait();
+        for (int kb = 0; kb < head; ++kb) tokens(kb, kb);
+    }
+    if (warp == kMmaWarp) tmem_alloc(&ctrl->tmem_base, kTmemCols);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp != kTmaWarp) {
+        pdl_wait();
+        pdl_launch_dependents();
+    }
+
+    if (kPush<NT> && S > 1) cluster_started();
+    const uint32_t tmem = ctrl->tmem_base;
+
     if (warp == kTmaWarp) {
         if (lane == 0) {
-            const uint64_t policy = l2_evict_first_policy();   // a weight is read by this CTA only, or soon by few
-            // K block kb of this CTA's range: its range of K (DX) and column in it
-            auto weights = [&](int s, int kb) {
-                uint8_t *w = sW + s * kWStage;
-                const bool second = DX && k0 + kb >= p.kr;
-                const int k = (k0 + kb - (second ? p.kr : 0)) * kK;
-                if constexpr (MN) {
-                    const CUtensorMap *m = second || half ? &tmW1 : &tmW0;
-                    tma_load_2d_hint(m, w, &ctrl->full[s], n0, k, policy);
-                    tma_load_2d_hint(m, w + kWStage / 2, &ctrl->full[s], n0 + 64, k, policy);
-                } else if constexpr (GATED) {
-                    tma_load_2d_hint(&tmW0, w, &ctrl->full[s], k, n0, policy);
-                    tma_load_2d_hint(&tmW1, w + kWStage / 2, &ctrl->full[s], k, n0, policy);
-                } else {
-                    tma_load_2d_hint(&tmW0, w, &ctrl->full[s], k, n0, policy);
-                }
-            };
-            auto tokens = [&](int s, int kb) {
-                const bool second = DX && k0 + kb >= p.kr;
-                const int k = (k0 + kb - (second ? p.kr : 0)) * kK;
-                if constexpr (WEIGHT) tma_load_2d(&tmX, sX + s * kXStage, &ctrl->full[s], t0, k);
-                else tma_load_2d(second ? &tmX1 : &tmX, sX + s * kXStage, &ctrl->full[s], k, t0);
-            };
-            const int head = min(nk, kStages);
-            for (int kb = 0; kb < head; ++kb) {
-                mbar_expect_tx(&ctrl->full[kb], kWStage + kXStage);
-                weights(kb, kb);
-            }
-            if (p.early) pdl_wait();
-            for (int kb = 0; kb < head; ++kb) tokens(kb, kb);
             bool ok = true;
             int kb = head;
             for (; kb < nk; ++kb) {
@@ -369,10 +368,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
                     for (int z = 0; z < 16; z += 4) {
                         const float4 f = *reinterpret_cast<const float4 *>(sc + q + z);
-                        acc[q + z] = fmaf(v[z], f.x, acc[q + z]);
-                        acc[q + z + 1] = fmaf(v[z + 1], f.y, acc[q + z + 1]);
-                        acc[q + z + 2] = fmaf(v[z + 2], f.z, acc[q + z + 2]);
-                        acc[q + z + 3] = fmaf(v[z + 3], f.w, acc[q + z + 3]);
+                        float *o = &acc[q + z];
+                        const float2 a = fma2(make_float2(v[z], v[z + 1]), make_float2(f.x, f.y), make_float2(o[0], o[1]));
+                        const float2 b = fma2(make_float2(v[z + 2], v[z + 3]), make_float2(f.z, f.w), make_float2(o[2], o[3]));
+                        o[0] = a.x;
+                        o[1] = a.y;
+                        o[2] = b.x;
+                        o[3] = b.y;
                     }
                 }
                 tc_fence_before();
