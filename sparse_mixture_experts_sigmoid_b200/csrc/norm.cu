@@ -1017,7 +1017,8 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
                 : c->dtype == MOE_F16 ? bwd_kernel<__half>(sp, dbias != nullptr)
                                       : bwd_kernel<float>(sp, dbias != nullptr);
     cudaError_t e = cudaSuccess;
-    if (smem > 48 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // without the attribute a block has 48 KB, the kernel's own arrays (under 4 KB) included
+    if (smem > 44 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     const int threads = sp.groups * sp.W * 32;
     const int blocks = blocks_for(sp, c->T, std::min(bwd_most(c->d), resident_blocks(kern, threads, smem)));
     if (e == cudaSuccess) e = launch_kernel(kern, blocks, threads, smem, s, a);

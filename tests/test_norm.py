@@ -273,6 +273,31 @@ def test_backward(case):
     check_backward(*case)
 
 
+# widths whose rows in flight take 48 KB of shared memory exactly
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,dtype,d,use_dh,use_bias", [
+    ("layer", "f16", 256, True, True), ("rms", "bf16", 256, True, False), ("rms", "bf16", 384, False, False),
+    ("layer", "f32", 128, True, True), ("layer", "f32", 192, False, True), ("rms", "f32", 192, False, False),
+])
+def test_backward_at_the_first_shared_memory_limit(kind, dtype, d, use_dh, use_bias):
+    check_backward(kind, dtype, dtype, 1006, d, use_dh, use_bias)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [6130, 6144])
+def test_backward_of_unaligned_rows_at_the_first_shared_memory_limit(d):
+    v = make(21, d, "bf16", "bf16", 6)
+    cfg, w, x = B.norm_config(21, d, kind="rms"), cuda(v["weight"]), cuda(v["x"])
+    _, _, _, rstd = B.norm_forward(cfg, x, w, want_stats=True)
+    dx0, dw0, _ = B.norm_backward(cfg, x, w, None, rstd, cuda(v["dy"]))
+    raw = torch.zeros(21 * d + 1, dtype=torch.bfloat16, device="cuda")
+    raw[1:] = cuda(v["dy"]).flatten()
+    dx, dw, _ = B.norm_backward(cfg, x, w, None, rstd, raw[1:].view(21, d))
+    # two kernels' 32-bit results of one formula, the first rounded to bf16 once by each
+    assert (dx.float() - dx0.float()).abs().max() <= torch.finfo(torch.bfloat16).eps * dx0.float().abs().max()
+    assert (dw - dw0).abs().max() <= F32 * (cuda(v["dy"]).float().abs() * (x.float() * rstd[:, None]).abs()).sum(0).max()
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind", ["layer", "rms"])
 def test_backward_against_differences(kind):
