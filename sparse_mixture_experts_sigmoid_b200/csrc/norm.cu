@@ -338,12 +338,13 @@ struct NormBwd {
     int d, W, groups;
     bool wf32, want_db;
     uint32_t *err;
+    int depth;              // norm_bwd_wide_kernel: rows in its ring, and whether dh's are among them
+    bool ring_dh;
 };
 
 // The block's partial sums: its groups add their columns one after another in
-// `cols` ([2, d], groups > 1), the last one writes them out.  Whole words: eight
-// (four) consecutive columns of a thread at a time.
-template <typename T, int VPT, bool SHIFT, bool DB>
+// `cols` ([2, d], groups > 1), the last one writes them out.
+template <typename T, int VPT, bool DB>
 __device__ __forceinline__ void write_part(const NormBwd &a, float *cols, int group, int c0, int cj,
                                            const float2 (&dw)[VPT][kPairs<T>],
                                            const float2 (&db)[DB ? VPT : 1][kPairs<T>]) {
@@ -359,24 +360,11 @@ __device__ __forceinline__ void write_part(const NormBwd &a, float *cols, int gr
                 for (int h = 0; h < (DB ? 2 : 1); ++h) {
                     const int c = c0 + j * cj;
                     float *to = (last ? out : cols) + h * d, *from = cols + h * d;
-                    if constexpr (SHIFT) {
 #pragma unroll
-                        for (int e = 0; e < 2 * P; ++e) {
-                            if (c + e < 0 || c + e >= d) continue;
-                            const float2 v = h ? db[DB ? j : 0][e / 2] : dw[j][e / 2];
-                            to[c + e] = (e & 1 ? v.y : v.x) + (k ? from[c + e] : 0.f);
-                        }
-                    } else if (c < d) {
-#pragma unroll
-                        for (int q = 0; q < P; q += 2) {
-                            const float2 u = h ? db[DB ? j : 0][q] : dw[j][q], v = h ? db[DB ? j : 0][q + 1] : dw[j][q + 1];
-                            float4 f = make_float4(u.x, u.y, v.x, v.y);
-                            if (k) {
-                                const float4 b = *reinterpret_cast<const float4 *>(from + c + 2 * q);
-                                f = make_float4(f.x + b.x, f.y + b.y, f.z + b.z, f.w + b.w);
-                            }
-                            *reinterpret_cast<float4 *>(to + c + 2 * q) = f;
-                        }
+                    for (int e = 0; e < 2 * P; ++e) {
+                        if (c + e < 0 || c + e >= d) continue;
+                        const float2 v = h ? db[DB ? j : 0][e / 2] : dw[j][e / 2];
+                        to[c + e] = (e & 1 ? v.y : v.x) + (k ? from[c + e] : 0.f);
                     }
                 }
             }
@@ -385,12 +373,10 @@ __device__ __forceinline__ void write_part(const NormBwd &a, float *cols, int gr
     }
 }
 
-// Up to two words a thread, a row's words are held between its two passes and
-// the next row's are requested meanwhile; of wider rows only the gradients' sums
-// stay in registers, and the second pass reads the row again, from L1.
-template <typename T, int VPT, bool SHIFT, bool DB, int THREADS>
-__global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) norm_bwd_kernel(NormBwd a) {
-    constexpr bool HOLD = VPT <= 2;
+// The backward pass of shifted rows (up to two words a thread): a row's words are
+// held between its two passes, and the next row's are requested meanwhile.
+template <typename T, int VPT, bool DB, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1) norm_bwd_shift_kernel(NormBwd a) {
     constexpr int E = kElems<T>, P = kPairs<T>;
     __shared__ float2 red[8 * 32];
     extern __shared__ float cols[];     // groups > 1: [2, d]
@@ -401,7 +387,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
     const float inv = 1.f / (float)d;
     const int64_t step = (int64_t)gridDim.x * a.groups;
     int64_t r = (int64_t)blockIdx.x * a.groups + group;
-    const int shift = SHIFT ? (int)(r * d % E) : 0;
+    const int shift = (int)(r * d % E);
     const bool layer = a.mean != nullptr, more = a.dh != nullptr, wf32 = a.wf32;
     // this thread's first word of the row in each tensor
     const int64_t o = r * d + i * E - shift;
@@ -420,63 +406,55 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
         }
     pdl_wait();
     pdl_launch_dependents();
-    float2 held[SHIFT ? VPT : 1][P];   // shifted rows: the weights, taken once
-    if constexpr (SHIFT) {
+    float2 w[VPT][P];   // the weights, taken once
 #pragma unroll
-        for (int j = 0; j < VPT; ++j) load_param<T, true>(a.weight, wf32, c0 + j * cj, d, held[j]);
-    }
-    uint4 nh[HOLD ? VPT : 1], ny[HOLD ? VPT : 1];
+    for (int j = 0; j < VPT; ++j) load_param<T, true>(a.weight, wf32, c0 + j * cj, d, w[j]);
+    uint4 nh[VPT], ny[VPT];
     float nm = 0.f, ns = 0.f;
     if (r < a.T) {
-        if constexpr (HOLD) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                nh[j] = load_word<T, SHIFT>(h + j * cj, c0 + j * cj, d);
-                ny[j] = load_word<T, SHIFT>(dy + j * cj, c0 + j * cj, d);
-            }
+        for (int j = 0; j < VPT; ++j) {
+            nh[j] = load_word<T, true>(h + j * cj, c0 + j * cj, d);
+            ny[j] = load_word<T, true>(dy + j * cj, c0 + j * cj, d);
         }
         if (layer) nm = a.mean[r];
         ns = a.rstd[r];
     }
     for (; r < a.T; r += step) {
-        uint4 cd[HOLD ? VPT : 1];
+        uint4 cd[VPT];
         const float mean = nm, rstd = ns;
         const bool next = r + step < a.T;
-        if (HOLD && more) {
+        if (more) {
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) cd[j] = load_word<T, SHIFT>(dh + j * cj, c0 + j * cj, d);
+            for (int j = 0; j < VPT; ++j) cd[j] = load_word<T, true>(dh + j * cj, c0 + j * cj, d);
         }
         if (next) {
             if (layer) nm = a.mean[r + step];
             ns = a.rstd[r + step];
         }
-        float2 z[HOLD ? VPT : 1][P], g[HOLD ? VPT : 1][P];
+        float2 z[VPT][P], g[VPT][P];
         float2 sg = both(0.f), sz = both(0.f);   // sums of g and of g (h - mean)
         // elements outside the row have dy = 0: they add nothing to any sum
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            constexpr bool kHold = HOLD;
-            const int q = kHold ? j : 0, c = c0 + j * cj;
-            float2 loaded[P], y[P];
-            float2(&w)[P] = SHIFT ? held[SHIFT ? j : 0] : loaded;
-            if constexpr (!SHIFT) load_param<T, false>(a.weight, wf32, c, d, w);
-            unpack<T>(kHold ? nh[q] : load_word<T, SHIFT>(h + j * cj, c, d), z[q]);
-            unpack<T>(kHold ? ny[q] : load_word<T, SHIFT>(dy + j * cj, c, d), y);
+            float2 y[P];
+            unpack<T>(nh[j], z[j]);
+            unpack<T>(ny[j], y);
 #pragma unroll
             for (int k = 0; k < P; ++k) {
-                z[q][k] = add2(z[q][k], both(-mean));
-                g[q][k] = mul2(y[k], w[k]);
-                sg = add2(sg, g[q][k]);
-                sz = fma2(g[q][k], z[q][k], sz);
-                dw[j][k] = fma2(mul2(y[k], both(rstd)), z[q][k], dw[j][k]);
+                z[j][k] = add2(z[j][k], both(-mean));
+                g[j][k] = mul2(y[k], w[j][k]);
+                sg = add2(sg, g[j][k]);
+                sz = fma2(g[j][k], z[j][k], sz);
+                dw[j][k] = fma2(mul2(y[k], both(rstd)), z[j][k], dw[j][k]);
                 if (DB) db[j][k] = add2(db[j][k], y[k]);
             }
         }
-        if (HOLD && next) {
+        if (next) {
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                nh[j] = load_word<T, SHIFT>(h + jump + j * cj, c0 + j * cj, d);
-                ny[j] = load_word<T, SHIFT>(dy + jump + j * cj, c0 + j * cj, d);
+                nh[j] = load_word<T, true>(h + jump + j * cj, c0 + j * cj, d);
+                ny[j] = load_word<T, true>(dy + jump + j * cj, c0 + j * cj, d);
             }
         }
         const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), slot, turn, wi, W, 1 + group);
@@ -484,36 +462,22 @@ __global__ void __launch_bounds__(THREADS, THREADS == 256 && !SHIFT ? 2 : 1) nor
         const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            constexpr bool kHold = HOLD;
-            const int q = kHold ? j : 0, c = c0 + j * cj;
-            if constexpr (!HOLD) {
-                float2 w[P];
-                load_param<T, false>(a.weight, wf32, c, d, w);
-                unpack<T>(load_word<T, SHIFT>(h + j * cj, c, d), z[0]);
-                unpack<T>(load_word<T, SHIFT>(dy + j * cj, c, d), g[0]);
-                if (more) cd[0] = load_word<T, SHIFT>(dh + j * cj, c, d);
 #pragma unroll
-                for (int k = 0; k < P; ++k) {
-                    z[0][k] = add2(z[0][k], both(-mean));
-                    g[0][k] = mul2(g[0][k], w[k]);
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < P; ++k) z[q][k] = fma2(z[q][k], both(c2), fma2(g[q][k], both(rstd), both(c1)));
+            for (int k = 0; k < P; ++k) z[j][k] = fma2(z[j][k], both(c2), fma2(g[j][k], both(rstd), both(c1)));
             if (more) {
                 float2 y[P];
-                unpack<T>(cd[q], y);
+                unpack<T>(cd[j], y);
 #pragma unroll
-                for (int k = 0; k < P; ++k) z[q][k] = add2(z[q][k], y[k]);
+                for (int k = 0; k < P; ++k) z[j][k] = add2(z[j][k], y[k]);
             }
-            store_word<T, SHIFT>(dx + j * cj, c, d, pack<T>(z[q]));
+            store_word<T, true>(dx + j * cj, c0 + j * cj, d, pack<T>(z[j]));
         }
         h += jump;
         dy += jump;
         if (more) dh += jump;
         dx += jump;
     }
-    if (a.part) write_part<T, VPT, SHIFT, DB>(a, cols, group, c0, cj, dw, db);
+    if (a.part) write_part<T, VPT, DB>(a, cols, group, c0, cj, dw, db);
 }
 
 // The backward pass of whole-word rows of up to two words a thread (three in a
@@ -686,6 +650,163 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
             f = make_float4(f.x + b.x, f.y + b.y, f.z + b.z, f.w + b.w);
         }
         *reinterpret_cast<float4 *>(out + c) = f;
+    }
+}
+
+// The backward pass of wide rows (whole words, more than two a thread): a block per
+// row, and a ring of as many rows as fit into shared memory (one to four), filled as
+// above; dh's rows are in it only if two rows fit with them (else they are fetched
+// into L2 meanwhile).  The weights stand beside it as they are.  Only the gradients'
+// sums stay in registers: the second pass reads the row from shared memory again.
+// Read from global memory twice, with no row in flight, T = 2989, d = 11224 in fp32
+// took 258 us and T = 2516, d = 13336 in bf16 90.
+constexpr int kWideSmem = 224 * 1024;
+constexpr int kWideRows = 4;
+
+template <typename T, int VPT, bool DB>
+__global__ void __launch_bounds__(512, 1) norm_bwd_wide_kernel(NormBwd a) {
+    constexpr int E = kElems<T>, P = kPairs<T>;
+    __shared__ float2 red[32];
+    __shared__ uint64_t landed[kWideRows];
+    __shared__ int gave_up;
+    extern __shared__ __align__(16) uint8_t ring[];   // [depth][h | dy | dh], weights
+    const int W = a.W, G = W * 32, d = a.d, i = threadIdx.x, depth = a.depth;
+    const bool layer = a.mean != nullptr, more = a.dh != nullptr, wf32 = a.wf32;
+    const uint32_t bytes = (uint32_t)d * sizeof(T), stage = bytes * (a.ring_dh ? 3 : 2);
+    int turn = 0;
+    const float inv = 1.f / (float)d;
+    const int64_t step = gridDim.x;
+    const int c0 = i * E, cj = G * E;   // this thread's first column, and from one word to the next
+    float2 dw[VPT][P], db[DB ? VPT : 1][P];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+        for (int k = 0; k < P; ++k) {
+            dw[j][k] = both(0.f);
+            if (DB) db[j][k] = both(0.f);
+        }
+    if (i == 0) {
+        for (int k = 0; k < depth; ++k) tc::mbar_init(&landed[k], 1);
+        gave_up = 0;
+    }
+    tc::fence_barrier_init();
+    __syncthreads();
+    pdl_wait();
+    pdl_launch_dependents();
+    auto request = [&](int64_t row, int k) {
+        uint8_t *to = ring + (size_t)k * stage;
+        tc::mbar_expect_tx(&landed[k], stage);
+        tc::bulk_load(to, static_cast<const T *>(a.h) + row * d, bytes, &landed[k]);
+        tc::bulk_load(to + bytes, static_cast<const T *>(a.dy) + row * d, bytes, &landed[k]);
+        if (a.ring_dh) tc::bulk_load(to + 2 * bytes, static_cast<const T *>(a.dh) + row * d, bytes, &landed[k]);
+        else if (more)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(static_cast<const T *>(a.dh) + row * d), "r"(bytes)
+                         : "memory");
+    };
+    int64_t r = blockIdx.x;
+    // depth - 1 rows ahead; the place of the row before this one is free when all
+    // threads have met in this one's sum (a single place: when they meet behind it)
+    const int ahead = depth > 1 ? depth - 1 : 1;
+    if (i == 0)
+        for (int k = 0; k < ahead; ++k)
+            if (r + k * step < a.T) request(r + k * step, k);
+    uint8_t *weights = ring + (size_t)depth * stage;
+    for (int c = i * 16; c < d * (wf32 ? 4 : (int)sizeof(T)); c += blockDim.x * 16)
+        *reinterpret_cast<uint4 *>(weights + c) = __ldg(reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(a.weight) + c));
+    __syncthreads();
+    // this thread's weights from column c on
+    auto weight = [&](int c, float2 (&o)[P]) {
+        if (wf32) {
+#pragma unroll
+            for (int q = 0; q < P; q += 2) {
+                const float4 f = *reinterpret_cast<const float4 *>(weights + 4 * (c + 2 * q));
+                o[q] = make_float2(f.x, f.y);
+                o[q + 1] = make_float2(f.z, f.w);
+            }
+        } else {
+            unpack<T>(*reinterpret_cast<const uint4 *>(weights + sizeof(T) * c), o);
+        }
+    };
+    float nm = layer && r < a.T ? a.mean[r] : 0.f, ns = r < a.T ? a.rstd[r] : 0.f;   // the next row's statistics
+    int k = 0;                 // ring position
+    uint32_t phase = 0;
+    for (; r < a.T; r += step) {
+        const float mean = nm, rstd = ns;
+        if (r + step < a.T) {
+            if (layer) nm = a.mean[r + step];
+            ns = a.rstd[r + step];
+        }
+        // a wait that runs out is reported; the pass goes on, so that its barriers end
+        if (!tc::mbar_try_wait(&landed[k], phase)) tc::wait_bar(&landed[k], phase, &gave_up, a.err);
+        const uint4 *h = reinterpret_cast<const uint4 *>(ring + (size_t)k * stage) + i;
+        const uint4 *dy = reinterpret_cast<const uint4 *>(ring + (size_t)k * stage + bytes) + i;
+        float2 sg = both(0.f), sz = both(0.f);   // sums of g and of g (h - mean)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = c0 + j * cj;
+            if (c >= d) continue;
+            float2 w[P], z[P], y[P];
+            weight(c, w);
+            unpack<T>(h[j * G], z);
+            unpack<T>(dy[j * G], y);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                const float2 zc = add2(z[q], both(-mean)), g = mul2(y[q], w[q]);
+                sg = add2(sg, g);
+                sz = fma2(g, zc, sz);
+                dw[j][q] = fma2(mul2(y[q], both(rstd)), zc, dw[j][q]);
+                if (DB) db[j][q] = add2(db[j][q], y[q]);
+            }
+        }
+        const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), red, turn, i >> 5, W, 1);
+        if (depth > 1 && i == 0 && r + ahead * step < a.T) request(r + ahead * step, k == 0 ? depth - 1 : k - 1);
+        // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
+        const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
+        const uint4 *dh = more ? (a.ring_dh ? dy + bytes / 16 : reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dh) + r * d) + i)
+                               : nullptr;
+        uint4 *dx = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + r * d) + i;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int c = c0 + j * cj;
+            if (c >= d) continue;
+            float2 w[P], z[P], y[P];
+            weight(c, w);
+            unpack<T>(h[j * G], z);
+            unpack<T>(dy[j * G], y);
+#pragma unroll
+            for (int q = 0; q < P; ++q)
+                z[q] = fma2(add2(z[q], both(-mean)), both(c2), fma2(mul2(y[q], w[q]), both(rstd), both(c1)));
+            if (more) {
+                unpack<T>(dh[j * G], y);
+#pragma unroll
+                for (int q = 0; q < P; ++q) z[q] = add2(z[q], y[q]);
+            }
+            dx[j * G] = pack<T>(z);
+        }
+        if (depth == 1) {
+            __syncthreads();
+            if (i == 0 && r + step < a.T) request(r + step, 0);
+        }
+        if (++k == depth) {
+            k = 0;
+            phase ^= 1;
+        }
+    }
+    if (!a.part) return;
+    float *out = a.part + (int64_t)blockIdx.x * 2 * d;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int c = c0 + j * cj;
+        if (c >= d) continue;
+#pragma unroll
+        for (int q = 0; q < P; q += 2) {
+            const float2 u = dw[j][q], v = dw[j][q + 1];
+            *reinterpret_cast<float4 *>(out + c + 2 * q) = make_float4(u.x, u.y, v.x, v.y);
+            if constexpr (DB) {
+                const float2 x = db[j][q], y = db[j][q + 1];
+                *reinterpret_cast<float4 *>(out + d + c + 2 * q) = make_float4(x.x, x.y, y.x, y.y);
+            }
+        }
     }
 }
 
@@ -912,15 +1033,15 @@ auto fwd_kernel(const Spread &s) -> void (*)(NormFwd) {
 template <typename T, bool DB>
 auto bwd_words(const Spread &s) -> void (*)(NormBwd) {
     if (s.shift) {
-        if (s.vpt == 1) return s.W <= 8 ? norm_bwd_kernel<T, 1, true, DB, 256> : norm_bwd_kernel<T, 1, true, DB, 512>;
-        return s.W <= 8 ? norm_bwd_kernel<T, 2, true, DB, 256> : norm_bwd_kernel<T, 2, true, DB, 512>;
+        if (s.vpt == 1) return s.W <= 8 ? norm_bwd_shift_kernel<T, 1, DB, 256> : norm_bwd_shift_kernel<T, 1, DB, 512>;
+        return s.W <= 8 ? norm_bwd_shift_kernel<T, 2, DB, 256> : norm_bwd_shift_kernel<T, 2, DB, 512>;
     }
     if (s.vpt == 1) return norm_bwd_ring_kernel<T, 1, DB>;
     if (s.vpt == 2) return norm_bwd_ring_kernel<T, 2, DB>;
     if constexpr (!DB)
         if (s.vpt == 3) return norm_bwd_ring_kernel<T, 3, false>;
-    if (s.vpt == 4) return norm_bwd_kernel<T, 4, false, DB, 512>;
-    if constexpr (sizeof(T) == 4) return norm_bwd_kernel<T, 8, false, DB, 512>;
+    if (s.vpt == 4) return norm_bwd_wide_kernel<T, 4, DB>;
+    if constexpr (sizeof(T) == 4) return norm_bwd_wide_kernel<T, 8, DB>;
     return nullptr;
 }
 template <typename T>
@@ -928,14 +1049,22 @@ auto bwd_kernel(const Spread &s, bool db) -> void (*)(NormBwd) {
     if (s.vpt == 0) return norm_bwd_general_kernel<T>;
     return db ? bwd_words<T, true>(s) : bwd_words<T, false>(s);
 }
+size_t weight_bytes(const NormBwd &a, size_t row) { return a.wf32 ? sizeof(float) * (size_t)a.d : row; }
+// The ring of norm_bwd_wide_kernel: its rows, and whether dh's are among them.
+void wide_ring(NormBwd &a, size_t row) {
+    const size_t space = kWideSmem - weight_bytes(a, row);   // (weights and two tensors' rows: 192 KB at most)
+    a.ring_dh = a.dh && 2 * 3 * row <= space;
+    a.depth = (int)std::min<size_t>(kWideRows, space / ((a.ring_dh ? 3 : 2) * row));
+}
 // Dynamic shared memory of that kernel: the columns' sums of a block's groups,
 // or the ring (and the weights after it), whose memory the groups' sums take when
 // it is drained (4 * 2 * 16 bits a column and group at least, the sums 2 * 32).
-size_t bwd_smem(const Spread &s, int d, int elem, bool more) {
-    const size_t sums = s.groups > 1 || s.vpt == 0 ? 2 * sizeof(float) * (size_t)d : 0;
-    if (s.vpt == 0 || s.shift || s.vpt > 3) return sums;
-    const size_t weights = s.vpt == 3 ? sizeof(float) * (size_t)d : 0;
-    return std::max(sums, (size_t)s.groups * kRing * (more ? 3 : 2) * (size_t)d * elem + weights);
+size_t bwd_smem(const Spread &s, const NormBwd &a, size_t row) {
+    const size_t d = (size_t)a.d, sums = s.groups > 1 || s.vpt == 0 ? 2 * sizeof(float) * d : 0;
+    if (s.vpt == 0 || s.shift) return sums;
+    if (s.vpt > 3) return (size_t)a.depth * (a.ring_dh ? 3 : 2) * row + weight_bytes(a, row);
+    const size_t weights = s.vpt == 3 ? sizeof(float) * d : 0;
+    return std::max(sums, (size_t)s.groups * kRing * (a.dh ? 3 : 2) * row + weights);
 }
 
 moe_status check(const moe_norm_config *c) {
@@ -1010,9 +1139,11 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     uint32_t *err = device_error_word();
     if (!err) return MOE_ERR_CUDA;
     float *part = params ? static_cast<float *>(ws) : nullptr;
-    const NormBwd a{h, weight, dy, dh, mean, rstd, dx, part, c->T, c->d, sp.W, sp.groups, c->w_dtype == MOE_F32,
-                    dbias != nullptr, err};
-    const size_t smem = bwd_smem(sp, c->d, elem_size(c->dtype), dh != nullptr);
+    NormBwd a{h, weight, dy, dh, mean, rstd, dx, part, c->T, c->d, sp.W, sp.groups, c->w_dtype == MOE_F32,
+              dbias != nullptr, err, 0, false};
+    const size_t row = (size_t)c->d * elem_size(c->dtype);
+    if (sp.vpt > 3) wide_ring(a, row);
+    const size_t smem = bwd_smem(sp, a, row);
     auto kern = c->dtype == MOE_BF16  ? bwd_kernel<__nv_bfloat16>(sp, dbias != nullptr)
                 : c->dtype == MOE_F16 ? bwd_kernel<__half>(sp, dbias != nullptr)
                                       : bwd_kernel<float>(sp, dbias != nullptr);

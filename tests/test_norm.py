@@ -273,6 +273,19 @@ def test_backward(case):
     check_backward(*case)
 
 
+# wide rows, several a block, with one to four of them in flight and dh's among them or not
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,dtype,w_dtype,T,d,use_dh,use_bias", [
+    ("layer", "f32", "f32", 450, 16384, True, True), ("rms", "f32", "f32", 451, 16384, False, False),
+    ("rms", "f32", "f32", 450, 11224, True, False), ("layer", "f32", "f32", 600, 8196, False, True),
+    ("layer", "bf16", "f32", 450, 16384, True, False), ("rms", "bf16", "bf16", 450, 13336, False, True),
+    ("layer", "f16", "f16", 750, 8200, True, True), ("rms", "bf16", "f32", 900, 8200, False, False),
+    ("rms", "f32", "f32", 750, 4100, True, True), ("layer", "f32", "f32", 149, 4100, False, False),
+])
+def test_backward_of_wide_rows(kind, dtype, w_dtype, T, d, use_dh, use_bias):
+    check_backward(kind, dtype, w_dtype, T, d, use_dh, use_bias)
+
+
 # widths whose rows in flight take 48 KB of shared memory exactly
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind,dtype,d,use_dh,use_bias", [
