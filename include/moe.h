@@ -1,6 +1,8 @@
 /*
  * moe.h -- C ABI of libmoe.so: the forward pass of a top-k routed
- * mixture-of-experts (MoE) SwiGLU FFN layer on an NVIDIA B200 (sm_100a).
+ * mixture-of-experts (MoE) SwiGLU FFN layer on an NVIDIA B200 (sm_100a), its
+ * training and 4-bit forms, and the operators of the decoder block around it:
+ * layer and RMS norm, the dense gated feed-forward block, 8-bit linear layers.
  *
  * The layer (one token row x of width d):
  *
@@ -35,7 +37,8 @@
  *    frees nothing and never synchronises the stream; all work is enqueued
  *    on `stream` (a cudaStream_t; NULL is the legacy default stream).
  *  - Element type of x, weights, act and y: bf16 (MOE_BF16) or fp32
- *    (MOE_F32), as cfg->dtype says.  Scores, gates and accumulators are
+ *    (MOE_F32), as cfg->dtype says (the operators around the layer: fp16,
+ *    MOE_F16, too).  Scores, gates and accumulators are
  *    fp32; ids and permutations are int32.
  *  - Arguments are validated on the host before anything is launched; an
  *    invalid call returns an error and enqueues nothing.  MOE_ERR_CUDA means
@@ -416,7 +419,8 @@ moe_status moe_quantize_fp8(const void *x, int32_t dtype, int64_t rows, int32_t 
  *   c[m, n] = sum_k a[m, k] a_scales[m, k / 128] b[n, k] b_scales[n / 128, k / 128]
  * a [M, K] with 1 x 128 blocks, b [N, K] with 128 x 128 blocks (as
  * moe_quantize_fp8 writes them); c MOE_BF16, MOE_F16 or MOE_F32.  Products and
- * sums are fp32, in a fixed order.  K a multiple of 16 and N of 8 (else
+ * sums are fp32, in a fixed order; a_scales b_scales is multiplied first, so a
+ * pair of blocks whose scales' product passes fp32's range gives inf or NaN.  K a multiple of 16 and N of 8 (else
  * MOE_ERR_UNSUPPORTED); a, b and c 16-byte aligned; M = 0 is allowed. */
 moe_status moe_gemm_fp8(int64_t M, int32_t N, int32_t K, const uint8_t *a, const float *a_scales,
                         const uint8_t *b, const float *b_scales, void *c, int32_t c_dtype,

@@ -1,4 +1,5 @@
-"""B200-native forward pass of a top-k routed mixture-of-experts SwiGLU FFN layer.
+"""B200-native forward pass of a top-k routed mixture-of-experts SwiGLU FFN layer, its training pass,
+and the operators of the decoder block around it.
 
 The compute lives in ``libmoe.so`` (hand-written CUDA for sm_100a behind a C
 ABI, declared in ``include/moe.h``).  This package is its thin Python binding

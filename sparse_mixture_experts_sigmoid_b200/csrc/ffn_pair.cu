@@ -22,6 +22,13 @@
 // reduction runs over the tokens); the tensor map's boxes differ, the bytes of
 // the operand are never moved or transposed in memory.
 //
+// Measured: T = 4096, d = 2048, h = 5632 bf16: GATED with u and v kept 132 us (1435
+// TFLOP/s), down 66 (1438), DGATED 88 (1072; 276 MB of kept values and gradients
+// pass beside the operands), dx and the weights' gradients 377 (1253, the power
+// cap's rate); T = d = 4096, h = 14336 both forward products 1080 (1336).  256 x 256
+// tiles: with every pair at work L2 feeds a K block in 0.43 us where its MMAs take
+// 0.27, and 128-column tiles take the MMAs nearly as long (440 cycles, not 256).
+//
 // Every mbarrier wait is bounded as in the grouped kernels.
 #include <algorithm>
 

