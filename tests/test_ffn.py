@@ -329,3 +329,18 @@ def test_captured_replayed_and_on_two_streams(T):
         torch.cuda.synchronize()
         for k in ref:
             assert torch.equal(out[k], ref[k]), k
+
+
+@pytest.mark.gpu
+def test_offsets_past_32_bits():
+    """Activations of more than 2^31 elements.  dy is zero but in the last rows, so the weights' gradients are theirs."""
+    T, d, h, last = 2 ** 31 // 8192 + 500, 64, 8192, 300
+    v = make(T, d, h, "bf16")
+    v["dy"][:-last] = 0
+    got = run(B.ffn_config(T, d, h, act="silu"), v)
+    end = {k: t[-last:] if k in ("x", "dy") else t for k, t in v.items()}
+    half = torch.finfo(torch.bfloat16).eps / 2
+    out, tol = reference(end, "silu", half)
+    assert not got["dx"][:-last].any() and B.device_status() == 0
+    for k in ("y",) + GRADS:
+        check(k, got[k][-last:] if k in ("y", "dx") else got[k], out[k], tol[k], half)

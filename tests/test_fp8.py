@@ -264,3 +264,24 @@ def test_captured_replayed_and_on_another_stream(M):
     x.mul_(-2)
     graph.replay()
     assert torch.equal(y, want * -2)   # a power of two: the same codes under twice the scales
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("br", [1, 128])
+def test_quantiser_s_offsets_past_32_bits(br):
+    cols, last = 16384, 128
+    rows = 2 ** 31 // cols + 10 * last
+    x = torch.empty(rows, cols, device="cuda", dtype=torch.bfloat16).normal_(generator=torch.Generator(device="cuda").manual_seed(1))
+    q, s = B.quantize_fp8(x, br)
+    q1, s1 = B.quantize_fp8(x[-last:].contiguous(), br)
+    assert torch.equal(q[-last:].view(torch.uint8), q1.view(torch.uint8)) and torch.equal(s[-s1.shape[0]:], s1)
+
+
+@pytest.mark.gpu
+def test_product_s_offsets_past_32_bits():
+    M, N, K, last = 2 ** 31 // 8192 + 777, 8192, 144, 300
+    aq, sa, bq, sb = operands(M, N, K)
+    y = B.gemm_fp8(aq, sa, bq, sb)
+    for rows in (slice(0, last), slice(M - last, M)):
+        check(y[rows], aq[rows], sa[rows], bq, sb, "bf16")
+    assert B.device_status() == 0

@@ -391,3 +391,28 @@ def test_captured_and_on_another_stream():
     torch.cuda.synchronize()
     for a, b in zip([t.clone() for t in out], step()):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [16384, 16381])
+def test_offsets_past_32_bits(d):
+    """Tensors of more than 2^31 elements: the last rows are what a call on them alone gives, and only they have a
+    gradient to add to the weight's."""
+    T, last = 2 ** 31 // d + 1000, 37
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, d, generator=g, device="cuda", dtype=torch.bfloat16)
+    w = torch.randn(d, generator=g, device="cuda").to(torch.bfloat16)
+    dy = torch.zeros(T, d, device="cuda", dtype=torch.bfloat16)
+    dy[-last:] = torch.randn(last, d, generator=g, device="cuda").to(torch.bfloat16)
+    end = x[-last:].clone(), dy[-last:].clone()
+    cfg, few = B.norm_config(T, d), B.norm_config(last, d)
+    y1, _, m1, r1 = B.norm_forward(few, end[0], w, want_stats=True)
+    dx1, dw1, _ = B.norm_backward(few, end[0], w, m1, r1, end[1])
+    _, _, m, r = B.norm_forward(cfg, x, w, want_stats=True, y=(y := torch.empty_like(x)))
+    assert torch.equal(m[-last:], m1) and torch.equal(r[-last:], r1) and torch.equal(y[-last:], y1)
+    del y
+    dx, dw, _ = B.norm_backward(cfg, x, w, m, r, dy, dx=dy)   # in place
+    assert torch.equal(dx[-last:], dx1) and not dx[:-last].any()
+    # the same terms, added over other blocks
+    xh = (end[0].float() - m1[:, None]) * r1[:, None]
+    assert ((dw - dw1).abs() <= F32 * (end[1].float() * xh).abs().sum(0)).all()
