@@ -420,7 +420,8 @@ moe_status moe_quantize_fp8(const void *x, int32_t dtype, int64_t rows, int32_t 
  * a [M, K] with 1 x 128 blocks, b [N, K] with 128 x 128 blocks (as
  * moe_quantize_fp8 writes them); c MOE_BF16, MOE_F16 or MOE_F32.  Products and
  * sums are fp32, in a fixed order; a_scales b_scales is multiplied first, so a
- * pair of blocks whose scales' product passes fp32's range gives inf or NaN.  K a multiple of 16 and N of 8 (else
+ * pair of blocks whose scales' product passes fp32's range gives inf or NaN.
+ * c overlaps none of the others.  K a multiple of 16 and N of 8 (else
  * MOE_ERR_UNSUPPORTED); a, b and c 16-byte aligned; M = 0 is allowed. */
 moe_status moe_gemm_fp8(int64_t M, int32_t N, int32_t K, const uint8_t *a, const float *a_scales,
                         const uint8_t *b, const float *b_scales, void *c, int32_t c_dtype,
@@ -507,7 +508,7 @@ moe_status moe_ffn_workspace_size(const moe_ffn_config *cfg, int32_t train, size
 
 /* x [T, d]; w_gate, w_up [h, d]; w_down [d, h]; y [T, d] out; all 16-byte
  * aligned (else MOE_ERR_INVALID_ARG).  ws: at least moe_ffn_workspace_size
- * bytes, 256-byte aligned.  moe_ffn_forward_train gives the same y and keeps
+ * bytes, 256-byte aligned.  y overlaps none of the others.  moe_ffn_forward_train gives the same y and keeps
  * in ws what moe_ffn_backward needs (u, v and a). */
 moe_status moe_ffn_forward(const moe_ffn_config *cfg, const void *x, const void *w_gate,
                            const void *w_up, const void *w_down, void *y, void *ws, size_t ws_bytes,
@@ -520,7 +521,8 @@ moe_status moe_ffn_forward_train(const moe_ffn_config *cfg, const void *x, const
  * the same workspace, which stays as the forward left it (the call may be
  * repeated, with another dy).  dx [T, d], dw_gate, dw_up [h, d], dw_down [d, h]
  * are overwritten; each may be NULL (not computed).  x is read only for dw_gate
- * and dw_up, the weights only for dx and for them.  Every sum has a fixed
+ * and dw_up, the weights only for dx and for them.  No output overlaps an input
+ * or another output.  Every sum has a fixed
  * order: repeated calls give identical bits.  T = 0 writes zero weight
  * gradients. */
 moe_status moe_ffn_backward(const moe_ffn_config *cfg, const void *x, const void *w_gate,

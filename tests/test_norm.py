@@ -416,3 +416,24 @@ def test_offsets_past_32_bits(d):
     # the same terms, added over other blocks
     xh = (end[0].float() - m1[:, None]) * r1[:, None]
     assert ((dw - dw1).abs() <= F32 * (end[1].float() * xh).abs().sum(0)).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype,d", [("bf16", 64), ("f16", 333), ("f32", 1411), ("bf16", 5001), ("bf16", 8200), ("f32", 16384),
+                                     ("bf16", 16383)])
+@pytest.mark.parametrize("shift", [0, 1])   # on a 16-byte boundary, and one element past it
+def test_nothing_outside_the_outputs_is_written(dtype, d, shift):
+    T, dt = 301, TORCH[dtype]
+    v = {k: cuda(t) for k, t in make(T, d, dtype, dtype, d).items()}
+    cfg = B.norm_config(T, d, dtype=dtype)
+
+    def guarded():
+        raw = torch.full((T * d + 64 + shift,), 7.0, dtype=dt, device="cuda")
+        return raw, raw[32 + shift:32 + shift + T * d].view(T, d)
+
+    raws, (y, h, dx) = zip(*(guarded() for _ in range(3)))
+    _, _, mean, rstd = B.norm_forward(cfg, v["x"], v["weight"], v["bias"], v["residual"], y=y, h=h, want_stats=True)
+    B.norm_backward(cfg, h, v["weight"], mean, rstd, v["dy"], dh=v["dh"], dx=dx, want_bias=True)
+    for raw, out in zip(raws, (y, h, dx)):
+        assert (raw[:32 + shift] == 7).all() and (raw[32 + shift + T * d:] == 7).all() and out.isfinite().all()
+    assert torch.equal(h, (v["x"].float() + v["residual"].float()).to(dt))
