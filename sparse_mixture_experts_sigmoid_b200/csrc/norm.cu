@@ -660,17 +660,23 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
 
 // The backward pass of wide rows (whole words, more than two a thread): a block per
 // row, and a ring of as many rows as fit into shared memory (one to four), filled as
-// above; dh's rows are in it only if two rows fit with them (else they are fetched
-// into L2 meanwhile).  The weights stand beside it as they are.  Only the gradients'
-// sums stay in registers: the second pass reads the row from shared memory again.
+// above; dh's rows are in it only if two rows (held ones, see below: three) fit with
+// them (else they are fetched into L2 meanwhile).  The weights stand beside it as they are.  Three words a thread
+// are held between the passes where the registers allow it (wide_hold), dh's too: the
+// row's place in the ring is free after the first.  Of others only the gradients' sums
+// stay, and the second pass takes the row from shared memory again (held, with the
+// place freed after the second: T = 2516, d = 13336 bf16 50 us against 45).
 // Read from global memory twice, with no row in flight, T = 2989, d = 11224 in fp32
 // took 258 us and T = 2516, d = 13336 in bf16 90.
 constexpr int kWideSmem = 224 * 1024;
 constexpr int kWideRows = 4;
 
+constexpr bool wide_hold(int vpt, bool db, int elem) { return vpt == 3 && (!db || elem == 4); }
+
 template <typename T, int VPT, bool DB>
 __global__ void __launch_bounds__(512, 1) norm_bwd_wide_kernel(NormBwd a) {
     constexpr int E = kElems<T>, P = kPairs<T>;
+    constexpr bool HOLD = wide_hold(VPT, DB, sizeof(T));
     __shared__ float2 red[32];
     __shared__ uint64_t landed[kWideRows];
     __shared__ int gave_up;
@@ -709,9 +715,10 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_wide_kernel(NormBwd a) {
                          : "memory");
     };
     int64_t r = blockIdx.x;
-    // depth - 1 rows ahead; the place of the row before this one is free when all
-    // threads have met in this one's sum (a single place: when they meet behind it)
-    const int ahead = depth > 1 ? depth - 1 : 1;
+    // held rows: depth rows ahead, the place of a row is free when all threads have met
+    // in its sum; else that of the row before it (a single place: when they meet behind
+    // the row), depth - 1 rows ahead
+    const int ahead = HOLD || depth == 1 ? depth : depth - 1;
     if (i == 0)
         for (int k = 0; k < ahead; ++k)
             if (r + k * step < a.T) request(r + k * step, k);
@@ -745,50 +752,66 @@ __global__ void __launch_bounds__(512, 1) norm_bwd_wide_kernel(NormBwd a) {
         if (!tc::mbar_try_wait(&landed[k], phase)) tc::wait_bar(&landed[k], phase, &gave_up, a.err);
         const uint4 *h = reinterpret_cast<const uint4 *>(ring + (size_t)k * stage) + i;
         const uint4 *dy = reinterpret_cast<const uint4 *>(ring + (size_t)k * stage + bytes) + i;
-        float2 sg = both(0.f), sz = both(0.f);   // sums of g and of g (h - mean)
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int c = c0 + j * cj;
-            if (c >= d) continue;
-            float2 w[P], z[P], y[P];
-            weight(c, w);
+        // h - mean and g of word j
+        auto word = [&](int j, float2 (&z)[P], float2 (&g)[P], float2 (&y)[P]) {
+            float2 w[P];
+            weight(c0 + j * cj, w);
             unpack<T>(h[j * G], z);
             unpack<T>(dy[j * G], y);
 #pragma unroll
             for (int q = 0; q < P; ++q) {
-                const float2 zc = add2(z[q], both(-mean)), g = mul2(y[q], w[q]);
-                sg = add2(sg, g);
-                sz = fma2(g, zc, sz);
-                dw[j][q] = fma2(mul2(y[q], both(rstd)), zc, dw[j][q]);
+                z[q] = add2(z[q], both(-mean));
+                g[q] = mul2(y[q], w[q]);
+            }
+        };
+        float2 z[HOLD ? VPT : 1][P], g[HOLD ? VPT : 1][P];
+        float2 sg = both(0.f), sz = both(0.f);   // sums of g and of g (h - mean)
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            constexpr bool kHold = HOLD;
+            const int o = kHold ? j : 0;
+            if (c0 + j * cj >= d) continue;
+            float2 y[P];
+            word(j, z[o], g[o], y);
+#pragma unroll
+            for (int q = 0; q < P; ++q) {
+                sg = add2(sg, g[o][q]);
+                sz = fma2(g[o][q], z[o][q], sz);
+                dw[j][q] = fma2(mul2(y[q], both(rstd)), z[o][q], dw[j][q]);
                 if (DB) db[j][q] = add2(db[j][q], y[q]);
             }
         }
-        const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), red, turn, i >> 5, W, 1);
-        if (depth > 1 && i == 0 && r + ahead * step < a.T) request(r + ahead * step, k == 0 ? depth - 1 : k - 1);
-        // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
-        const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
+        uint4 held_dh[HOLD ? VPT : 1];
         const uint4 *dh = more ? (a.ring_dh ? dy + bytes / 16 : reinterpret_cast<const uint4 *>(static_cast<const T *>(a.dh) + r * d) + i)
                                : nullptr;
+        if constexpr (HOLD) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+                if (more && c0 + j * cj < d) held_dh[j] = dh[j * G];
+        }
+        const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), red, turn, i >> 5, W, 1);
+        if ((HOLD || depth > 1) && i == 0 && r + ahead * step < a.T)
+            request(r + ahead * step, HOLD ? k : k == 0 ? depth - 1 : k - 1);
+        // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
+        const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
         uint4 *dx = reinterpret_cast<uint4 *>(static_cast<T *>(a.dx) + r * d) + i;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int c = c0 + j * cj;
-            if (c >= d) continue;
-            float2 w[P], z[P], y[P];
-            weight(c, w);
-            unpack<T>(h[j * G], z);
-            unpack<T>(dy[j * G], y);
+            constexpr bool kHold = HOLD;
+            const int o = kHold ? j : 0;
+            if (c0 + j * cj >= d) continue;
+            float2 y[P];
+            if constexpr (!HOLD) word(j, z[0], g[0], y);
 #pragma unroll
-            for (int q = 0; q < P; ++q)
-                z[q] = fma2(add2(z[q], both(-mean)), both(c2), fma2(mul2(y[q], w[q]), both(rstd), both(c1)));
+            for (int q = 0; q < P; ++q) z[o][q] = fma2(z[o][q], both(c2), fma2(g[o][q], both(rstd), both(c1)));
             if (more) {
-                unpack<T>(dh[j * G], y);
+                unpack<T>(HOLD ? held_dh[o] : dh[j * G], y);
 #pragma unroll
-                for (int q = 0; q < P; ++q) z[q] = add2(z[q], y[q]);
+                for (int q = 0; q < P; ++q) z[o][q] = add2(z[o][q], y[q]);
             }
-            dx[j * G] = pack<T>(z);
+            dx[j * G] = pack<T>(z[o]);
         }
-        if (depth == 1) {
+        if (!HOLD && depth == 1) {
             __syncthreads();
             if (i == 0 && r + step < a.T) request(r + step, 0);
         }
@@ -960,20 +983,21 @@ __global__ void __launch_bounds__(32 * kParamWarps) norm_param_kernel(const floa
 // How a row is spread: VPT words per thread, W warps per row, `groups` rows
 // per block; vpt = 0 is the general kernel.  Of one, two and (`three`, whole words) three
 // words a thread, the one that leaves the fewest words of its warps idle, and
-// of those the one with the fewest warps: one warp needs no barrier.  Four
-// (eight) words where more than 16 warps would be needed.
+// of those the one with the fewest warps: one warp needs no barrier.  Where more than
+// 16 warps would be needed, four words (eight), or three (`wide_three`: the backward
+// pass is bound by its warps' issue there; T = 4096, d = 10000 bf16 60 us with four).
 struct Spread {
     int vpt, W, groups;
     bool shift;
 };
-Spread spread(int d, int elems, bool aligned, bool three) {
+Spread spread(int d, int elems, bool aligned, bool three, bool wide_three) {
     const bool shift = d % elems != 0;
     const int words = (d + (shift ? elems - 1 : 0) + elems - 1) / elems;
     const int most = (shift ? 2 : (elems == 4 ? 8 : 4)) * 32 * kMaxWarps;
     if (!aligned || words > most) return Spread{0, kGenThreads / 32, 1, false};
     Spread s{0, 0, 0, shift};
     if (words > 64 * kMaxWarps) {
-        s.vpt = words <= 128 * kMaxWarps ? 4 : 8;
+        s.vpt = wide_three && words <= 96 * kMaxWarps ? 3 : words <= 128 * kMaxWarps ? 4 : 8;
         s.W = (words + 32 * s.vpt - 1) / (32 * s.vpt);
     } else {
         for (int v = 1; v <= (three && !shift && words <= 96 ? 3 : 2); ++v) {
@@ -987,6 +1011,8 @@ Spread spread(int d, int elems, bool aligned, bool three) {
     s.groups = std::max(1, 8 / s.W);
     return s;
 }
+// Rows of norm_bwd_wide_kernel.
+bool wide(const Spread &s) { return s.vpt > 2 && s.W > 8; }
 // Blocks for T rows, `most` at most: the rows in flight a multiple of eight when
 // rows are shifted (see Row).
 int blocks_for(const Spread &s, int64_t T, int most) {
@@ -1044,7 +1070,8 @@ auto bwd_words(const Spread &s) -> void (*)(NormBwd) {
     if (s.vpt == 1) return norm_bwd_ring_kernel<T, 1, DB>;
     if (s.vpt == 2) return norm_bwd_ring_kernel<T, 2, DB>;
     if constexpr (!DB)
-        if (s.vpt == 3) return norm_bwd_ring_kernel<T, 3, false>;
+        if (!wide(s)) return norm_bwd_ring_kernel<T, 3, false>;
+    if (s.vpt == 3) return norm_bwd_wide_kernel<T, 3, DB>;
     if (s.vpt == 4) return norm_bwd_wide_kernel<T, 4, DB>;
     if constexpr (sizeof(T) == 4) return norm_bwd_wide_kernel<T, 8, DB>;
     return nullptr;
@@ -1056,9 +1083,9 @@ auto bwd_kernel(const Spread &s, bool db) -> void (*)(NormBwd) {
 }
 size_t weight_bytes(const NormBwd &a, size_t row) { return a.wf32 ? sizeof(float) * (size_t)a.d : row; }
 // The ring of norm_bwd_wide_kernel: its rows, and whether dh's are among them.
-void wide_ring(NormBwd &a, size_t row) {
+void wide_ring(NormBwd &a, size_t row, bool hold) {
     const size_t space = kWideSmem - weight_bytes(a, row);   // (weights and two tensors' rows: 192 KB at most)
-    a.ring_dh = a.dh && 2 * 3 * row <= space;
+    a.ring_dh = a.dh && (hold ? 3 : 2) * 3 * row <= space;
     a.depth = (int)std::min<size_t>(kWideRows, space / ((a.ring_dh ? 3 : 2) * row));
 }
 // Dynamic shared memory of that kernel: the columns' sums of a block's groups,
@@ -1067,7 +1094,7 @@ void wide_ring(NormBwd &a, size_t row) {
 size_t bwd_smem(const Spread &s, const NormBwd &a, size_t row) {
     const size_t d = (size_t)a.d, sums = s.groups > 1 || s.vpt == 0 ? 2 * sizeof(float) * d : 0;
     if (s.vpt == 0 || s.shift) return sums;
-    if (s.vpt > 3) return (size_t)a.depth * (a.ring_dh ? 3 : 2) * row + weight_bytes(a, row);
+    if (wide(s)) return (size_t)a.depth * (a.ring_dh ? 3 : 2) * row + weight_bytes(a, row);
     const size_t weights = s.vpt == 3 ? sizeof(float) * d : 0;
     return std::max(sums, (size_t)s.groups * kRing * (a.dh ? 3 : 2) * row + weights);
 }
@@ -1109,7 +1136,7 @@ moe_status moe_norm_forward(const moe_norm_config *c, const void *x, const void 
     const int E = 16 / elem_size(c->dtype);
     const bool aligned = aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(bias) && aligned16(h) &&
                          aligned16(y);
-    const Spread sp = spread(c->d, E, aligned, true);
+    const Spread sp = spread(c->d, E, aligned, true, false);
     const NormFwd a{x, residual, weight, bias, h, y, mean, rstd, c->T, c->d, sp.W, sp.groups,
                     c->kind == MOE_NORM_LAYER, c->w_dtype == MOE_F32, c->eps};
     const int threads = sp.groups * sp.W * 32;
@@ -1137,7 +1164,7 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     const bool params = dweight || dbias;
     const int E = 16 / elem_size(c->dtype);
     const bool aligned = aligned16(h) && aligned16(weight) && aligned16(dy) && aligned16(dh) && aligned16(dx);
-    const Spread sp = spread(c->d, E, aligned, dbias == nullptr);
+    const Spread sp = spread(c->d, E, aligned, dbias == nullptr, true);
     if (params && (!ws || ws_bytes < part_rows(*c) * 2 * (size_t)c->d * sizeof(float) ||
                    (reinterpret_cast<uintptr_t>(ws) & 255)))
         return MOE_ERR_WORKSPACE;
@@ -1147,7 +1174,7 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     NormBwd a{h, weight, dy, dh, mean, rstd, dx, part, c->T, c->d, sp.W, sp.groups, c->w_dtype == MOE_F32,
               dbias != nullptr, err, 0, false};
     const size_t row = (size_t)c->d * elem_size(c->dtype);
-    if (sp.vpt > 3) wide_ring(a, row);
+    if (wide(sp)) wide_ring(a, row, wide_hold(sp.vpt, dbias != nullptr, elem_size(c->dtype)));
     const size_t smem = bwd_smem(sp, a, row);
     auto kern = c->dtype == MOE_BF16  ? bwd_kernel<__nv_bfloat16>(sp, dbias != nullptr)
                 : c->dtype == MOE_F16 ? bwd_kernel<__half>(sp, dbias != nullptr)
