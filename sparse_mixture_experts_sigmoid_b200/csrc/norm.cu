@@ -661,11 +661,12 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
 // The backward pass of wide rows (whole words, more than two a thread): a block per
 // row, and a ring of as many rows as fit into shared memory (one to four), filled as
 // above; dh's rows are in it only if two rows (held ones, see below: three) fit with
-// them (else they are fetched into L2 meanwhile).  The weights stand beside it as they are.  Three words a thread
-// are held between the passes where the registers allow it (wide_hold), dh's too: the
-// row's place in the ring is free after the first.  Of others only the gradients' sums
-// stay, and the second pass takes the row from shared memory again (held, with the
-// place freed after the second: T = 2516, d = 13336 bf16 50 us against 45).
+// them, else they are fetched into L2 meanwhile.  The weights stand beside it as they
+// are.  Three words a thread are held between the passes where the registers allow it
+// (wide_hold), dh's too: the row's place in the ring is free after the first.  Of
+// others only the gradients' sums stay, and the second pass takes the row from shared
+// memory again (held, with the place freed after the second: T = 2516, d = 13336 bf16
+// 50 us against 45).
 // Read from global memory twice, with no row in flight, T = 2989, d = 11224 in fp32
 // took 258 us and T = 2516, d = 13336 in bf16 90.
 constexpr int kWideSmem = 224 * 1024;
