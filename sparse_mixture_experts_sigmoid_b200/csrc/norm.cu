@@ -188,10 +188,12 @@ __device__ __forceinline__ float2 shfl_of(float2 v, int o) {
 // warp in it), in a fixed order.  `slot` is the group's buffer of 2 x 16 values
 // of this type, used in turn: a warp writes half `turn` again only after a
 // barrier that every warp reaches after it has read that half.
+// A group that is part of a warp has `lanes` threads (a power of two, W = 1).
 template <typename V>
-__device__ __forceinline__ V group_sum(V v, V *slot, int &turn, int w, int W, int bar) {
+__device__ __forceinline__ V group_sum(V v, V *slot, int &turn, int w, int W, int bar, int lanes = 32) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v = add_of(v, shfl_of(v, o));
+    for (int o = 16; o > 0; o >>= 1)
+        if (o < lanes) v = add_of(v, shfl_of(v, o));
     if (W == 1) return v;
     V *s = slot + turn;
     turn ^= 16;
@@ -209,7 +211,7 @@ struct NormFwd {
     void *h, *y;
     float *mean, *rstd;
     int64_t T;
-    int d, W, groups;       // warps per row, rows in flight per block
+    int d, W, lanes, groups;   // warps and threads per row, rows in flight per block
     bool layer, wf32;
     float eps;
 };
@@ -219,18 +221,23 @@ struct NormFwd {
 template <int VPT, bool SHIFT, int THREADS>
 constexpr int kFwdBlocks = THREADS == 256 && !SHIFT ? (VPT <= 2 ? 3 : 2) : 1;
 
-template <typename T, int VPT, bool SHIFT, int THREADS>
+// PART: a group is part of a warp.  (An instance of its own: the same tests in the
+// others took 2047 x 1411 fp32 from 8.9 to 11.2 us.)
+template <typename T, int VPT, bool SHIFT, int THREADS, bool PART = false>
 __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm_fwd_kernel(NormFwd a) {
     constexpr int E = kElems<T>, P = kPairs<T>;
     using R = Row<T, VPT, SHIFT>;
     __shared__ float red[8 * 32];
-    const int W = a.W, G = W * 32, d = a.d;
+    const int W = PART ? 1 : a.W, G = PART ? a.lanes : W * 32, d = a.d;
     const int group = threadIdx.x / G, i = threadIdx.x - group * G, w = i >> 5;
-    float *slot = red + 32 * group;
+    float *slot = red + (PART ? 0 : 32 * group);
     int turn = 0;
     const float df = (float)d, inv = 1.f / df;
     const int64_t step = (int64_t)gridDim.x * a.groups;
     int64_t r = (int64_t)blockIdx.x * a.groups + group;
+    // the rows of one warp's groups are consecutive: all its lanes stay until the first
+    // of them is past the end
+    const int sub = PART ? group & (32 / G - 1) : 0;
     const int shift = SHIFT ? (int)(r * d % E) : 0;
     const bool add = a.residual != nullptr, bias = a.bias != nullptr, wf32 = a.wf32;
     const T *x = static_cast<const T *>(a.x), *res = static_cast<const T *>(a.residual);
@@ -249,11 +256,16 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
         }
     }
     R nx, nr;
+    if constexpr (PART) {
+        nx = R{};
+        nr = R{};
+    }
     if (r < a.T) {
         nx.load(x + o, i, G, d, shift);
         if (add) nr.load(res + o, i, G, d, shift);
     }
-    for (; r < a.T; r += step) {
+    for (; r - sub < a.T; r += step) {
+        const bool here = !PART || r < a.T;
         float2 c[VPT][P];
 #pragma unroll
         for (int j = 0; j < VPT; ++j) unpack<T>(nx.v[j], c[j]);
@@ -266,7 +278,7 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
                 for (int k = 0; k < P; ++k) c[j][k] = add2(c[j][k], z[k]);
                 const uint4 u = pack<T>(c[j]);
                 const int c0 = R::first(i, G, j, shift);
-                store_word<T, SHIFT>(static_cast<T *>(a.h) + o + c0, c0, d, u);
+                if (here) store_word<T, SHIFT>(static_cast<T *>(a.h) + o + c0, c0, d, u);
                 unpack<T>(u, c[j]);   // the norm is of the rows as they are stored
             }
         }
@@ -282,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
                 for (int k = 0; k < P; ++k) s = add2(s, c[j][k]);
-            const float t = group_sum(s.x + s.y, slot, turn, w, W, 1 + group);
+            const float t = group_sum(s.x + s.y, slot, turn, w, W, 1 + group, PART ? G : 32);
             mean = t * inv;
             mean = fmaf(fmaf(-mean, df, t), inv, mean);   // the quotient t / d, rounded once
 #pragma unroll
@@ -305,8 +317,8 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
         for (int j = 0; j < VPT; ++j)
 #pragma unroll
             for (int k = 0; k < P; ++k) q = fma2(c[j][k], c[j][k], q);
-        const float rstd = rsqrtf(group_sum(q.x + q.y, slot, turn, w, W, 1 + group) * inv + a.eps);
-        if (i == 0) {
+        const float rstd = rsqrtf(group_sum(q.x + q.y, slot, turn, w, W, 1 + group, PART ? G : 32) * inv + a.eps);
+        if (i == 0 && here) {
             if (a.mean) a.mean[r] = mean;
             if (a.rstd) a.rstd[r] = rstd;
         }
@@ -328,7 +340,7 @@ __global__ void __launch_bounds__(THREADS, kFwdBlocks<VPT, SHIFT, THREADS>) norm
 #pragma unroll
                 for (int k = 0; k < P; ++k) c[j][k] = mul2(c[j][k], g[k]);
             }
-            store_word<T, SHIFT>(static_cast<T *>(a.y) + o + c0, c0, d, pack<T>(c[j]));
+            if (here) store_word<T, SHIFT>(static_cast<T *>(a.y) + o + c0, c0, d, pack<T>(c[j]));
         }
         o += jump;
     }
@@ -990,13 +1002,14 @@ __global__ void __launch_bounds__(32 * kParamWarps) norm_param_kernel(const floa
 struct Spread {
     int vpt, W, groups;
     bool shift;
+    int lanes;
 };
 Spread spread(int d, int elems, bool aligned, bool three, bool wide_three) {
     const bool shift = d % elems != 0;
     const int words = (d + (shift ? elems - 1 : 0) + elems - 1) / elems;
     const int most = (shift ? 2 : (elems == 4 ? 8 : 4)) * 32 * kMaxWarps;
-    if (!aligned || words > most) return Spread{0, kGenThreads / 32, 1, false};
-    Spread s{0, 0, 0, shift};
+    if (!aligned || words > most) return Spread{0, kGenThreads / 32, 1, false, kGenThreads};
+    Spread s{0, 0, 0, shift, 0};
     if (words > 64 * kMaxWarps) {
         s.vpt = wide_three && words <= 96 * kMaxWarps ? 3 : words <= 128 * kMaxWarps ? 4 : 8;
         s.W = (words + 32 * s.vpt - 1) / (32 * s.vpt);
@@ -1010,7 +1023,16 @@ Spread spread(int d, int elems, bool aligned, bool three, bool wide_three) {
         }
     }
     s.groups = std::max(1, 8 / s.W);
+    s.lanes = 32 * s.W;
     return s;
+}
+// Forward: rows of up to 16 words a part of a warp each (four lanes at least); a warp
+// each, 262144 x 64 bf16 took 42 us where parts take 20.
+void part_of_a_warp(Spread &s, int d, int elems) {
+    const int words = (d + (s.shift ? elems - 1 : 0) + elems - 1) / elems;
+    if (s.vpt != 1 || words > 16) return;
+    while (s.lanes > 4 && s.lanes / 2 >= words) s.lanes /= 2;
+    s.groups = 256 / s.lanes;
 }
 // Rows of norm_bwd_wide_kernel.
 bool wide(const Spread &s) { return s.vpt > 2 && s.W > 8; }
@@ -1047,6 +1069,7 @@ bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // or of up to 512 for rows of more than eight warps.
 template <typename T, bool SHIFT>
 auto fwd_words(const Spread &s) -> void (*)(NormFwd) {
+    if (s.lanes < 32) return norm_fwd_kernel<T, 1, SHIFT, 256, true>;
     if (s.vpt == 1) return s.W <= 8 ? norm_fwd_kernel<T, 1, SHIFT, 256> : norm_fwd_kernel<T, 1, SHIFT, 512>;
     if (s.vpt == 2) return s.W <= 8 ? norm_fwd_kernel<T, 2, SHIFT, 256> : norm_fwd_kernel<T, 2, SHIFT, 512>;
     if constexpr (!SHIFT)
@@ -1137,10 +1160,11 @@ moe_status moe_norm_forward(const moe_norm_config *c, const void *x, const void 
     const int E = 16 / elem_size(c->dtype);
     const bool aligned = aligned16(x) && aligned16(residual) && aligned16(weight) && aligned16(bias) && aligned16(h) &&
                          aligned16(y);
-    const Spread sp = spread(c->d, E, aligned, true, false);
-    const NormFwd a{x, residual, weight, bias, h, y, mean, rstd, c->T, c->d, sp.W, sp.groups,
+    Spread sp = spread(c->d, E, aligned, true, false);
+    part_of_a_warp(sp, c->d, E);
+    const NormFwd a{x, residual, weight, bias, h, y, mean, rstd, c->T, c->d, sp.W, sp.lanes, sp.groups,
                     c->kind == MOE_NORM_LAYER, c->w_dtype == MOE_F32, c->eps};
-    const int threads = sp.groups * sp.W * 32;
+    const int threads = sp.groups * sp.lanes;
     auto kern = c->dtype == MOE_BF16  ? fwd_kernel<__nv_bfloat16>(sp)
                 : c->dtype == MOE_F16 ? fwd_kernel<__half>(sp)
                                       : fwd_kernel<float>(sp);

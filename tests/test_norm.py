@@ -172,6 +172,34 @@ def test_forward(case):
     check_forward(*case)
 
 
+# rows that take part of a warp: from 4 to 16 lanes, the last warp's rows not all there, rows a warp of the grid takes again
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [
+    ("rms", "bf16", "bf16", 1021, 64, False, False), ("layer", "f16", "f32", 4099, 33, True, True),
+    ("layer", "f32", "f32", 777, 16, True, True), ("rms", "bf16", "f32", 20003, 128, True, False),
+    ("layer", "bf16", "bf16", 3, 100, False, True), ("rms", "f32", "f32", 1, 8, False, False),
+    ("layer", "f16", "f16", 30011, 9, False, True), ("rms", "f32", "f32", 12345, 61, True, False),
+    ("layer", "bf16", "bf16", 33333, 8, True, True), ("layer", "f32", "f32", 65, 64, True, False),
+], ids=lambda c: "-".join(map(str, c)))
+def test_forward_of_short_rows(case):
+    check_forward(*case)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("d", [8, 24, 33, 100])
+def test_short_rows_do_not_meet(d):
+    """An infinity or NaN in one row leaves its neighbours in the warp as they were."""
+    v = make(70, d, "bf16", "bf16", d)
+    cfg, w = B.norm_config(70, d), cuda(v["weight"])
+    y0, _, m0, r0 = B.norm_forward(cfg, cuda(v["x"]), w, want_stats=True)
+    x = cuda(v["x"])
+    x[5, 0], x[41, d - 1] = float("inf"), float("nan")
+    y, _, m, r = B.norm_forward(cfg, x, w, want_stats=True)
+    rest = [i for i in range(70) if i not in (5, 41)]
+    assert torch.equal(y[rest], y0[rest]) and torch.equal(m[rest], m0[rest]) and torch.equal(r[rest], r0[rest])
+    assert y[5].isnan().any() and y[41].isnan().all()
+
+
 @pytest.mark.gpu
 def test_forward_of_rows_far_from_zero():
     """The variance is summed about the mean: rows of mean 1000 and unit spread keep it."""
