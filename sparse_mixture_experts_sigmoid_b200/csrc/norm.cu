@@ -352,7 +352,7 @@ struct NormBwd {
     void *dx;
     float *part;            // [gridDim.x, 2, d]: dw then db of each block (nullptr: not wanted)
     int64_t T;
-    int d, W, groups;
+    int d, W, lanes, groups;
     bool wf32, want_db;
     uint32_t *err;
     int depth;              // norm_bwd_wide_kernel: rows in its ring, and whether dh's are among them
@@ -505,7 +505,9 @@ __global__ void __launch_bounds__(THREADS, 1) norm_bwd_shift_kernel(NormBwd a) {
 // HBM, 41 us at T = 8192, d = 2048 and 44 us at T = 30001, d = 640.
 constexpr int kRing = 4;
 
-template <typename T, int VPT, bool DB>
+// PART: a group is part of a warp; the rows of a warp's groups are consecutive, and
+// each copy brings those of all of them.
+template <typename T, int VPT, bool DB, bool PART = false>
 __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_bwd_ring_kernel(NormBwd a) {
     // three words a thread leave no registers for the weights: they stay in
     // shared memory, as fp32
@@ -515,12 +517,15 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
     __shared__ uint64_t landed[8][kRing];
     __shared__ int gave_up;
     extern __shared__ __align__(16) uint8_t ring[];   // [group][kRing][h | dy | dh]; then the columns' sums [2, d]
-    const int W = a.W, G = W * 32, d = a.d;
+    const int W = PART ? 1 : a.W, G = PART ? a.lanes : W * 32, d = a.d;
     const int group = threadIdx.x / G, i = threadIdx.x - group * G, wi = i >> 5;
+    // the rows that one ring holds at a time (`unit`: whose ring it is)
+    const int rows = PART ? 32 / G : 1, unit = PART ? threadIdx.x >> 5 : group, sub = PART ? group & (rows - 1) : 0;
+    const bool asks = PART ? (threadIdx.x & 31) == 0 : i == 0;
     const bool layer = a.mean != nullptr, more = a.dh != nullptr, wf32 = a.wf32;
-    const uint32_t bytes = (uint32_t)d * sizeof(T), stage = bytes * (more ? 3 : 2);
-    uint8_t *mine = ring + (size_t)group * kRing * stage;
-    float2 *slot = red + 32 * group;
+    const uint32_t bytes = (uint32_t)d * sizeof(T), each = rows * bytes, stage = each * (more ? 3 : 2);
+    uint8_t *mine = ring + (size_t)unit * kRing * stage;
+    float2 *slot = red + (PART ? 0 : 32 * group);
     int turn = 0;
     const float inv = 1.f / (float)d;
     const int64_t step = (int64_t)gridDim.x * a.groups;
@@ -535,26 +540,27 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
             dw[j][k] = both(0.f);
             if (DB) db[j][k] = both(0.f);
         }
-    if (i == 0)
-        for (int k = 0; k < kRing; ++k) tc::mbar_init(&landed[group][k], 1);
+    if (asks)
+        for (int k = 0; k < kRing; ++k) tc::mbar_init(&landed[unit][k], 1);
     if (threadIdx.x == 0) gave_up = 0;
     tc::fence_barrier_init();
     __syncthreads();
     pdl_wait();
     pdl_launch_dependents();
     auto request = [&](int64_t row, int k) {
-        uint64_t *bar = &landed[group][k];
+        uint64_t *bar = &landed[unit][k];
         uint8_t *to = mine + k * stage;
-        tc::mbar_expect_tx(bar, stage);
-        tc::bulk_load(to, static_cast<const T *>(a.h) + row * d, bytes, bar);
-        tc::bulk_load(to + bytes, static_cast<const T *>(a.dy) + row * d, bytes, bar);
-        if (more) tc::bulk_load(to + 2 * bytes, static_cast<const T *>(a.dh) + row * d, bytes, bar);
+        const uint32_t n = PART ? (uint32_t)min((int64_t)rows, a.T - row) * bytes : bytes;
+        tc::mbar_expect_tx(bar, n * (more ? 3 : 2));
+        tc::bulk_load(to, static_cast<const T *>(a.h) + row * d, n, bar);
+        tc::bulk_load(to + each, static_cast<const T *>(a.dy) + row * d, n, bar);
+        if (more) tc::bulk_load(to + 2 * each, static_cast<const T *>(a.dh) + row * d, n, bar);
     };
-    if (i == 0)
+    if (asks)
         for (int k = 0; k < kRing - 1; ++k)
             if (r + k * step < a.T) request(r + k * step, k);
     float2 w[W_SHARED ? 1 : VPT][P];   // this thread's weights, for all its rows
-    float *shared_w = reinterpret_cast<float *>(ring + (size_t)a.groups * kRing * stage);
+    float *shared_w = reinterpret_cast<float *>(ring + (size_t)a.groups * kRing * stage);   // (not PART)
     if constexpr (W_SHARED) {
         for (int c = threadIdx.x; c < d; c += blockDim.x) shared_w[c] = param<T>(a.weight, wf32, c);
         __syncthreads();
@@ -571,8 +577,9 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
         }
     int k = 0;                 // ring position
     uint32_t phase = 0;
-    for (; r < a.T; r += step) {
-        const float mean = nm[0], rstd = ns[0];
+    for (; r - sub < a.T; r += step) {   // (all lanes of a warp stay until its first row is past the end)
+        const bool here = !PART || r < a.T;
+        const float mean = here ? nm[0] : 0.f, rstd = here ? ns[0] : 0.f;
         nm[0] = nm[1];
         ns[0] = ns[1];
         if (r + 2 * step < a.T) {
@@ -580,14 +587,14 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
             ns[1] = a.rstd[r + 2 * step];
         }
         // a wait that runs out is reported; the pass goes on, so that its barriers end
-        if (!tc::mbar_try_wait(&landed[group][k], phase)) tc::wait_bar(&landed[group][k], phase, &gave_up, a.err);
-        const uint4 *h = reinterpret_cast<const uint4 *>(mine + k * stage) + i;
-        const uint4 *dy = reinterpret_cast<const uint4 *>(mine + k * stage + bytes) + i;
+        if (!tc::mbar_try_wait(&landed[unit][k], phase)) tc::wait_bar(&landed[unit][k], phase, &gave_up, a.err);
+        const uint4 *h = reinterpret_cast<const uint4 *>(mine + k * stage + sub * bytes) + i;
+        const uint4 *dy = reinterpret_cast<const uint4 *>(mine + k * stage + each + sub * bytes) + i;
         float2 z[VPT][P], g[VPT][P];
         float2 sg = both(0.f), sz = both(0.f);   // sums of g and of g (h - mean)
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const bool in = c0 + j * cj < d;
+            const bool in = here && c0 + j * cj < d;
             if constexpr (W_SHARED) {
 #pragma unroll
                 for (int q = 0; q < P; q += 2) {
@@ -610,17 +617,17 @@ __global__ void __launch_bounds__(VPT == 3 ? 256 : 512, VPT == 3 ? 2 : 1) norm_b
                 if (DB) db[j][q] = add2(db[j][q], y[q]);
             }
         }
-        const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), slot, turn, wi, W, 1 + group);
+        const float2 s = group_sum(make_float2(sg.x + sg.y, sz.x + sz.y), slot, turn, wi, W, 1 + group, PART ? G : 32);
         // every thread of the group is past the row before this one: its place is free
         // (one warp has met in shuffles only, which order no memory)
         if (W == 1) __syncwarp();
-        if (i == 0 && r + (kRing - 1) * step < a.T) request(r + (kRing - 1) * step, k == 0 ? kRing - 1 : k - 1);
+        if (asks && r + (kRing - 1) * step < a.T) request(r + (kRing - 1) * step, k == 0 ? kRing - 1 : k - 1);
         // dx = rstd g - rstd avg(g) - (h - mean) rstd^2 avg(g xhat)
         const float c1 = layer ? -rstd * (s.x * inv) : 0.f, c2 = -rstd * rstd * (rstd * s.y * inv);
-        const uint4 *dh = reinterpret_cast<const uint4 *>(mine + k * stage + 2 * bytes) + i;
+        const uint4 *dh = reinterpret_cast<const uint4 *>(mine + k * stage + 2 * each + sub * bytes) + i;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const bool in = c0 + j * cj < d;
+            const bool in = here && c0 + j * cj < d;
 #pragma unroll
             for (int q = 0; q < P; ++q) z[j][q] = fma2(z[j][q], both(c2), fma2(g[j][q], both(rstd), both(c1)));
             if (more) {
@@ -1026,8 +1033,8 @@ Spread spread(int d, int elems, bool aligned, bool three, bool wide_three) {
     s.lanes = 32 * s.W;
     return s;
 }
-// Forward: rows of up to 16 words a part of a warp each (four lanes at least); a warp
-// each, 262144 x 64 bf16 took 42 us where parts take 20.
+// Rows of up to 16 words (in the backward pass: whole ones) a part of a warp each, four
+// lanes at least; a warp each, 262144 x 64 bf16 took 42 us forward where parts take 17.
 void part_of_a_warp(Spread &s, int d, int elems) {
     const int words = (d + (s.shift ? elems - 1 : 0) + elems - 1) / elems;
     if (s.vpt != 1 || words > 16) return;
@@ -1091,6 +1098,7 @@ auto bwd_words(const Spread &s) -> void (*)(NormBwd) {
         if (s.vpt == 1) return s.W <= 8 ? norm_bwd_shift_kernel<T, 1, DB, 256> : norm_bwd_shift_kernel<T, 1, DB, 512>;
         return s.W <= 8 ? norm_bwd_shift_kernel<T, 2, DB, 256> : norm_bwd_shift_kernel<T, 2, DB, 512>;
     }
+    if (s.lanes < 32) return norm_bwd_ring_kernel<T, 1, DB, true>;
     if (s.vpt == 1) return norm_bwd_ring_kernel<T, 1, DB>;
     if (s.vpt == 2) return norm_bwd_ring_kernel<T, 2, DB>;
     if constexpr (!DB)
@@ -1189,14 +1197,15 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     const bool params = dweight || dbias;
     const int E = 16 / elem_size(c->dtype);
     const bool aligned = aligned16(h) && aligned16(weight) && aligned16(dy) && aligned16(dh) && aligned16(dx);
-    const Spread sp = spread(c->d, E, aligned, dbias == nullptr, true);
+    Spread sp = spread(c->d, E, aligned, dbias == nullptr, true);
+    if (!sp.shift) part_of_a_warp(sp, c->d, E);
     if (params && (!ws || ws_bytes < part_rows(*c) * 2 * (size_t)c->d * sizeof(float) ||
                    (reinterpret_cast<uintptr_t>(ws) & 255)))
         return MOE_ERR_WORKSPACE;
     uint32_t *err = device_error_word();
     if (!err) return MOE_ERR_CUDA;
     float *part = params ? static_cast<float *>(ws) : nullptr;
-    NormBwd a{h, weight, dy, dh, mean, rstd, dx, part, c->T, c->d, sp.W, sp.groups, c->w_dtype == MOE_F32,
+    NormBwd a{h, weight, dy, dh, mean, rstd, dx, part, c->T, c->d, sp.W, sp.lanes, sp.groups, c->w_dtype == MOE_F32,
               dbias != nullptr, err, 0, false};
     const size_t row = (size_t)c->d * elem_size(c->dtype);
     if (wide(sp)) wide_ring(a, row, wide_hold(sp.vpt, dbias != nullptr, elem_size(c->dtype)));
@@ -1207,7 +1216,7 @@ moe_status moe_norm_backward(const moe_norm_config *c, const void *h, const void
     cudaError_t e = cudaSuccess;
     // without the attribute a block has 48 KB, the kernel's own arrays (under 4 KB) included
     if (smem > 44 * 1024) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    const int threads = sp.groups * sp.W * 32;
+    const int threads = sp.groups * sp.lanes;
     const int blocks = blocks_for(sp, c->T, std::min(bwd_most(c->d), resident_blocks(kern, threads, smem)));
     if (e == cudaSuccess) e = launch_kernel(kern, blocks, threads, smem, s, a);
     if (e == cudaSuccess && params)

@@ -301,6 +301,18 @@ def test_backward(case):
     check_backward(*case)
 
 
+# rows that take part of a warp (see the forward pass's), many of them a block and a warp's last ones not all there
+@pytest.mark.gpu
+@pytest.mark.parametrize("kind,dtype,w_dtype,T,d,use_dh,use_bias", [
+    ("rms", "bf16", "bf16", 20003, 64, False, False), ("layer", "f16", "f32", 9001, 128, True, True),
+    ("layer", "f32", "f32", 40001, 16, True, False), ("rms", "bf16", "f32", 3, 40, False, True),
+    ("layer", "bf16", "bf16", 50021, 8, True, True), ("rms", "f32", "f32", 1, 4, True, True),
+    ("layer", "f16", "f16", 4097, 104, False, True), ("rms", "f32", "f32", 12001, 60, True, False),
+])
+def test_backward_of_short_rows(kind, dtype, w_dtype, T, d, use_dh, use_bias):
+    check_backward(kind, dtype, w_dtype, T, d, use_dh, use_bias)
+
+
 # wide rows, several a block, with one to four of them in flight and dh's among them or not
 @pytest.mark.gpu
 @pytest.mark.parametrize("kind,dtype,w_dtype,T,d,use_dh,use_bias", [
