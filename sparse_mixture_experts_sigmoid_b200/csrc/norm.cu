@@ -1001,29 +1001,34 @@ __global__ void __launch_bounds__(32 * kParamWarps) norm_param_kernel(const floa
 }
 
 // How a row is spread: VPT words per thread, W warps per row, `groups` rows
-// per block; vpt = 0 is the general kernel.  Of one, two and (`three`, whole words) three
-// words a thread, the one that leaves the fewest words of its warps idle, and
-// of those the one with the fewest warps: one warp needs no barrier.  Where more than
-// 16 warps would be needed, four words (eight), or three (`wide_three`: the backward
-// pass is bound by its warps' issue there; T = 4096, d = 10000 bf16 60 us with four).
+// per block; vpt = 0 is the general kernel.  Of one, two and (`three`, whole words)
+// three words a thread, the one that leaves the fewest words of its warps idle, and of
+// those the one with the fewest warps: one warp needs no barrier.  Whole words: two a
+// thread in place of five (backward: seven) or more warps of one word although half a
+// warp is idle (d = 3160 bf16, 6329 rows forward 23 -> 21.5 us, backward 35 -> 26; d =
+// 1200, 16666 rows forward 26 -> 21, but backward 27 -> 29; of shifted rows slower).
+// Where more than 16 warps would be needed, four words (eight), or three (backward: it
+// is bound by its warps' issue there; T = 4096, d = 10000 bf16 60 us with four).
 struct Spread {
     int vpt, W, groups;
     bool shift;
     int lanes;
 };
-Spread spread(int d, int elems, bool aligned, bool three, bool wide_three) {
+Spread spread(int d, int elems, bool aligned, bool three, bool backward) {
     const bool shift = d % elems != 0;
     const int words = (d + (shift ? elems - 1 : 0) + elems - 1) / elems;
     const int most = (shift ? 2 : (elems == 4 ? 8 : 4)) * 32 * kMaxWarps;
     if (!aligned || words > most) return Spread{0, kGenThreads / 32, 1, false, kGenThreads};
     Spread s{0, 0, 0, shift, 0};
     if (words > 64 * kMaxWarps) {
-        s.vpt = wide_three && words <= 96 * kMaxWarps ? 3 : words <= 128 * kMaxWarps ? 4 : 8;
+        s.vpt = backward && words <= 96 * kMaxWarps ? 3 : words <= 128 * kMaxWarps ? 4 : 8;
         s.W = (words + 32 * s.vpt - 1) / (32 * s.vpt);
     } else {
         for (int v = 1; v <= (three && !shift && words <= 96 ? 3 : 2); ++v) {
             const int w = (words + 32 * v - 1) / (32 * v);
-            if (w <= kMaxWarps && (!s.vpt || w * v <= s.W * s.vpt)) {
+            // (an odd number of warps of one word: half of them and a half idle)
+            const bool half = v == 2 && !shift && s.W >= (backward ? 7 : 5);
+            if (w <= kMaxWarps && (!s.vpt || w * v <= s.W * s.vpt + half)) {
                 s.vpt = v;
                 s.W = w;
             }
