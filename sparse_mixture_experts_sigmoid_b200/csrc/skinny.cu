@@ -52,12 +52,16 @@ constexpr int kThreads = 6 * 32;
 constexpr int kMaxStages = 6;
 constexpr int kSmem = 113 * 1024;          // two CTAs per SM
 
+// A CTA adds a multiple of four rows: of 64 or 128 in 3 or 6 parts, the last part fewer.
+constexpr int kSumRows = 144;              // 6 parts of 24 rows (GATED: 12 of each product)
+__host__ __device__ constexpr int part_rows(int rows, int S) { return (rows + 4 * S - 1) / (4 * S) * 4; }
+
 // Whether the sums are pushed, and the bytes that they take beside the ring.
 template <int NT>
 constexpr bool kPush = NT <= 64;
 template <int NT>
 constexpr int recv_bytes() {
-    return kPush<NT> ? kRows * NT * 4 : 0;
+    return kPush<NT> ? kSumRows * NT * 4 : 0;
 }
 template <int NT>
 constexpr int stages() {
@@ -212,7 +216,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (half) tile -= half_tiles;
     const int tt = tile / p.mt, m = tile - tt * p.mt;
     const int t0 = tt * NT, n0 = m * kOutRows, nt = min(NT, p.T - t0);
-    const int per = kOutRows / S, width = kRows / S;   // output rows, and sums' rows, of this CTA
+    const int per = part_rows(kOutRows, S), width = GATED ? 2 * per : per;   // output rows, and sums' rows, of a CTA
+    const int own = min(per, kOutRows - rank * per);                         // of this one
     const int k0 = (int)((int64_t)p.kb * rank / S), k1 = (int)((int64_t)p.kb * (rank + 1) / S), nk = k1 - k0;
 
     // the producer sets its barriers up and requests the first stages; meanwhile the
@@ -420,12 +425,12 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
     if (warp == kTmaWarp) pdl_wait();   // (its other lanes) before anything is written
 
-    // 1 / S of the tile's rows, over the S ranges in their order
+    // this CTA's part of the tile's rows, over the S ranges in their order
     if constexpr (WEIGHT) {
         // four columns of a row a step (T is a multiple of 8: in or out together)
         const int quads = nt / 4;
         void *out = half ? p.out1 : p.out;
-        for (int i = threadIdx.x; i < per * quads; i += kThreads) {
+        for (int i = threadIdx.x; i < own * quads; i += kThreads) {
             const int r = i / quads, t = 4 * (i - r * quads), n = n0 + rank * per + r;
             if (n >= p.N) continue;
             float u[4];
@@ -434,8 +439,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else if constexpr (kPush<NT>) {
         // one row of four tokens a step
-        for (int i = threadIdx.x; i < per * ((nt + 3) / 4); i += kThreads) {
-            const int t = i / per * 4, r = i - (i / per) * per, n = n0 + rank * per + r;
+        for (int i = threadIdx.x; i < own * ((nt + 3) / 4); i += kThreads) {
+            const int t = i / own * 4, r = i - (i / own) * own, n = n0 + rank * per + r;
             if (n >= p.N) continue;
             const float *at = recv + t * width + 4 * r;
             float u[4], v[4];
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
     } else {
         // four rows of one token a step
-        const int quads = per / 4, r0 = rank * per;
+        const int quads = own / 4, r0 = rank * per;
         for (int i = threadIdx.x; i < quads * nt; i += kThreads) {
             const int t = i / quads, r = r0 + 4 * (i - t * quads), n = n0 + r;
             if (n >= p.N) continue;   // N is a multiple of 8: four rows are in or out together
@@ -527,9 +532,9 @@ bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_
 // every SM, with four K blocks each at least (half as many, or half as many again: 5
 // to 20 % slower on the sizes that wants() lists).
 int ranges(int64_t tiles, int kb) {
-    int S = 1;
-    while (S < 8 && tiles * S * 2 <= 2 * num_sms() && kb >= 8 * S) S *= 2;
-    return S;
+    for (int S : {8, 6, 4, 3, 2})
+        if (tiles * S <= 2 * num_sms() && kb >= 4 * S) return S;
+    return 1;
 }
 
 template <Form F, int NT>

@@ -188,6 +188,17 @@ def test_step_matches_the_formulas(T, d, h, act, dtype):
     check("y", y, out["y"], tol["y"], half)
 
 
+# products with K in three and in six ranges (forward, du | dv, dx, weights' gradients): uneven parts of a tile's rows
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,d,h,act,dtype", [
+    (1, 1024, 5632, "silu", "bf16"), (57, 2048, 5632, "gelu_tanh", "f16"), (20, 1600, 2568, "silu", "bf16"),
+    (40, 5008, 1032, "silu", "f16"), (9, 10000, 792, "gelu_tanh", "bf16"), (100, 2504, 1608, "silu", "bf16"),
+    (8200, 328, 1000, "silu", "bf16"),
+])
+def test_step_of_uneven_parts(T, d, h, act, dtype):
+    test_step_matches_the_formulas(T, d, h, act, dtype)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 def test_large_pre_activations(dtype):

@@ -183,6 +183,16 @@ def test_product_matches_the_formula(M, N, K, dtype):
     check(y, *ops, dtype)
 
 
+# K in three and in six ranges: their parts of a tile's rows are not alike
+@pytest.mark.gpu
+@pytest.mark.parametrize("M,N,K", [(1, 10008, 1600), (31, 10000, 1552), (9, 5000, 3104), (64, 2504, 3136), (180, 1672, 3088)])
+def test_product_of_uneven_parts(M, N, K):
+    ops = operands(M, N, K)
+    y = B.gemm_fp8(*ops)
+    assert torch.equal(y, B.gemm_fp8(*ops)) and B.device_status() == 0
+    check(y, *ops, "bf16")
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("M", [5, 300])
 def test_scales_of_every_block_count(M):
