@@ -34,6 +34,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "ffn.cuh"
 #include "skinny.cuh"
@@ -528,12 +529,61 @@ bool make_rows(CUtensorMap *m, const void *base, int esize, int64_t rows, int64_
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// K ranges of a product of `tiles` tiles and kb K blocks: as many as fill two CTAs on
-// every SM, with four K blocks each at least (half as many, or half as many again: 5
-// to 20 % slower on the sizes that wants() lists).
+template <int NT, bool FP8>
+constexpr size_t smem_bytes() {
+    return 1024 + (size_t)stages<NT>() * (kWStage + NT * 128) + recv_bytes<NT>() + (FP8 ? 4 * 2 * NT * 4 : 0) + sizeof(Ctrl);
+}
+static_assert(smem_bytes<64, true>() <= kSmem && smem_bytes<128, false>() <= kSmem, "two CTAs per SM");
+
+// Clusters of S CTAs that the GPU holds at one time with one CTA per SM (what the
+// runtime answers for any kernel that allocates TMEM): fewer than SMs / S, as a cluster
+// stays within a group of SMs.  Asked once per device, alike for every form.
+int single_clusters(int S) {
+    constexpr int kDevices = 64;
+    static std::atomic<int> known[kDevices][9];
+    int dev = 0, blocks = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kDevices) return 0;
+    int n = known[dev][S].load(std::memory_order_relaxed);
+    if (n) return n;
+    auto kern = skinny_kernel<Form::kStore, 64>;
+    constexpr size_t smem = smem_bytes<64, false>();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(S * num_sms()));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&blocks, kern, kThreads, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();   // (a device that cannot say: no clusters)
+        return 0;
+    }
+    if (blocks > 1) n /= blocks;
+    known[dev][S].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+// And with two per SM, which every form allows: two layers of such clusters, or of the
+// large ones as many as of half their size.  (148 SMs: 148, 90, 66, 45 and 33 clusters of
+// 2, 3, 4, 6 and 8; up to 148, 92, 71, 45 and 33 tiles ran in one go.)
+int clusters(int S) {
+    const int n = 2 * single_clusters(S);
+    return S < 6 ? n : std::max(n, single_clusters(S / 2));
+}
+
+// K ranges of a product of `tiles` tiles and kb K blocks: as many as the GPU holds at
+// one time, with four K blocks each at least.  (Fewer leave SMs with one CTA beside
+// SMs with two; one cluster more than are held waits for a whole one to end: 4096 deep
+// in 8 bits, 71 tiles in four ranges 9.4 us, 72 tiles 14.9, in three 9.8.)
 int ranges(int64_t tiles, int kb) {
     for (int S : {8, 6, 4, 3, 2})
-        if (tiles * S <= 2 * num_sms() && kb >= 4 * S) return S;
+        if (kb >= 4 * S && tiles <= clusters(S)) return S;
     return 1;
 }
 
@@ -573,8 +623,7 @@ cudaError_t launch_nt(const Product &g, cudaStream_t s) {
     p.err = g.err;
     const int tiles = p.mt * (int)((g.T + NT - 1) / NT) * (WEIGHT && g.w1 ? 2 : 1);
     p.S = ranges(tiles, p.kb);
-    const size_t smem = 1024 + (size_t)stages<NT>() * (kWStage + NT * 128) + recv_bytes<NT>() +
-                        (FP8 ? 4 * 2 * NT * 4 : 0) + sizeof(Ctrl);
+    constexpr size_t smem = smem_bytes<NT, FP8>();
     auto kern = skinny_kernel<F, NT>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
@@ -634,7 +683,7 @@ cudaError_t launch_form(const Product &g, cudaStream_t s) {
 // The 256-row tiles need enough tiles for the pairs of SMs and a long enough K; this
 // kernel reads the weights again for every 128 (8 bits: 64) tokens.  In 8 bits, past
 // 32 tokens, it also adds each K block's product under its scales, 1 us a block
-// where the 256-row tiles take 0.45: it needs K in four ranges.
+// where the 256-row tiles take 0.45: it needs K in three ranges.
 bool wants(Form form, int64_t T, int N, int K) {
     const int64_t tiles = (T + 255) / 256 * ((N + 255) / 256);
     switch (form) {
@@ -642,7 +691,7 @@ bool wants(Form form, int64_t T, int N, int K) {
         case Form::kDGated: return T <= 32 || (K >= 512 && (T <= 128 || tiles <= 24));
         case Form::kDx: return tiles <= 16 && K >= 1024;
         case Form::kWeight: return tiles <= 8 && K >= 4096;
-        case Form::kFp8: return T <= 32 || ranges((T + 63) / 64 * ((N + kRows - 1) / kRows), (K + 127) / 128) >= 4;
+        case Form::kFp8: return T <= 32 || ranges((T + 63) / 64 * ((N + kRows - 1) / kRows), (K + 127) / 128) >= 3;
         default: return T <= 64 || (tiles <= 24 && K >= 1024);
     }
 }
