@@ -25,10 +25,10 @@
 // everything is local; reading the sums from the other CTAs instead, which 128
 // tokens' sums leave the only way, took 1 to 1.5 us more a product.
 //
-// Measured: T = 1, d = 4096, h = 14336 bf16 the forward block's two products 58 us
-// (6.1 TB/s), T = 57, d = 2048, h = 5632 25 (of which 10.6 are bytes: a product has
+// Measured: T = 1, d = 4096, h = 14336 bf16 the forward block's two products 57 us
+// (6.2 TB/s), T = 57, d = 2048, h = 5632 22 (of which 10.6 are bytes: a product has
 // 5 us of latency, to its first weights and from its last), 8 bits M = 9, 14336 x
-// 4096 14.6.
+// 4096 14.8.
 //
 // Every mbarrier wait is bounded as in the grouped kernels.
 #include <cuda_fp16.h>
@@ -664,22 +664,23 @@ cudaError_t launch_form(const Product &g, cudaStream_t s) {
 
 // Measured on both sides (us, this kernel / the 256-row tiles; d x h of the block,
 // or N x K of the 8-bit product):
-//   GATED  640 x 2048: T = 64 21/22, 256 23/23, 1024 29/23;  4096 x 14336: T = 64
-//          112/119, 256 159/126;  1024 x 512 (few tiles): T = 512 23/25, 768 28/25
-//   STORE  2048 x 5632: T = 64 26/45, 768 54/58, 2048 116/101;  4096 x 14336: T = 256
-//          97/126, 768 240/208;  512 x 8192: T = 2048 75/111, 4096 126/114;  K = 512:
-//          27/24 at T = 128
+//   GATED (with the down projection) 640 x 2048: T = 64 11/13, 256 15/15, 512 21/19;
+//          4096 x 14336: T = 64 68/79, 128 83/88, 256 122/94;  2048 x 5632: T = 64
+//          21/24, 128 30/29;  1024 x 512 (few tiles): T = 512 15/17, 768 18/17
+//   STORE (with the gated product) 2048 x 5632: T = 64 21/42, 768 54/59, 1024 64/67;
+//          4096 x 14336: T = 256 95/121, 512 161/159, 768 231/201;  512 x 8192: T =
+//          4096 97/111;  2048 x 512 (short K): T = 128 19/19, 512 28/33
 //   8 bits 14336 x 4096: T = 32 15/19, 64 21/20, 128 35/20;  2048 x 2048: T = 256 9/12,
-//          512 12/12;  640 x 8192: T = 768 19/34, 1024 33/33;  5632 x 2048: T = 64
-//          9/12, 128 12/12, 256 19/12
+//          512 12/12;  640 x 8192: T = 768 19/34, 1024 24/33;  5632 x 2048: T = 64
+//          9/12, 128 11/12, 256 19/12
 //   and of the whole backward pass with this kernel in the place of one product:
 //   DGATED (with one weight's gradient) 3672 x 384: T = 64 13/32, 2048 36/45, 4096
 //          62/61;  2048 x 5632: T = 128 23/28, 256 31/32, 512 48/38;  640 x 2048: T =
 //          256 18/19, 512 22/21;  208 x 2944 (short K): T = 32 13/15, 64 16/15
-//   DX     640 x 2048: T = 9 23/41, 1024 43/47, 2048 61/54;  4096 x 14336: T = 64
-//          154/234, 512 364/347;  3672 x 384 (short K): T = 64 51/46
-//   WEIGHT 80 x 168: T = 1024 30/25, 8192 40/69;  512 x 512: T = 2048 44/38, 8192
-//          65/84;  640 x 2048 (more tiles): T = 8192 299/189
+//   DX     640 x 2048: T = 9 16/34, 1024 40/45, 2048 51/47;  4096 x 14336: T = 64
+//          134/226, 256 218/228, 512 369/349;  3672 x 384 (short K): T = 64 21/17
+//   WEIGHT 80 x 168: T = 1024 27/23, 8192 38/67;  512 x 512: T = 2048 43/37, 4096
+//          46/50;  640 x 2048 (more tiles): T = 8192 257/152
 // The 256-row tiles need enough tiles for the pairs of SMs and a long enough K; this
 // kernel reads the weights again for every 128 (8 bits: 64) tokens.  In 8 bits, past
 // 32 tokens, it also adds each K block's product under its scales, 1 us a block
@@ -692,7 +693,7 @@ bool wants(Form form, int64_t T, int N, int K) {
         case Form::kDx: return tiles <= 16 && K >= 1024;
         case Form::kWeight: return tiles <= 8 && K >= 4096;
         case Form::kFp8: return T <= 32 || ranges((T + 63) / 64 * ((N + kRows - 1) / kRows), (K + 127) / 128) >= 3;
-        default: return T <= 64 || (tiles <= 24 && K >= 1024);
+        default: return T <= 64 || (tiles <= 32 && K >= 512);
     }
 }
 
