@@ -454,7 +454,8 @@ typedef struct {
  *     MOE_ERR_INVALID_ARG); y [T, d] out;
  *   mean, rstd [T] fp32 out, each optional: what moe_norm_backward takes.
  * h may be x or residual, and y may be x or residual, but not both the same
- * tensor (h == y: MOE_ERR_INVALID_ARG).  Statistics are fp32, the variance summed about the mean. */
+ * tensor (h == y: MOE_ERR_INVALID_ARG).  Statistics are fp32, the variance
+ * summed about the mean. */
 moe_status moe_norm_forward(const moe_norm_config *cfg, const void *x, const void *residual,
                             const void *weight, const void *bias, void *h, void *y, float *mean,
                             float *rstd, void *stream);
@@ -508,8 +509,9 @@ moe_status moe_ffn_workspace_size(const moe_ffn_config *cfg, int32_t train, size
 
 /* x [T, d]; w_gate, w_up [h, d]; w_down [d, h]; y [T, d] out; all 16-byte
  * aligned (else MOE_ERR_INVALID_ARG).  ws: at least moe_ffn_workspace_size
- * bytes, 256-byte aligned.  y overlaps none of the others.  moe_ffn_forward_train gives the same y and keeps
- * in ws what moe_ffn_backward needs (u, v and a). */
+ * bytes, 256-byte aligned.  y overlaps none of the others.
+ * moe_ffn_forward_train gives the same y and keeps in ws what moe_ffn_backward
+ * needs (u, v and a). */
 moe_status moe_ffn_forward(const moe_ffn_config *cfg, const void *x, const void *w_gate,
                            const void *w_up, const void *w_down, void *y, void *ws, size_t ws_bytes,
                            void *stream);
@@ -522,9 +524,8 @@ moe_status moe_ffn_forward_train(const moe_ffn_config *cfg, const void *x, const
  * repeated, with another dy).  dx [T, d], dw_gate, dw_up [h, d], dw_down [d, h]
  * are overwritten; each may be NULL (not computed).  x is read only for dw_gate
  * and dw_up, the weights only for dx and for them.  No output overlaps an input
- * or another output.  Every sum has a fixed
- * order: repeated calls give identical bits.  T = 0 writes zero weight
- * gradients. */
+ * or another output.  Every sum has a fixed order: repeated calls give identical
+ * bits.  T = 0 writes zero weight gradients. */
 moe_status moe_ffn_backward(const moe_ffn_config *cfg, const void *x, const void *w_gate,
                             const void *w_up, const void *w_down, const void *dy, void *ws,
                             size_t ws_bytes, void *dx, void *dw_gate, void *dw_up, void *dw_down,
